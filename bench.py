@@ -116,12 +116,12 @@ def _code_tokens(text):
 
 
 def kernel_source_hash():
-    """Hash of the HIP sources' code (comments and layout ignored), to tie
-    recorded counters to the code they measured."""
+    """Hash of the delta rule's and the conv's HIP sources' code (comments and
+    layout ignored), to tie recorded counters to the code they measured."""
     import glob
     import hashlib
     h = hashlib.sha256()
-    for f in sorted(glob.glob(os.path.join(ROOT, "chunked_gated_delta_04_amd", "csrc", "*"))):
+    for f in sorted(glob.glob(os.path.join(ROOT, "chunked_gated_delta_04_amd", "csrc", "gdn_*"))):
         h.update(os.path.basename(f).encode())
         with open(f, encoding="utf-8", errors="replace") as fh:
             h.update(_code_tokens(fh.read()).encode())

@@ -1,0 +1,68 @@
+// Host-side declarations of the linear attention with a decay for each head.
+#pragma once
+
+#include "gdn_internal.h"
+
+namespace gdn {
+
+// Token rows of one operand: row t of head h starts at p + t * stride + h * D.
+// Value head hv reads head hv / G.
+struct LinRows {
+  const uint16_t* p;
+  int64_t stride;
+  int G;
+};
+
+// How a pack is cut into segments that run side by side: segment i of
+// sequence n covers tokens [i S, (i + 1) S) of it and has the slot
+// cu[n] / S + n + i, so that a slot's sequence follows from cu_seqlens alone
+// and T / S + N slots hold every pack. S is a multiple of the 64-token chunk.
+struct LinCut {
+  const int32_t* cu;
+  int N, T, HV;
+  int S;      // tokens per segment
+  int slots;  // T / S + N
+};
+
+// One pass over the chunks of every segment, front to back or back to front:
+//   out_t = sum over the pass's earlier tokens and t itself of
+//           decay^|t - j| (a_t . b_j) c_j, plus a_t times the carried state X,
+// where X [contracted with a][column of c] is carried with the decay and
+// gathers b_j c_j^T. The four uses differ in the operands, the direction, and
+// in whether X is the stored state [V][K] read along its rows or its columns.
+struct LinPass {
+  LinRows a, b, c;
+  void* out;           // bf16 (or fp32 where `wide`) rows [T, HV, D]
+  const float* start;  // [slots, HV, D, D] states that the segments start from, or null:
+  StateRef io;         // where the sequences' states come from and end
+};
+
+enum class LinKind {
+  kOut,  // o: a = q, b = k, c = v, front to back
+  kDq,   // dq: a = dO, b = v, c = k, front to back, the state's transpose
+  kDv,   // dv: a = k, b = q, c = dO, back to front
+  kDk,   // dk: a = v, b = dO, c = q, back to front, the state's transpose
+};
+
+hipError_t launch_lin_pass(LinKind kind, bool wide, int D, const LinCut& cut, const float* log_decay,
+                           float scale, const LinPass& pass, hipStream_t stream);
+
+// What each segment adds to the state that it carries on (front to back: all
+// but a sequence's last; back to front: all but its first), from a zero start.
+hipError_t launch_lin_gather(bool back, int D, const LinCut& cut, const float* log_decay, float scale,
+                             const LinRows& b, const LinRows& c, float* states, hipStream_t stream);
+
+// In place: what the segments add -> the states that the segments start from,
+// with each sequence's start state from io (io.h0 may be null).
+hipError_t launch_lin_join(bool back, bool gathered, int D, const LinCut& cut, const float* log_decay,
+                           const StateRef& io, float* states, hipStream_t stream);
+
+// out[t][h] = sum over the key head's G value heads of wide[t][h G + i], to bf16.
+hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wide, uint16_t* out,
+                           hipStream_t stream);
+
+hipError_t launch_lin_step(int D, int N, int HV, float scale, const LinRows& q, const LinRows& k,
+                           const LinRows& v, const float* log_decay, float* pool, int slots,
+                           const int32_t* idx, uint16_t* o, hipStream_t stream);
+
+}  // namespace gdn

@@ -37,6 +37,8 @@ EXPORTED = (
     "gdn_conv_update",
     "gdn_chunk_fwd_timed", "gdn_chunk_bwd_timed", "gdn_stage_name",
     "gdn_chunk_fwd_paged_noalloc", "gdn_chunk_fwd_paged_noalloc_max_bytes",
+    "gdn_linear_saved_size", "gdn_linear_fwd_workspace_size", "gdn_linear_bwd_workspace_size",
+    "gdn_linear_fwd", "gdn_linear_fwd_paged", "gdn_linear_bwd", "gdn_linear_step",
 )
 GDN_MAX_STAGES = 8
 
@@ -55,6 +57,16 @@ class GdnConvProblem(ctypes.Structure):
         ("N", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32),
         ("W", ctypes.c_int32), ("activation", ctypes.c_int32),
         ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+    ]
+
+
+class GdnLinearProblem(ctypes.Structure):
+    _fields_ = [
+        ("N", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("HV", ctypes.c_int32), ("K", ctypes.c_int32), ("V", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
     ]
 
 
@@ -114,6 +126,20 @@ _lib.gdn_stage_name.argtypes = [ctypes.c_int, ctypes.c_int]
 _lib.gdn_recurrent_step.restype = ctypes.c_int
 _lib.gdn_recurrent_step.argtypes = ([_i32] * 5 + [ctypes.c_float] + [_vp] * 8 + [_i32] +
                                     [_vp] * 4)
+
+_LP = ctypes.POINTER(GdnLinearProblem)
+for _n in ("gdn_linear_saved_size", "gdn_linear_fwd_workspace_size",
+           "gdn_linear_bwd_workspace_size"):
+    getattr(_lib, _n).restype = _sz
+    getattr(_lib, _n).argtypes = [_LP]
+_lib.gdn_linear_fwd.restype = ctypes.c_int
+_lib.gdn_linear_fwd.argtypes = [_LP] + [_vp] * 9 + [_sz, _vp]
+_lib.gdn_linear_fwd_paged.restype = ctypes.c_int
+_lib.gdn_linear_fwd_paged.argtypes = [_LP] + [_vp] * 5 + [_i32] + [_vp] * 6 + [_sz, _vp]
+_lib.gdn_linear_bwd.restype = ctypes.c_int
+_lib.gdn_linear_bwd.argtypes = [_LP] + [_vp] * 12 + [_sz, _vp]
+_lib.gdn_linear_step.restype = ctypes.c_int
+_lib.gdn_linear_step.argtypes = [_LP] + [_vp] * 5 + [_i32] + [_vp] * 4
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -565,3 +591,229 @@ def conv_update(x, weight, bias, state_pool, indices, indices_host=None, activat
     gdn_conv_update(N, C, W, activation, x, weight, bias, state_pool, state_pool.shape[0],
                     indices, indices_host, y, stream)
     return y
+
+
+# ---------------------------------------------------------------- device tensors of a call
+# The operators below check every tensor's device, type and shape before its
+# pointer is handed on, run on the tensors' device whichever is current, and
+# allocate on the stream that they run on.
+def _dev(t, shape, dtype, name, dev):
+    """Device pointer of a contiguous tensor of this shape on this device (None -> NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, dev):
+    """Device pointer and token stride (0: dense) of a [tokens, heads, columns] tensor whose heads
+    are dense rows: a tensor of its own or a slice of a wider buffer's rows."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if n == 0:
+        return None, 0
+    if (sd != 1 and d > 1) or (sh != d and h > 1) or (sn < h * d and n > 1):
+        raise ValueError(f"{name} must have dense heads and tokens apart, got strides {t.stride()}")
+    return t.data_ptr(), sn if n > 1 and sn != h * d else 0
+
+
+def _on_device(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a tensor on the GPU")
+    return t.device
+
+
+class _Run:
+    """The device and stream of a call: `stream` (a torch stream or a raw handle), or the device's
+    current one. Inside it, both are current."""
+
+    def __init__(self, dev, stream):
+        self.dev, self.more = dev, None
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        self.handle = (stream or torch.cuda.current_stream(dev)).cuda_stream
+        if stream is not None:
+            self.more = torch.cuda.stream(stream)
+        elif dev.index != torch.cuda.current_device():
+            self.more = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.more is not None:
+            self.more.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.more is not None:
+            self.more.__exit__(*exc)
+
+
+# ---------------------------------------------------------------- linear attention
+_bf16, _f32 = torch.bfloat16, torch.float32
+
+
+def make_linear_problem(N, T, H, HV, D, cu_seqlens=None, cu_seqlens_host=None, scale=0.0,
+                        q_stride=0, k_stride=0, v_stride=0):
+    """Build the gdn_linear_problem descriptor (K = V = D). cu_seqlens: int32 device tensor [N+1];
+    cu_seqlens_host: optional int32 CPU tensor [N+1] (both kept alive by the caller)."""
+    p = GdnLinearProblem()
+    p.N, p.T, p.H, p.HV, p.K, p.V, p.scale = N, T, H, HV, D, D, scale
+    p.q_stride, p.k_stride, p.v_stride = q_stride, k_stride, v_stride
+    if cu_seqlens is not None:
+        p.cu_seqlens = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens",
+                            _on_device(cu_seqlens, "cu_seqlens"))
+    if cu_seqlens_host is not None:
+        if cu_seqlens_host.numel() != N + 1:
+            raise ValueError(f"cu_seqlens_host must hold {N + 1} boundaries")
+        p.cu_seqlens_host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
+    return p
+
+
+def gdn_linear_saved_size(problem):
+    return int(_lib.gdn_linear_saved_size(ctypes.byref(problem)))
+
+
+def gdn_linear_fwd_workspace_size(problem):
+    return int(_lib.gdn_linear_fwd_workspace_size(ctypes.byref(problem)))
+
+
+def gdn_linear_bwd_workspace_size(problem):
+    return int(_lib.gdn_linear_bwd_workspace_size(ctypes.byref(problem)))
+
+
+def _linear_shapes(q, k, v):
+    T, H, D = q.shape
+    if k.shape != q.shape or v.dim() != 3 or v.shape[0] != T or v.shape[2] != D:
+        raise ValueError(f"q, k, v must be [T, H, D], [T, H, D], [T, HV, D], got {tuple(q.shape)}, "
+                         f"{tuple(k.shape)}, {tuple(v.shape)}")
+    return T, H, v.shape[1], D
+
+
+def _linear_call(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, scale):
+    """(device, problem, pointers of q, k, v, log_decay) of one call."""
+    dev = _on_device(q, "q")
+    T, H, HV, D = _linear_shapes(q, k, v)
+    (qp, qs), (kp, ks), (vp, vs) = (_rows(q, _bf16, "q", dev), _rows(k, _bf16, "k", dev),
+                                    _rows(v, _bf16, "v", dev))
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else T
+    if cu_seqlens is not None and cu_seqlens.device != dev:
+        raise ValueError(f"cu_seqlens must be on {dev}, got {cu_seqlens.device}")
+    p = make_linear_problem(N, T, H, HV, D, cu_seqlens, cu_seqlens_host, scale, qs, ks, vs)
+    return dev, p, (qp, kp, vp, _dev(log_decay, (HV,), _f32, "log_decay", dev))
+
+
+def _bytes(t):
+    return t.numel() * t.element_size() if t is not None else 0
+
+
+def _buffer(t, name, dev):
+    if t is None:
+        return None
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {dev}")
+    return t.data_ptr()
+
+
+def _alloc_bytes(n, dev):
+    return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+
+
+def linear_fwd(q, k, v, log_decay, cu_seqlens, h0=None, scale=0.0, cu_seqlens_host=None,
+               save_for_backward=False, output_final_state=True, stream=None):
+    """Linear attention with a decay for each head over a pack (gdn_linear_fwd).
+
+    q, k [T, H, D], v [T, HV, D] bf16, D = 64 or 128, dense or slices of a wider buffer's rows;
+    log_decay [HV] fp32; cu_seqlens [N+1] int32; h0 [N, HV, D, D] fp32 or None.
+    Returns (o [T, HV, D] bf16, hT [N, HV, D, D] fp32 or None, saved or None)."""
+    dev, p, ptrs = _linear_call(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, scale)
+    N, T, HV, D = p.N, p.T, p.HV, p.K
+    h0p = _dev(h0, (N, HV, D, D), _f32, "h0", dev)
+    with _Run(dev, stream) as s:
+        o = torch.empty(T, HV, D, dtype=_bf16, device=dev)
+        hT = torch.empty(N, HV, D, D, dtype=_f32, device=dev) if output_final_state else None
+        saved = _alloc_bytes(gdn_linear_saved_size(p), dev) if save_for_backward else None
+        ws = None if save_for_backward else _alloc_bytes(gdn_linear_fwd_workspace_size(p), dev)
+        st = _lib.gdn_linear_fwd(ctypes.byref(p), *ptrs, h0p, o.data_ptr(),
+                                 _buffer(hT, "hT", dev), _buffer(saved, "saved", dev),
+                                 _buffer(ws, "workspace", dev), _bytes(ws), s)
+    _check(st, "gdn_linear_fwd")
+    return o, hT, saved
+
+
+def linear_fwd_paged(q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indices,
+                     has_initial_state=None, indices_host=None, scale=0.0, cu_seqlens_host=None,
+                     save_for_backward=False, stream=None):
+    """linear_fwd whose sequences' states are blocks of state_pool [slots, HV, D, D] fp32, updated
+    in place (gdn_linear_fwd_paged). Returns (o, saved or None)."""
+    dev, p, ptrs = _linear_call(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, scale)
+    N, T, HV, D = p.N, p.T, p.HV, p.K
+    slots = state_pool.shape[0]
+    if indices_host is not None and indices_host.numel() != N:
+        raise ValueError(f"indices_host must hold {N} indices")
+    more = (_dev(state_pool, (slots, HV, D, D), _f32, "state_pool", dev), slots,
+            _dev(ssm_state_indices, (N,), torch.int32, "ssm_state_indices", dev),
+            _dev(has_initial_state, (N,), torch.int32, "has_initial_state", dev),
+            _host_ptr(indices_host, "indices_host"))
+    with _Run(dev, stream) as s:
+        o = torch.empty(T, HV, D, dtype=_bf16, device=dev)
+        saved = _alloc_bytes(gdn_linear_saved_size(p), dev) if save_for_backward else None
+        ws = None if save_for_backward else _alloc_bytes(gdn_linear_fwd_workspace_size(p), dev)
+        st = _lib.gdn_linear_fwd_paged(ctypes.byref(p), *ptrs, *more, o.data_ptr(),
+                                       _buffer(saved, "saved", dev),
+                                       _buffer(ws, "workspace", dev), _bytes(ws), s)
+    _check(st, "gdn_linear_fwd_paged")
+    return o, saved
+
+
+def linear_bwd(q, k, v, log_decay, cu_seqlens, saved, dO, dhT=None, scale=0.0,
+               cu_seqlens_host=None, want_dh0=True, stream=None):
+    """Gradients of linear_fwd (gdn_linear_bwd): dict dq, dk [T, H, D], dv [T, HV, D] bf16 and
+    dh0 [N, HV, D, D] fp32 (None unless want_dh0)."""
+    dev, p, ptrs = _linear_call(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, scale)
+    N, T, H, HV, D = p.N, p.T, p.H, p.HV, p.K
+    if _bytes(saved) < gdn_linear_saved_size(p):
+        raise ValueError(f"saved holds {_bytes(saved)} bytes, the problem needs "
+                         f"{gdn_linear_saved_size(p)} (gdn_linear_saved_size)")
+    more = (_buffer(saved, "saved", dev), _dev(dO, (T, HV, D), _bf16, "dO", dev),
+            _dev(dhT, (N, HV, D, D), _f32, "dhT", dev))
+    with _Run(dev, stream) as s:
+        dq, dk = (torch.empty(T, H, D, dtype=_bf16, device=dev) for _ in range(2))
+        dv = torch.empty(T, HV, D, dtype=_bf16, device=dev)
+        dh0 = torch.empty(N, HV, D, D, dtype=_f32, device=dev) if want_dh0 else None
+        ws = _alloc_bytes(gdn_linear_bwd_workspace_size(p), dev)
+        st = _lib.gdn_linear_bwd(ctypes.byref(p), *ptrs, *more, dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), _buffer(dh0, "dh0", dev),
+                                 _buffer(ws, "workspace", dev), _bytes(ws), s)
+    _check(st, "gdn_linear_bwd")
+    return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
+
+
+def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=None, scale=0.0,
+                stream=None):
+    """One token per row (gdn_linear_step): q, k [N, H, D], v [N, HV, D]; state_pool
+    [slots, HV, D, D] fp32 is updated in place. Returns o [N, HV, D] bf16."""
+    dev, p, ptrs = _linear_call(q, k, v, log_decay, None, None, scale)
+    N, HV, D = p.N, p.HV, p.K
+    slots = state_pool.shape[0]
+    if indices_host is not None and indices_host.numel() != N:
+        raise ValueError(f"indices_host must hold {N} indices")
+    more = (_dev(state_pool, (slots, HV, D, D), _f32, "state_pool", dev), slots,
+            _dev(ssm_state_indices, (N,), torch.int32, "ssm_state_indices", dev),
+            _host_ptr(indices_host, "indices_host"))
+    with _Run(dev, stream) as s:
+        o = torch.empty(N, HV, D, dtype=_bf16, device=dev)
+        st = _lib.gdn_linear_step(ctypes.byref(p), *ptrs, *more, o.data_ptr(), s)
+    _check(st, "gdn_linear_step")
+    return o

@@ -408,6 +408,102 @@ int gdn_conv_update(int32_t N, int32_t C, int32_t W, int32_t activation, const u
                     int32_t slots, const int32_t* indices, const int32_t* indices_host,
                     uint16_t* y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence of the delta
+ * rule above without its correction, with one fixed decay lam = e^log_decay
+ * per value head,
+ *   S_t = lam S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,
+ * on the same packs, head groups and states: value head hv reads key head
+ * hv / (HV / H), states are fp32 [V, K], sequences are packed by cu_seqlens
+ * and the decode pool is [slots, HV, V, K]. q and k are used as given (no
+ * norm); the decays are constants of the layer and have no gradient.
+ *
+ *   N, T, H, HV   as in gdn_problem
+ *   K, V          head dims, K = V = 64 or 128
+ *   scale         multiplier of o; <= 0 selects K^-1/2
+ *   cu_seqlens, cu_seqlens_host   as in gdn_problem
+ *   q_stride, k_stride, v_stride  elements from one token of q, k, v to the
+ *                 next (its heads are dense), for rows inside a wider buffer
+ *                 such as the short convolution's output: a multiple of 8, at
+ *                 least H * K (HV * V) and below 2^23, or 0 for dense rows.
+ * log_decay is fp32 [HV] on the device. -inf is decay zero (every value from
+ * -128 down counts as that); values above 0 are growth.
+ * A NaN or infinity in a token's q, k or v can spoil the outputs of the 64
+ * tokens of its chunk (counted from the sequence's start), earlier ones too,
+ * besides the later tokens of its sequence; no other sequence is touched. */
+typedef struct {
+  int32_t N, T, H, HV, K, V;
+  float scale;
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+  int64_t q_stride, k_stride, v_stride;
+} gdn_linear_problem;
+
+/* Bytes of the `saved` buffer that gdn_linear_fwd fills for gdn_linear_bwd
+ * and workspace bytes of the calls (0 on a bad problem). They depend on
+ * (N, T, H, HV, K) only. The forward needs no workspace for some problems
+ * (size 0, workspace may be NULL). Workspaces are 16-byte aligned device
+ * memory, used only during the call, and need not be zeroed. */
+size_t gdn_linear_saved_size(const gdn_linear_problem* p);
+size_t gdn_linear_fwd_workspace_size(const gdn_linear_problem* p);
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem* p);
+
+/* Chunked forward.
+ *   q, k      bf16 [T, H, K], v bf16 [T, HV, V], rows as the strides say
+ *   log_decay fp32 [HV]
+ *   h0        fp32 [N, HV, V, K] initial states, or NULL for zero states
+ *   o         bf16 [T, HV, V] (written)
+ *   hT        fp32 [N, HV, V, K] final states, or NULL to skip
+ *   saved     gdn_linear_saved_size(p) bytes kept for gdn_linear_bwd, or NULL
+ *             when no backward follows (fp32 states that parts of the
+ *             sequences start from, in an order internal to this library).
+ * A sequence of length 0 gets hT = h0 (or 0); T = 0 is valid. Rows of o at or
+ * past cu_seqlens[N] are left as they were.
+ * Errors: GDN_ERR_NULL (p, or q, k, v, o when T > 0, log_decay or cu_seqlens
+ * when N > 0), GDN_ERR_SHAPE (extents or strides), GDN_ERR_UNSUPPORTED,
+ * GDN_ERR_SEQLENS, GDN_ERR_ALIGN, GDN_ERR_WORKSPACE, GDN_ERR_HIP. */
+int gdn_linear_fwd(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,
+                   const uint16_t* v, const float* log_decay, const float* h0, uint16_t* o,
+                   float* hT, void* saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Chunked forward whose start and end states live in a state pool, updated in
+ * place, with the index and has_initial_state rules of gdn_chunk_fwd_paged.
+ * The results equal gdn_linear_fwd with h0 / hT gathered from and scattered to
+ * the pool, bit for bit. Errors: those of gdn_linear_fwd, and of
+ * gdn_chunk_fwd_paged for the pool and its indices. */
+int gdn_linear_fwd_paged(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,
+                         const uint16_t* v, const float* log_decay, float* state_pool,
+                         int32_t slots, const int32_t* ssm_state_indices,
+                         const int32_t* has_initial_state, const int32_t* indices_host,
+                         uint16_t* o, void* saved, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Backward of gdn_linear_fwd (same p, q, k, v, log_decay).
+ *   saved     as written by the forward for the same problem and inputs
+ *   dO        bf16 [T, HV, V] cotangent of o
+ *   dhT       fp32 [N, HV, V, K] cotangent of hT, or NULL for zero
+ *   dq, dk    bf16 [T, H, K]; dv bf16 [T, HV, V] (dense)
+ *   dh0       fp32 [N, HV, V, K] cotangent of h0, or NULL to skip
+ * The value heads of one key head are summed into dq, dk in fp32 in a fixed
+ * order; no atomics. Errors: as gdn_linear_fwd, GDN_ERR_NULL for saved, dO,
+ * dq, dk, dv. */
+int gdn_linear_bwd(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,
+                   const uint16_t* v, const float* log_decay, const void* saved,
+                   const uint16_t* dO, const float* dhT, uint16_t* dq, uint16_t* dk, uint16_t* dv,
+                   float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per row, in place on a state pool: T = N rows, cu_seqlens not
+ * read. q, k [N, H, K], v [N, HV, V] with the problem's strides; o bf16
+ * [N, HV, V]; state_pool, slots, ssm_state_indices and indices_host as in
+ * gdn_recurrent_step (an index <= 0 or >= slots: a zero output row, no block
+ * read or written). N = 0 is valid and enqueues nothing.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_INDEX,
+ * GDN_ERR_ALIGN, GDN_ERR_HIP. */
+int gdn_linear_step(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,
+                    const uint16_t* v, const float* log_decay, float* state_pool, int32_t slots,
+                    const int32_t* ssm_state_indices, const int32_t* indices_host, uint16_t* o,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif
