@@ -1,0 +1,111 @@
+// Host- and device-side declarations of the operators around the recurrences:
+// rotary positions and the root-mean-square norm. Their tensors are bf16, fp16
+// or fp32, computed in fp32.
+#pragma once
+
+#include <hip/hip_fp16.h>
+
+#include "gdn_common.h"
+
+namespace gdn {
+
+// element types, numbered as gdn_dtype
+enum class Elem : int { kBf16 = 0, kFp16 = 1, kFp32 = 2 };
+
+struct Bf16 {
+  uint16_t u;
+};
+struct Fp16 {
+  uint16_t u;
+};
+
+__device__ __forceinline__ float to_f32(Bf16 x) { return bf2f(x.u); }
+__device__ __forceinline__ float to_f32(Fp16 x) { return (float)__builtin_bit_cast(_Float16, x.u); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ Bf16 from_f32<Bf16>(float x) { return {f2bf(x)}; }
+template <>
+__device__ __forceinline__ Fp16 from_f32<Fp16>(float x) { return {__builtin_bit_cast(uint16_t, (_Float16)x)}; }
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+
+// N consecutive elements as fp32: 16 bytes at once where N elements are 16
+// bytes (p 16-byte aligned), else element by element.
+template <typename T, int N>
+__device__ __forceinline__ void load_n(const T* p, float* x) {
+  if constexpr (N * sizeof(T) == 16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_f32(p[i]);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* p, const float* x) {
+  if constexpr (N * sizeof(T) == 16) {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = from_f32<T>(x[i]);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = from_f32<T>(x[i]);
+  }
+}
+
+// One set of rows [T, heads, D] of the rotary operator: in and out may be the same.
+struct RotaryRows {
+  const void* in;
+  void* out;
+  int64_t in_stride, out_stride;  // elements between tokens
+  int heads;
+};
+
+struct RotaryArgs {
+  int T, D, R;
+  float mscale, sign;  // sign -1: the transposed turn
+  const float* inv_freq;
+  const int32_t* positions;  // [T], or null: by the sequences
+  int N;
+  const int32_t* cu;
+  const int32_t* offsets;  // [N] or null
+  RotaryRows q, k;
+};
+
+// wide: 16 bytes at a time (the caller has checked extents and alignment)
+hipError_t launch_rotary(Elem type, bool interleaved, bool wide, const RotaryArgs& a, hipStream_t s);
+
+struct NormArgs {
+  int rows, D;
+  float eps, unit;  // the weight's offset
+  int group;        // columns a scale: 0 none (no e4m3 output), D a row, or 128
+  const void *x, *residual, *weight;
+  int64_t x_stride, residual_stride;
+  void *residual_out, *y;
+  uint8_t* y8;
+  float *scales, *rstd;
+};
+hipError_t launch_rmsnorm_fwd(Elem type, bool wide, const NormArgs& a, hipStream_t s);
+
+struct NormGradArgs {
+  int rows, D;
+  float unit;
+  const void *s, *weight, *dy, *ds;
+  const float* rstd;
+  int64_t s_stride;
+  void* dx;
+  float *dweight, *partial;  // partial: [norm_partials, D], or null without dweight
+};
+// row groups that each sum one partial of dweight
+int norm_partials(int rows, int D);
+hipError_t launch_rmsnorm_bwd(Elem type, bool wide, const NormGradArgs& a, hipStream_t s);
+
+constexpr int kNormMaxD = 16384;
+
+}  // namespace gdn

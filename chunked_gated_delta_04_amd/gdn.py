@@ -39,6 +39,8 @@ EXPORTED = (
     "gdn_chunk_fwd_paged_noalloc", "gdn_chunk_fwd_paged_noalloc_max_bytes",
     "gdn_linear_saved_size", "gdn_linear_fwd_workspace_size", "gdn_linear_bwd_workspace_size",
     "gdn_linear_fwd", "gdn_linear_fwd_paged", "gdn_linear_bwd", "gdn_linear_step",
+    "gdn_rotary", "gdn_rotary_bwd", "gdn_rotary_inv_freq",
+    "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "gdn_rmsnorm_bwd_workspace_size",
 )
 GDN_MAX_STAGES = 8
 
@@ -67,6 +69,20 @@ class GdnLinearProblem(ctypes.Structure):
         ("scale", ctypes.c_float),
         ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
         ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+    ]
+
+
+class GdnRotaryProblem(ctypes.Structure):
+    _fields_ = [(_n, ctypes.c_int32) for _n in ("T", "HQ", "HK", "D", "R", "interleaved", "dtype")] + [
+        ("mscale", ctypes.c_float), ("positions", ctypes.c_void_p), ("N", ctypes.c_int32),
+        ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+    ] + [(_n, ctypes.c_int64) for _n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+
+
+class GdnRmsnormProblem(ctypes.Structure):
+    _fields_ = [(_n, ctypes.c_int32) for _n in ("rows", "D", "dtype", "unit_offset", "group")] + [
+        ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
     ]
 
 
@@ -140,6 +156,21 @@ _lib.gdn_linear_bwd.restype = ctypes.c_int
 _lib.gdn_linear_bwd.argtypes = [_LP] + [_vp] * 12 + [_sz, _vp]
 _lib.gdn_linear_step.restype = ctypes.c_int
 _lib.gdn_linear_step.argtypes = [_LP] + [_vp] * 5 + [_i32] + [_vp] * 4
+
+_RP = ctypes.POINTER(GdnRotaryProblem)
+for _n in ("gdn_rotary", "gdn_rotary_bwd"):
+    getattr(_lib, _n).restype = ctypes.c_int
+    getattr(_lib, _n).argtypes = [_RP] + [_vp] * 6
+_lib.gdn_rotary_inv_freq.restype = ctypes.c_int
+_lib.gdn_rotary_inv_freq.argtypes = [_i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double,
+                                     _vp, ctypes.POINTER(ctypes.c_float)]
+_NP = ctypes.POINTER(GdnRmsnormProblem)
+_lib.gdn_rmsnorm_fwd.restype = ctypes.c_int
+_lib.gdn_rmsnorm_fwd.argtypes = [_NP] + [_vp] * 9
+_lib.gdn_rmsnorm_bwd.restype = ctypes.c_int
+_lib.gdn_rmsnorm_bwd.argtypes = [_NP] + [_vp] * 8 + [_sz, _vp]
+_lib.gdn_rmsnorm_bwd_workspace_size.restype = _sz
+_lib.gdn_rmsnorm_bwd_workspace_size.argtypes = [_NP]
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -817,3 +848,176 @@ def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=
         st = _lib.gdn_linear_step(ctypes.byref(p), *ptrs, *more, o.data_ptr(), s)
     _check(st, "gdn_linear_step")
     return o
+
+
+# ---------------------------------------------------------------- rotary positions and the norm
+_ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROPE = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _elem(t, name):
+    if t.dtype not in _ELEM:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return _ELEM[t.dtype]
+
+
+def rotary_inv_freq(R, base=10000.0, scaling=None, factor=1.0, original=4096, device=None):
+    """(inv_freq [R / 2] fp32, attention factor) of R turning columns (gdn_rotary_inv_freq).
+    scaling: None, "linear", "ntk" or "yarn", for contexts `factor` times as long as `original`."""
+    f, m = torch.empty(max(R // 2, 1), dtype=torch.float32), ctypes.c_float(1.0)
+    _check(_lib.gdn_rotary_inv_freq(R, base, _ROPE[scaling], factor, original, f.data_ptr(),
+                                    ctypes.byref(m)), "gdn_rotary_inv_freq")
+    return f.to(device) if device is not None else f, m.value
+
+
+def _rotary(call, q, k, inv_freq, positions, cu_seqlens, offsets, cu_seqlens_host, interleaved,
+            mscale, q_out, k_out, stream, back):
+    dev = _on_device(q, "q")
+    T, HQ, D = q.shape
+    p = GdnRotaryProblem()
+    p.T, p.HQ, p.D, p.R = T, HQ, D, 2 * inv_freq.numel()
+    p.dtype, p.interleaved, p.mscale = _elem(q, "q"), bool(interleaved), mscale
+    if k is not None and (k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k must be [{T}, HK, {D}], got {tuple(k.shape)}")
+    p.HK = k.shape[1] if k is not None else 0
+    if positions is not None:
+        p.positions = _dev(positions, (T,), torch.int32, "positions", dev)
+    elif cu_seqlens is None:
+        raise ValueError("positions or cu_seqlens are needed")
+    else:
+        N = p.N = cu_seqlens.numel() - 1
+        p.cu_seqlens = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", dev)
+        p.offsets = _dev(offsets, (N,), torch.int32, "offsets", dev)
+        if cu_seqlens_host is not None:
+            if cu_seqlens_host.numel() != N + 1:
+                raise ValueError(f"cu_seqlens_host must hold {N + 1} boundaries")
+            p.cu_seqlens_host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
+    freq = _dev(inv_freq, (inv_freq.numel(),), _f32, "inv_freq", dev)
+    qp, qs = _rows(q, q.dtype, "q", dev)
+    kp, ks = _rows(k, q.dtype, "k", dev) if k is not None else (None, 0)
+    with _Run(dev, stream) as s:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+            raise ValueError("q_out and k_out must have the shapes of q and k")
+        qo, qos = _rows(q_out, q.dtype, "q_out", dev)
+        ko, kos = _rows(k_out, q.dtype, "k_out", dev) if k is not None else (None, 0)
+        if back:
+            p.q_out_stride, p.k_out_stride, p.q_stride, p.k_stride = qs, ks, qos, kos
+        else:
+            p.q_stride, p.k_stride, p.q_out_stride, p.k_out_stride = qs, ks, qos, kos
+        st = call(ctypes.byref(p), freq, qp, kp, qo, ko, s)
+    return st, q_out, k_out
+
+
+def rotary(q, k, inv_freq, positions=None, cu_seqlens=None, offsets=None, cu_seqlens_host=None,
+           interleaved=False, mscale=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions (gdn_rotary) of q [T, HQ, D] and k [T, HK, D] (or None), bf16, fp16 or fp32,
+    dense or slices of a wider buffer's rows; inv_freq [R / 2] fp32. Positions [T] int32, or each
+    token's place in its sequence by cu_seqlens [N+1] plus offsets [N]. q_out, k_out: where the
+    results go (q and k themselves: in place), by default new tensors. Returns (q_out, k_out)."""
+    st, qo, ko = _rotary(_lib.gdn_rotary, q, k, inv_freq, positions, cu_seqlens, offsets,
+                         cu_seqlens_host, interleaved, mscale, q_out, k_out, stream, False)
+    _check(st, "gdn_rotary")
+    return qo, ko
+
+
+def rotary_bwd(dq_out, dk_out, inv_freq, positions=None, cu_seqlens=None, offsets=None,
+               cu_seqlens_host=None, interleaved=False, mscale=1.0, dq=None, dk=None, stream=None):
+    """Gradients of rotary (gdn_rotary_bwd): (dq, dk) from those of its outputs."""
+    st, qo, ko = _rotary(_lib.gdn_rotary_bwd, dq_out, dk_out, inv_freq, positions, cu_seqlens,
+                         offsets, cu_seqlens_host, interleaved, mscale, dq, dk, stream, True)
+    _check(st, "gdn_rotary_bwd")
+    return qo, ko
+
+
+def _norm_rows(t, dtype, shape, name, dev):
+    """Pointer and row stride (0: dense) of a [rows, D] tensor whose rows are dense."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, D = shape
+    if rows == 0:
+        return None, 0
+    sr, sd = t.stride()
+    if (sd != 1 and D > 1) or (sr < D and rows > 1):
+        raise ValueError(f"{name} must have dense rows apart, got strides {t.stride()}")
+    return t.data_ptr(), sr if rows > 1 and sr != D else 0
+
+
+def _norm_problem(x, weight, unit_offset, eps, group, dev):
+    rows, D = x.shape
+    p = GdnRmsnormProblem()
+    p.rows, p.D, p.dtype, p.eps = rows, D, _elem(x, "x"), eps
+    p.unit_offset, p.group = bool(unit_offset), group
+    return p, _dev(weight, (D,), x.dtype, "weight", dev)
+
+
+def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-6, unit_offset=False, quant=None,
+                want_y=None, want_rstd=False, residual_out=None, stream=None):
+    """Root-mean-square norm (gdn_rmsnorm_fwd) of x [rows, D] (+ residual), bf16, fp16 or fp32, rows
+    dense or slices of wider ones. quant: None, "row" or 128 for an e4m3 output with a scale for each
+    row or each 128 columns. want_y: the output in x's type (by default where there is no e4m3 one).
+    Returns a dict of residual_out (with a residual), y, y8, scales, rstd (those asked for)."""
+    dev = _on_device(x, "x")
+    if quant not in (None, "row", 128):
+        raise ValueError(f'quant must be None, "row" or 128, got {quant!r}')
+    rows, D = x.shape
+    p, wp = _norm_problem(x, weight, unit_offset, eps, 128 if quant == 128 else 0, dev)
+    xp, p.x_stride = _norm_rows(x, x.dtype, (rows, D), "x", dev)
+    rp, p.residual_stride = _norm_rows(residual, x.dtype, (rows, D), "residual", dev)
+    want_y = quant is None if want_y is None else want_y
+    if not want_y and quant is None:
+        raise ValueError("nothing to compute: want_y is False and quant is None")
+    out = {}
+    with _Run(dev, stream) as s:
+        if residual is not None:
+            out["residual_out"] = torch.empty(rows, D, dtype=x.dtype, device=dev) if residual_out is None else residual_out
+        if want_y:
+            out["y"] = torch.empty(rows, D, dtype=x.dtype, device=dev)
+        if quant is not None:
+            out["y8"] = torch.empty(rows, D, dtype=torch.float8_e4m3fn, device=dev)
+            shape = (rows,) if quant == "row" else (rows, (D + 127) // 128)
+            out["scales"] = torch.empty(shape, dtype=_f32, device=dev)
+        if want_rstd:
+            out["rstd"] = torch.empty(rows, dtype=_f32, device=dev)
+        get = lambda n: out[n].data_ptr() if n in out else None  # noqa: E731
+        so = _dev(out.get("residual_out"), (rows, D), x.dtype, "residual_out", dev)
+        st = _lib.gdn_rmsnorm_fwd(ctypes.byref(p), xp, rp, wp, so, get("y"), get("y8"),
+                                  get("scales"), get("rstd"), s)
+    _check(st, "gdn_rmsnorm_fwd")
+    return out
+
+
+def gdn_rmsnorm_bwd_workspace_size(problem):
+    return int(_lib.gdn_rmsnorm_bwd_workspace_size(ctypes.byref(problem)))
+
+
+def rmsnorm_bwd(dy, s, weight, rstd, dresidual_out=None, unit_offset=False, want_dweight=None,
+                stream=None):
+    """Gradients of rmsnorm_fwd (gdn_rmsnorm_bwd): s is its residual_out (x without a residual).
+    Returns dict dx [rows, D] (of x and of residual) and dweight [D] fp32 (None without a weight)."""
+    dev = _on_device(dy, "dy")
+    rows, D = dy.shape
+    p, wp = _norm_problem(dy, weight, unit_offset, 0.0, 0, dev)
+    sp, p.x_stride = _norm_rows(s, dy.dtype, (rows, D), "s", dev)
+    dyp = _dev(dy, (rows, D), dy.dtype, "dy", dev)
+    dsp = _dev(dresidual_out, (rows, D), dy.dtype, "dresidual_out", dev)
+    rp = _dev(rstd, (rows,), _f32, "rstd", dev)
+    want_dweight = weight is not None if want_dweight is None else want_dweight
+    with _Run(dev, stream) as st_:
+        dx = torch.empty(rows, D, dtype=dy.dtype, device=dev)
+        dw = torch.empty(D, dtype=_f32, device=dev) if want_dweight else None
+        ws = _alloc_bytes(gdn_rmsnorm_bwd_workspace_size(p), dev) if want_dweight else None
+        st = _lib.gdn_rmsnorm_bwd(ctypes.byref(p), sp, wp, rp, dyp, dsp, dx.data_ptr(),
+                                  _buffer(dw, "dweight", dev), _buffer(ws, "workspace", dev),
+                                  _bytes(ws), st_)
+    _check(st, "gdn_rmsnorm_bwd")
+    return dict(dx=dx, dweight=dw)

@@ -504,6 +504,126 @@ int gdn_linear_step(const gdn_linear_problem* p, const uint16_t* q, const uint16
                     const int32_t* ssm_state_indices, const int32_t* indices_host, uint16_t* o,
                     void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the recurrences work on bf16, fp16 or fp32 tensors
+ * (void pointers of `dtype`'s elements) and compute in fp32. */
+typedef enum { GDN_BF16 = 0, GDN_FP16 = 1, GDN_FP32 = 2 } gdn_dtype;
+
+/* Rotary positions, in front of an attention over q and k: the first R
+ * columns of every head row turn in pairs by the angle position * inv_freq[j],
+ *   (a, b) -> mscale (a cos - b sin, a sin + b cos),
+ * where pair j is columns (j, j + R/2), or (2 j, 2 j + 1) when interleaved.
+ * The other D - R columns are copied. Angles are formed in fp64.
+ *   T           tokens (T >= 0)
+ *   HQ, HK      heads of q and k (HK = 0: no k)
+ *   D, R        columns of a head (at most 1024) and how many of them turn
+ *               (even, 2 <= R <= D)
+ *   interleaved 0 or 1
+ *   dtype       gdn_dtype of q, k and the outputs
+ *   mscale      attention factor on cosine and sine; <= 0 selects 1
+ *   positions   device int32 [T], or NULL: a token's position is its place in
+ *               its sequence, by cu_seqlens (device int32 [N + 1], as in
+ *               gdn_problem), plus offsets[n] (device int32 [N], the tokens
+ *               that sequence n had before; NULL: 0). Rows that no sequence
+ *               holds are then left as they were.
+ *   N, cu_seqlens_host  as in gdn_problem (not read with positions)
+ *   strides     elements from one token to the next (its heads are dense), 0
+ *               for dense rows; below 2^31
+ * In place is allowed (q_out = q with the same stride, likewise k); otherwise
+ * an output overlaps no input. Rows of 16-byte aligned pieces (pointers,
+ * strides, D and the turning half) are read 16 bytes at a time, any others
+ * element by element. */
+typedef struct {
+  int32_t T, HQ, HK, D, R, interleaved, dtype;
+  float mscale;
+  const int32_t* positions;
+  int32_t N;
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+  const int32_t* offsets;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+} gdn_rotary_problem;
+
+/* q [T, HQ, D], k [T, HK, D] -> q_out, k_out. inv_freq: device fp32 [R / 2].
+ * Errors: GDN_ERR_NULL (p; q, q_out, inv_freq, with HK > 0 k and k_out, and
+ * cu_seqlens without positions, when T > 0), GDN_ERR_SHAPE,
+ * GDN_ERR_UNSUPPORTED (D, R, interleaved, dtype), GDN_ERR_SEQLENS,
+ * GDN_ERR_ALIGN (a pointer not aligned to its elements), GDN_ERR_HIP. */
+int gdn_rotary(const gdn_rotary_problem* p, const float* inv_freq, const void* q, const void* k,
+               void* q_out, void* k_out, void* stream);
+/* The gradient: cotangents of q_out, k_out (with the out strides) turned back
+ * into those of q, k (with the in strides). Errors as gdn_rotary. */
+int gdn_rotary_bwd(const gdn_rotary_problem* p, const float* inv_freq, const void* dq_out,
+                   const void* dk_out, void* dq, void* dk, void* stream);
+
+/* Inverse frequencies of R turning columns into inv_freq (host, R / 2 floats)
+ * and the attention factor into *mscale (host), for contexts `factor` times
+ * as long as `original`:
+ *   GDN_ROPE_PLAIN   base^(-2j/R)
+ *   GDN_ROPE_LINEAR  those divided by factor (positions interpolated)
+ *   GDN_ROPE_NTK     those of the base * factor^(R / (R - 2)): the first stays,
+ *                    the last is divided by factor (R > 2)
+ *   GDN_ROPE_YARN    per pair between the first two, by a ramp over the turns
+ *                    it makes in `original` positions: 32 and more stay, 1 and
+ *                    fewer are divided; *mscale = 1 + 0.1 ln factor
+ * *mscale is 1 otherwise. Host only. Errors: GDN_ERR_NULL, GDN_ERR_SHAPE (R,
+ * base <= 1, factor < 1, original < 1 with YARN), GDN_ERR_UNSUPPORTED. */
+typedef enum {
+  GDN_ROPE_PLAIN = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_YARN = 3
+} gdn_rope_scaling;
+int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, double original,
+                        float* inv_freq, float* mscale);
+
+/* Root-mean-square norm of s = x + residual (s = x without one) over each
+ * row's D columns:
+ *   y = s / sqrt(mean(s^2) + eps) * (weight + unit),
+ * s rounded to dtype: it is what the residual stream holds and what the
+ * backward reads. The norm and its outputs come from that s in fp32.
+ *   rows, D     rows >= 0, 1 <= D <= 16384
+ *   dtype       gdn_dtype of x, residual, weight, residual_out, y and of the
+ *               gradients in and out
+ *   unit_offset 1: the weight is stored around zero (unit = 1); 0: unit = 0
+ *   group       columns that share a scale of y8: 0 (the whole row) or 128
+ *   x_stride, residual_stride  elements from one row of x (and of s in the
+ *               backward), of residual to the next, 0 for dense rows; the
+ *               other tensors are dense
+ * Forward:
+ *   residual, weight  NULL for none (weight 1, whatever unit_offset says)
+ *   residual_out  s; required with a residual, else ignored. It may be x or
+ *               residual itself (dense).
+ *   y           NULL to skip; it may be x (dense)
+ *   y8, scales  NULL to skip, or e4m3 (OCP, finite) [rows, D] and fp32
+ *               [rows] or, with group 128, [rows, ceil(D / 128)]: scale =
+ *               max(largest |y| of its columns, 2^-100) / 448, y8 = y / scale
+ *               rounded to nearest even, from y in fp32
+ *   rstd        fp32 [rows] for the backward, or NULL
+ * Errors: GDN_ERR_NULL (p; x, residual_out with a residual, y and y8 both,
+ * scales with y8, when rows > 0), GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED (D,
+ * dtype, group, unit_offset), GDN_ERR_ALIGN (a pointer not aligned to its
+ * elements), GDN_ERR_HIP. */
+typedef struct {
+  int32_t rows, D, dtype, unit_offset, group;
+  float eps;
+  int64_t x_stride, residual_stride;
+} gdn_rmsnorm_problem;
+int gdn_rmsnorm_fwd(const gdn_rmsnorm_problem* p, const void* x, const void* residual,
+                    const void* weight, void* residual_out, void* y, uint8_t* y8, float* scales,
+                    float* rstd, void* stream);
+
+/* Backward, with n = s rstd and dn = dy (weight + unit):
+ *   dx = rstd (dn - n mean(dn n)) + ds   (the gradient of x and of residual)
+ *   dweight = sum over the rows of dy n  (fp32 [D], or NULL to skip)
+ *   s, rstd     as the forward's residual_out (x without a residual) and rstd
+ *   ds          cotangent of residual_out, or NULL for zero
+ *   dx          may be dy or ds itself
+ * dweight is summed in a fixed order through the workspace
+ * (gdn_rmsnorm_bwd_workspace_size bytes, 16-byte aligned; not needed without
+ * dweight). Errors as the forward, GDN_ERR_WORKSPACE. */
+size_t gdn_rmsnorm_bwd_workspace_size(const gdn_rmsnorm_problem* p);
+int gdn_rmsnorm_bwd(const gdn_rmsnorm_problem* p, const void* s, const void* weight,
+                    const float* rstd, const void* dy, const void* ds, void* dx, float* dweight,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,169 @@
+"""The root-mean-square norm on the GPU against the fp64 oracle.
+
+Tolerances: an output in its type is off by half a step of it (bf16 2^-8, fp16 2^-11, fp32 2^-24, relative) and
+before that by fp32 arithmetic: the sum of squares of D terms by threads of at most 32 terms and a tree, and four more operations:
+2^-24 (32 + 16 + 8) < 2^-18. y8 is off by half a step of e4m3 (2^-4 relative, 2^-10 at least) of the scaled value. The
+backward's sums of signed terms take the same factor on their sums of absolute values; dweight adds the rows one
+after another (at most rows additions)."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer as Y
+from tests.gpu_helpers import f64
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from chunked_gated_delta_04_amd import gdn
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+LEAST = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -25, torch.float32: 0.0}
+F32 = 2.0 ** -18
+
+
+def within(got, ref, size=None, extra=1.0):
+    bound = HALF[got.dtype] * np.abs(ref) + F32 * extra * (np.abs(ref) if size is None else size) + LEAST[got.dtype]
+    err = np.abs(f64(got) - ref)
+    assert (err <= bound * (1 + 2.0 ** -6)).all(), (err.max(), (err / (bound + 1e-300)).max())
+
+
+def make(rows, D, dtype, seed, wide=0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(rows, D + wide, generator=gen) * 3).to(dtype).cuda()[:, :D]
+
+
+SIZES = [(1, 1), (3, 2), (5, 64), (17, 128), (9, 100), (33, 129), (2, 512), (7, 511), (4, 768), (3, 1024), (6, 2048), (2, 2047),
+         (5, 4096), (3, 4104), (2, 8192), (2, 8191), (2, 16384), (1, 12345), (1500, 136), (2300, 72)]
+
+
+@pytest.mark.parametrize("rows, D", SIZES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_forward_and_backward_match_the_oracle(rows, D, dtype):
+    print(rows, D, dtype, file=sys.stderr, flush=True)
+    for residual, weighted, unit, wide in ((True, True, False, 0), (False, True, True, 8), (True, False, False, 1)):
+        x, r = make(rows, D, dtype, 1, wide), make(rows, D, dtype, 2, wide) if residual else None
+        w = make(1, D, dtype, 3)[0].contiguous() if weighted else None
+        out = gdn.rmsnorm_fwd(x, w, residual=r, eps=1e-5, unit_offset=unit, want_rstd=True)
+        s = x
+        if residual:
+            s = out["residual_out"]
+            assert torch.equal(s, (x.float() + r.float()).to(dtype))
+        u = 1.0 if unit else 0.0
+        wf = f64(w) if weighted else None
+        y, rstd = Y.rmsnorm(f64(s), wf, 1e-5, u)
+        within(out["y"], y)
+        within(out["rstd"], rstd)
+        dy, ds = make(rows, D, dtype, 4).contiguous(), make(rows, D, dtype, 5).contiguous() if residual else None
+        g = gdn.rmsnorm_bwd(dy, s, w, out["rstd"], dresidual_out=ds, unit_offset=unit, want_dweight=True)
+        dsf = f64(ds) if residual else None
+        dx, dw = Y.rmsnorm_backward(f64(s), f64(dy), wf, 1e-5, u, dsf)
+        dn = np.abs(f64(dy) * (wf + u if weighted else 1.0))
+        n = np.abs(f64(s)) * rstd[:, None]
+        size = rstd[:, None] * (dn + n * (dn * n).mean(1, keepdims=True)) + (np.abs(dsf) if residual else 0.0)
+        within(g["dx"], dx, size)
+        within(g["dweight"], dw, (np.abs(f64(dy)) * n).sum(0), extra=1 + rows * 2.0 ** -6)
+        again = gdn.rmsnorm_bwd(dy, s, w, out["rstd"], dresidual_out=ds, unit_offset=unit, want_dweight=True)
+        assert torch.equal(again["dx"], g["dx"]) and torch.equal(again["dweight"], g["dweight"])
+        assert gdn.rmsnorm_bwd(dy, s, w, out["rstd"], ds, unit, want_dweight=False)["dweight"] is None
+
+
+@pytest.mark.parametrize("rows, D", SIZES)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_e4m3_matches_the_oracle(rows, D, dtype):
+    print(rows, D, dtype, file=sys.stderr, flush=True)
+    x, r, w = make(rows, D, dtype, 1, 8), make(rows, D, dtype, 2), make(1, D, dtype, 3)[0].contiguous()
+    if rows > 2:
+        x[1], r[1] = 0, 0  # a row of zeros
+    for quant, group in (("row", 0), (128, 128)):
+        for want_y in (False, True):
+            out = gdn.rmsnorm_fwd(x, w, residual=r, quant=quant, want_y=want_y)
+            y, _ = Y.rmsnorm(f64(out["residual_out"]), f64(w))
+            sc = Y.scales(y, group)
+            assert out["scales"].shape == sc.shape and ("y" in out) == want_y
+            within(out["scales"], sc)
+            per = np.repeat(sc, group, 1)[:, :D] if group else sc[:, None]
+            v = y / per
+            err = np.abs(f64(out["y8"].float()) - v)
+            assert (err <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10) * (1 + 2.0 ** -12)).all()
+            assert np.abs(f64(out["y8"].float())).max() <= 448
+            if want_y:
+                within(out["y"], y)
+
+
+def test_wide_and_narrow_paths_agree_closely():
+    x = make(50, 2048, torch.bfloat16, 7)
+    odd = torch.empty(50 * 2048 + 1, dtype=torch.bfloat16, device="cuda")[1:].view(50, 2048)
+    odd.copy_(x)
+    a, b = (gdn.rmsnorm_fwd(t, quant=128) for t in (x, odd))
+    assert torch.allclose(a["scales"], b["scales"], rtol=1e-6, atol=0)
+    assert (a["y8"].float() != b["y8"].float()).float().mean() < 1e-3
+
+
+def test_in_place_and_nothing_leaks_between_rows():
+    x, r = make(40, 520, torch.bfloat16, 1), make(40, 520, torch.bfloat16, 2)
+    want = gdn.rmsnorm_fwd(x, residual=r)
+    for target in ("x", "r"):
+        a, b = x.clone(), r.clone()
+        got = gdn.rmsnorm_fwd(a, residual=b, residual_out=a if target == "x" else b)
+        assert torch.equal(got["y"], want["y"]) and torch.equal(got["residual_out"], want["residual_out"])
+    x2 = x.clone()
+    x2[5, 3], x2[7] = float("nan"), float("inf")
+    got = gdn.rmsnorm_fwd(x2, residual=r, quant="row", want_y=True)
+    keep = [i for i in range(40) if i not in (5, 7)]
+    assert torch.equal(got["y"][keep], want["y"][keep]) and bool(got["y"][5].isnan().all())
+    assert bool(got["scales"][keep].isfinite().all()) and bool(got["y8"][5].float().isnan().all())
+
+
+def test_empty_rows():
+    x, w = torch.empty(0, 64, dtype=torch.float16, device="cuda"), torch.ones(64, dtype=torch.float16, device="cuda")
+    out = gdn.rmsnorm_fwd(x, w, residual=x, quant=128, want_rstd=True)
+    assert out["y8"].shape == (0, 64) and out["scales"].shape == (0, 1)
+    g = gdn.rmsnorm_bwd(x, x, w, torch.empty(0, device="cuda"))
+    assert g["dx"].shape == (0, 64) and torch.equal(g["dweight"], torch.zeros(64, device="cuda"))
+
+
+def test_another_stream_and_a_captured_graph():
+    x, r, w = make(300, 1000, torch.bfloat16, 1), make(300, 1000, torch.bfloat16, 2), make(1, 1000, torch.bfloat16, 3)[0].contiguous()
+
+    def run(stream=None):
+        o = gdn.rmsnorm_fwd(x, w, residual=r, quant=128, want_y=True, want_rstd=True, stream=stream)
+        g = gdn.rmsnorm_bwd(o["y"], o["residual_out"], w, o["rstd"], dresidual_out=o["y"], stream=stream)
+        return [o["y"], o["y8"].view(torch.uint8), o["scales"], o["rstd"], g["dx"], g["dweight"]]
+
+    want = run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = run(s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    x, w = torch.zeros(6, 64, device="cuda"), torch.zeros(64, device="cuda")
+    rstd = torch.zeros(6, device="cuda")
+    bad = [
+        (ValueError, lambda: gdn.rmsnorm_fwd(x, w[:63])), (TypeError, lambda: gdn.rmsnorm_fwd(x, w.half())),
+        (ValueError, lambda: gdn.rmsnorm_fwd(x, w.cpu())), (ValueError, lambda: gdn.rmsnorm_fwd(x, w, residual=x[:3])),
+        (TypeError, lambda: gdn.rmsnorm_fwd(x, w, residual=x.half())), (ValueError, lambda: gdn.rmsnorm_fwd(x, w, quant=64)),
+        (ValueError, lambda: gdn.rmsnorm_fwd(x, w, want_y=False)), (ValueError, lambda: gdn.rmsnorm_fwd(x.t(), None)),
+        (ValueError, lambda: gdn.rmsnorm_fwd(x[:1].expand(6, 64), w)), (TypeError, lambda: gdn.rmsnorm_fwd(x.double())),
+        (ValueError, lambda: gdn.rmsnorm_fwd(x, w, residual=x, residual_out=x[:, :32])),
+        (gdn.GdnError, lambda: gdn.rmsnorm_fwd(torch.zeros(1, 16385, device="cuda"))),
+        (ValueError, lambda: gdn.rmsnorm_bwd(x, x, w, rstd[:5])), (ValueError, lambda: gdn.rmsnorm_bwd(x, x[:5], w, rstd)),
+        (TypeError, lambda: gdn.rmsnorm_bwd(x, x.half(), w, rstd)), (ValueError, lambda: gdn.rmsnorm_bwd(x, x, w, rstd, dresidual_out=x[:2])),
+    ]
+    for error, call in bad:
+        with pytest.raises(error):
+            call()
