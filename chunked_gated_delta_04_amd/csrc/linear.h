@@ -32,34 +32,33 @@ struct LinCut {
 // in whether X is the stored state [V][K] read along its rows or its columns.
 struct LinPass {
   LinRows a, b, c;
-  void* out;           // bf16 (or fp32 where `wide`) rows [T, HV, D]
-  const float* start;  // [slots, HV, D, D] states that the segments start from, or null:
-  StateRef io;         // where the sequences' states come from and end
+  void* out;           // rows [T, HV, D]
+  const float* start;  // [slots, HV, D, D] states that the segments start from, or null: from io
+  StateRef io;         // where the sequences' states come from and a whole one's ends
 };
 
-enum class LinKind {
-  kOut,  // o: a = q, b = k, c = v, front to back
-  kDq,   // dq: a = dO, b = v, c = k, front to back, the state's transpose
-  kDv,   // dv: a = k, b = q, c = dO, back to front
-  kDk,   // dk: a = v, b = dO, c = q, back to front, the state's transpose
-};
-
-hipError_t launch_lin_pass(LinKind kind, bool wide, int D, const LinCut& cut, const float* log_decay,
-                           float scale, const LinPass& pass, hipStream_t stream);
-
-// What each segment adds to the state that it carries on (front to back: all
-// but a sequence's last; back to front: all but its first), from a zero start.
-hipError_t launch_lin_gather(bool back, int D, const LinCut& cut, const float* log_decay, float scale,
-                             const LinRows& b, const LinRows& c, float* states, hipStream_t stream);
-
+// o: a = q, b = k, c = v, front to back.
+hipError_t launch_lin_out(int D, const LinCut& cut, const float* log_decay, float scale, const LinPass& pass,
+                          hipStream_t stream);
+// dq: a = dO, b = v, c = k, front to back, the state's transpose; back to front
+// dv: a = k, b = q, c = dO and dk: a = v, b = dO, c = q, the state's transpose.
+// wide: dq's and dk's rows are fp32 rows of every value head.
+hipError_t launch_lin_grad(int D, bool wide, const LinCut& cut, const float* log_decay, float scale,
+                           const LinPass& dq, const LinPass& dv, const LinPass& dk, hipStream_t stream);
+// What each segment of a sequence of several adds to the state that it carries
+// on, from a zero start: front to back from b = k and c = v, back to front from
+// b = q and c = dO. ends: the last one's too (back to front, the first one's).
+hipError_t launch_lin_gather(int D, bool back, const LinCut& cut, const float* log_decay, float scale,
+                             const LinRows& b, const LinRows& c, bool ends, float* states, hipStream_t stream);
 // In place: what the segments add -> the states that the segments start from,
-// with each sequence's start state from io (io.h0 may be null).
-hipError_t launch_lin_join(bool back, bool gathered, int D, const LinCut& cut, const float* log_decay,
-                           const StateRef& io, float* states, hipStream_t stream);
+// each sequence's start state from io; and, to io, the end state of a sequence of
+// several segments (a whole one's is its pass's). io's may be null.
+hipError_t launch_lin_join(int D, bool back, const LinCut& cut, const float* log_decay, const StateRef& io,
+                           float* states, hipStream_t stream);
 
-// out[t][h] = sum over the key head's G value heads of wide[t][h G + i], to bf16.
-hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wide, uint16_t* out,
-                           hipStream_t stream);
+// dq[t][h] = sum over the key head's G value heads of wq[t][h G + i], to bf16; dk likewise.
+hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wq, const float* wk, uint16_t* dq,
+                           uint16_t* dk, hipStream_t stream);
 
 hipError_t launch_lin_step(int D, int N, int HV, float scale, const LinRows& q, const LinRows& k,
                            const LinRows& v, const float* log_decay, float* pool, int slots,

@@ -26,10 +26,36 @@ constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // workgroups of 256 threads i
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-// Tokens per segment, from the extents alone (the boundaries stay on the device).
+// Tokens per segment, from the extents alone, so that a `saved` buffer's layout
+// is its problem's (the boundaries stay on the device). Cutting a sequence costs
+// two launches, a second reading of k and v and 16 D^2 bytes a segment and head,
+// and makes items that run side by side.
+//   Few chains (sequences x value heads): 512 to 1023 items, two to a CU; at
+// least 256 tokens each. 1 x 8192 tokens, 8 heads of 128: 47 us with 256
+// tokens, 55 with 512, 352 uncut; 2 x 8192, 32 heads: 204 us with 1024, 268 with
+// 256, 439 uncut.
+//   Chains enough to fill the chip, and short: no cut in sequences of the mean
+// length. 16 x 1024, 8 heads: 56 us uncut, 78 with 256; 16 x 2048, 32 heads: 258
+// uncut, 406 with 1024; but 4 x 4096, 32 heads: 237 uncut, 204 with 1024. The
+// two times compared are fits of such measurements: a step of 64 tokens takes
+// an item 3.6 us (2.0 with D = 64) while every item has a CU (half a CU) to
+// itself; cut, 35 us and 7 passes over rows at 5 TB/s. Means over 2048 are left
+// out: where the lengths differ, the longest sequence's items then end long after
+// the others (12 sequences of 492 to 7435 tokens, 32 heads: 376 us with 2048, 487
+// with 4096).
 int64_t segment_tokens(const gdn_linear_problem* p) {
-  const int64_t whole = ((int64_t)p->T + kChunk - 1) / kChunk * kChunk;
-  return std::max<int64_t>(whole, kChunk);
+  const int64_t work = (int64_t)p->T * p->HV, chains = (int64_t)p->N * p->HV;
+  int64_t S = 256;
+  while (S < 4096 && S * 2 * 512 <= work) S *= 2;
+  const int64_t mean = p->N > 0 ? ((int64_t)p->T + p->N - 1) / p->N : 0;
+  if (chains >= 128 && mean <= 2048) {
+    const bool full = p->K == 128;
+    const double uncut = 10. + (double)mean / kChunk * (full ? 3.6 : 2.0) * std::max(1., (double)chains / (full ? 256 : 512));
+    const double cut = 35. + (double)work * p->K * 2 * 7 / 5e6;
+    if (uncut < cut)
+      while (S < mean) S *= 2;
+  }
+  return S;
 }
 
 bool bad_stride(int64_t s, int64_t dense) {
@@ -57,8 +83,8 @@ gdn_status check_pack(const gdn_linear_problem* p) {
   const gdn_status st = check_linear(p);
   if (st != GDN_OK) return st;
   const int64_t slots = (int64_t)p->T / segment_tokens(p) + p->N;
-  if (segment_tokens(p) > INT32_MAX || slots * p->HV > kMaxBlocks ||
-      (int64_t)p->N * p->HV * (p->K * p->V / 1024) > kMaxBlocks)
+  if (segment_tokens(p) > INT32_MAX || 2 * slots * p->HV + 16 > kMaxBlocks ||
+      (int64_t)p->N * p->HV * (p->K * p->V / 256) > 4 * kMaxBlocks)
     return GDN_ERR_SHAPE;
   if (p->cu_seqlens_host) {
     const int32_t* cu = p->cu_seqlens_host;
@@ -88,8 +114,14 @@ gdn_status check_indices(int N, int slots, const int32_t* host) {
 
 float scale_of(const gdn_linear_problem* p) { return p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->K); }
 
-// whether one sequence can hold more than one segment
-bool several(const gdn_linear_problem* p) { return p->T > segment_tokens(p); }
+// whether a sequence may hold more than one segment (with the host's boundaries: does)
+bool several(const gdn_linear_problem* p) {
+  const int64_t S = segment_tokens(p);
+  if (!p->cu_seqlens_host) return p->T > S;
+  for (int n = 0; n < p->N; ++n)
+    if (p->cu_seqlens_host[n + 1] - p->cu_seqlens_host[n] > S) return true;
+  return false;
+}
 
 size_t states_bytes(const gdn_linear_problem* p) {
   return (size_t)cut_of(p).slots * p->HV * p->K * p->V * sizeof(float);
@@ -97,10 +129,10 @@ size_t states_bytes(const gdn_linear_problem* p) {
 size_t wide_bytes(const gdn_linear_problem* p) {  // dq or dk of every value head
   return p->HV == p->H ? 0 : (size_t)p->T * p->HV * p->K * sizeof(float);
 }
-size_t fwd_bytes(const gdn_linear_problem* p) { return several(p) ? states_bytes(p) : 0; }
-size_t bwd_bytes(const gdn_linear_problem* p) {
-  return (several(p) ? states_bytes(p) : 0) + 2 * wide_bytes(p);
-}
+// sizes do not go by the boundaries
+size_t ends_bytes(const gdn_linear_problem* p) { return p->T > segment_tokens(p) ? states_bytes(p) : 0; }
+size_t fwd_bytes(const gdn_linear_problem* p) { return ends_bytes(p); }
+size_t bwd_bytes(const gdn_linear_problem* p) { return ends_bytes(p) + 2 * wide_bytes(p); }
 
 LinRows rows(const uint16_t* x, int64_t stride, int heads, int G, int D) {
   return {x, stride ? stride : (int64_t)heads * D, G};
@@ -131,13 +163,14 @@ int linear_fwd(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k
   const float scale = scale_of(p);
   const LinRows a = rows(q, p->q_stride, p->H, G, D), b = rows(k, p->k_stride, p->H, G, D),
                 c = rows(v, p->v_stride, p->HV, 1, D);
-  float* states = nullptr;  // of the segments' starts, where they are needed
+  const bool cut_up = several(p);
+  float* states = nullptr;  // that the segments start from, where they are needed
   if (saved) states = static_cast<float*>(saved);
-  else if (several(p)) states = static_cast<float*>(workspace);
-  if (several(p)) GDN_TRY(launch_lin_gather(false, D, cut, log_decay, scale, b, c, states, s));
-  if (states) GDN_TRY(launch_lin_join(false, several(p), D, cut, log_decay, io, states, s));
+  else if (cut_up) states = static_cast<float*>(workspace);
+  if (cut_up) GDN_TRY(launch_lin_gather(D, false, cut, log_decay, 1.f, b, c, io.hT != nullptr, states, s));
+  if (states) GDN_TRY(launch_lin_join(D, false, cut, log_decay, io, states, s));
   const LinPass pass{a, b, c, o, states, io};
-  GDN_TRY(launch_lin_pass(LinKind::kOut, false, D, cut, log_decay, scale, pass, s));
+  GDN_TRY(launch_lin_out(D, cut, log_decay, scale, pass, s));
   return GDN_OK;
 }
 
@@ -201,26 +234,20 @@ GDN_API int gdn_linear_bwd(const gdn_linear_problem* p, const uint16_t* q, const
   char* ws = static_cast<char*>(workspace);
   const StateRef io{dhT, dh0, nullptr, nullptr, 0, nullptr}, none{};
   const float* start = static_cast<const float*>(saved);
-  float* ends = nullptr;  // gradients of the states that the segments end with
-  if (several(p)) {
-    ends = reinterpret_cast<float*>(ws);
-    ws += states_bytes(p);
-    GDN_TRY(launch_lin_gather(true, D, cut, log_decay, scale, rq, ro, ends, s));
-    GDN_TRY(launch_lin_join(true, true, D, cut, log_decay, io, ends, s));
-  }
+  float* ends = several(p) ? reinterpret_cast<float*>(ws) : nullptr;  // gradients of the segments' end states
+  ws += ends_bytes(p);
   const bool wide = G > 1;
   float* wq = reinterpret_cast<float*>(ws);
   float* wk = reinterpret_cast<float*>(ws + wide_bytes(p));
   const LinPass pq{ro, rv, rk, wide ? (void*)wq : dq, start, none};
   const LinPass pv{rk, rq, ro, dv, ends, io};
   const LinPass pk{rv, ro, rq, wide ? (void*)wk : dk, ends, StateRef{dhT, nullptr, nullptr, nullptr, 0, nullptr}};
-  GDN_TRY(launch_lin_pass(LinKind::kDq, wide, D, cut, log_decay, scale, pq, s));
-  GDN_TRY(launch_lin_pass(LinKind::kDv, false, D, cut, log_decay, scale, pv, s));
-  GDN_TRY(launch_lin_pass(LinKind::kDk, wide, D, cut, log_decay, scale, pk, s));
-  if (wide && p->T > 0) {
-    GDN_TRY(launch_lin_fold(D, p->T, p->H, G, wq, dq, s));
-    GDN_TRY(launch_lin_fold(D, p->T, p->H, G, wk, dk, s));
+  if (ends) {
+    GDN_TRY(launch_lin_gather(D, true, cut, log_decay, scale, rq, ro, dh0 != nullptr, ends, s));
+    GDN_TRY(launch_lin_join(D, true, cut, log_decay, io, ends, s));
   }
+  GDN_TRY(launch_lin_grad(D, wide, cut, log_decay, scale, pq, pv, pk, s));
+  if (wide && p->T > 0) GDN_TRY(launch_lin_fold(D, p->T, p->H, G, wq, wk, dq, dk, s));
   return GDN_OK;
 }
 

@@ -17,6 +17,8 @@
 // own rounding. The state itself stays fp32, and what a chunk adds to it keeps
 // fp32's precision: the decayed rows of c (fp32) enter the MFMA as three bf16
 // pieces that hold all 24 bits, against b's exact bf16 rows.
+#include <type_traits>
+
 #include "linear.h"
 
 namespace gdn {
@@ -67,6 +69,9 @@ __device__ __forceinline__ Segment find_segment(const LinCut& c, int slot) {
   s.t1 = (int)min(t0 + c.S, (int64_t)s.eos);
   return s;
 }
+// whether it is its whole sequence
+__device__ __forceinline__ bool whole(const Segment& s) { return s.index == 0 && s.t1 >= s.eos; }
+__device__ __forceinline__ int chunks_of(const Segment& s) { return (s.t1 - s.t0 + kChunk - 1) / kChunk; }
 // whether the slot holds a segment: each sequence, an empty one too, has its first
 __device__ __forceinline__ bool unused(const Segment& s) {
   return s.index < 0 || (s.index > 0 && s.t0 >= s.eos);
@@ -91,34 +96,77 @@ __device__ __forceinline__ StateAt state_at(const StateRef& io, int seq, int hv,
   return {from ? from + base : nullptr, to ? to + base : nullptr};
 }
 
-// LDS rows of D bf16 with 8 elements of padding: 16-byte fragment reads of
-// consecutive rows then start 4 banks apart.
+// 64 rows of D bf16 in LDS, 16-byte pieces of a row permuted by the row's number
+// (xor): the 16 rows of a row-wise operand read, and the 4 rows x 2 pieces that a
+// lane group's transposing read takes, then all lie in different banks (with rows
+// padded by 16 bytes instead, nearly half of the LDS cycles were conflicts). The
+// permutation has a period of 16 rows, so it is a constant of the lane.
 template <int D>
-constexpr int kPitch = D + 8;
+__device__ __forceinline__ int piece_of(int row) {
+  const int x = D == 128 ? row & 15 : (row >> 1) & 7;
+  return ((x & 3) << 1) | ((x >> 2) & 1) | (x & 8);
+}
+// element offset of column c (a multiple of 4) of a row
+template <int D>
+__device__ __forceinline__ int at(int row, int c) {
+  return row * D + (((c >> 3) ^ piece_of<D>(row)) << 3) + (c & 4);
+}
 constexpr int kPPitch = kChunk + 8;
 
 // 64 rows of one operand, 16 bytes a piece, held by the NT threads.
 template <int D, int NT>
 struct RowRegs {
-  static constexpr int kPieces = kChunk * D / 8 / NT;
+  static constexpr int kPieces = kChunk * D / 8 / NT, kRows = kChunk / kPieces;  // rows a piece of all threads
   uint4 x[kPieces];
-  __device__ __forceinline__ void load(const LinRows& r, int64_t t0, int len, int hv, int tid) {
-    // rows past the chunk's end read as zeros
-    const int bytes = len > 0 ? (int)(((len - 1) * r.stride + D) * 2) : 0;
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(r.p) + t0 * r.stride + (int64_t)(hv / r.G) * D, 0, bytes, kBufferWord3);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int e = tid + i * NT, row = e / (D / 8), col = e % (D / 8);
-      x[i] = load_b128(rsrc, (int)(row * r.stride * 2) + col * 16);
-    }
+  // Piece i of the rows that a resource of chunk_rows covers; lane_byte: this thread's row (of kRows) and piece.
+  // Rows past the chunk's end lie past the resource and read as zeros.
+  __device__ __forceinline__ void load(int i, __amdgpu_buffer_rsrc_t rows, int lane_byte, int step_bytes) {
+    x[i] = load_b128(rows, lane_byte + i * step_bytes);
+  }
+  static __device__ __forceinline__ int lane_byte(int64_t stride, int tid) {
+    return (int)(tid / (D / 8) * stride * 2) + tid % (D / 8) * 16;
   }
   __device__ __forceinline__ void store(uint16_t* tile, int tid) const {
+    const int off = at<D>(tid / (D / 8), tid % (D / 8) * 8);  // kRows is a multiple of 16
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int e = tid + i * NT, row = e / (D / 8), col = e % (D / 8);
-      *reinterpret_cast<uint4*>(tile + row * kPitch<D> + col * 8) = x[i];
-    }
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(tile + off + i * kRows * D) = x[i];
+  }
+};
+// the head's columns of the pack's first token
+template <int D>
+__device__ __forceinline__ const uint16_t* head_of(const LinRows& r, int hv) {
+  return r.p + (int64_t)(hv / r.G) * D;
+}
+
+// The rows of len tokens from t0 on (none: an empty resource), of a head whose columns of token 0 are at p.
+template <int D>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, int64_t stride, int64_t t0, int len) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + t0 * stride, 0,
+                                           len > 0 ? (int)(((len - 1) * stride + D) * 2) : 0, kBufferWord3);
+}
+
+// A value that the compiler must not keep computed things of across the loop:
+// the LDS offsets that follow from it by one xor cost a register each otherwise.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+// Offsets of a wave's operand reads: one lane-dependent part each, to which a
+// read's pieces add by xor (they are bits below the row's) and its 16-row tiles
+// by plus.
+template <int D>
+struct Lane {
+  int row32, row16, ka, kb, va, vb;
+  __device__ __forceinline__ Lane(int lane, int wave) {
+    const int l32 = lane & 31, hi = lane >> 5, l16 = lane & 15, q4 = lane >> 4, j = lane & 15;
+    row32 = at<D>(l32, 8 * hi);
+    row16 = at<D>(l16, 8 * q4);
+    const int r = 8 * hi + (j >> 2), c = 16 * (q4 & 1);
+    const int swapped = ((j & 1) << 1) | ((j >> 1) & 1);  // see column8
+    ka = at<D>(r, c + 4 * swapped);
+    kb = at<D>(r + 4, c + 4 * swapped);
+    va = at<D>(r, 32 * wave + c + 4 * (j & 3));
+    vb = at<D>(r + 4, 32 * wave + c + 4 * (j & 3));
   }
 };
 
@@ -126,7 +174,7 @@ struct RowRegs {
 // 8 m + e of tile kb is k = 32 kb + 16 m + 8 (lane / 32) + e: the accumulator's
 // rows, taken in an order that makes 8 consecutive k one MFMA operand, so that
 // the state is multiplied from the registers that it is gathered in. (The
-// operand gathered from, b^T, is read in that order: see b_col8.)
+// operand gathered from, b^T, is read in that order: see column8.)
 template <int D>
 struct State {
   static constexpr int KB = D / 32;
@@ -175,6 +223,12 @@ struct State {
         }
       }
   }
+  __device__ __forceinline__ void decay(float f) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[kb][r] *= f;
+  }
   __device__ __forceinline__ bf16x8 operand(int kb, int m) const {
     const f32x16& s = x[kb];
     return __builtin_bit_cast(bf16x8, make_uint4(pk2(s[8 * m], s[8 * m + 1]), pk2(s[8 * m + 2], s[8 * m + 3]),
@@ -182,36 +236,38 @@ struct State {
   }
 };
 
-// Column c0 + lane % 16 of rows r0 .. r0 + 7 (as lds_col8), the 16 columns'
-// middle groups of four exchanged: the order of State's rows.
-__device__ __forceinline__ bf16x8 b_col8(const uint16_t* tile, int pitch, int r0, int c0, int lane) {
-  const int j = lane & 15, piece = ((j & 1) << 1) | ((j >> 1) & 1);
-  const uint2 a = lds_tr16(tile + (r0 + (j >> 2)) * pitch + c0 + 4 * piece);
-  const uint2 b = lds_tr16(tile + (r0 + 4 + (j >> 2)) * pitch + c0 + 4 * piece);
-  return __builtin_bit_cast(bf16x8, make_uint4(a.x, a.y, b.x, b.y));
+// A lane's column (lane % 16 of its group's 16) of 8 rows by two transposing reads
+// of 4 rows (see lds_tr16). b's are read with the 16 columns' middle groups of four
+// exchanged, which is the order of State's rows.
+__device__ __forceinline__ uint4 column8(const uint16_t* tile, int a, int b) {
+  const uint2 x = lds_tr16(tile + a), y = lds_tr16(tile + b);
+  return make_uint4(x.x, x.y, y.x, y.y);
 }
 
-// c's columns of one 16-token step times the tokens' weights, as three bf16
-// operands whose sum holds the fp32 products' 24 bits.
+// c's columns of one 16-token step times the tokens' weights, as kPieces bf16
+// operands: three hold the fp32 products' 24 bits, two their first 16.
+template <int kPieces>
 struct Split {
-  bf16x8 hi, mid, lo;
-};
-__device__ __forceinline__ Split split(const uint4& c, const float* w) {
-  uint32_t h[4], m[4], l[4];
-  const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+  bf16x8 x[kPieces];  // largest first
+  __device__ __forceinline__ void of(const uint4& c, const float* w) {
+    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+    uint32_t h[kPieces][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x0 = __uint_as_float(u[i] << 16) * w[2 * i];
-    const float x1 = __uint_as_float(u[i] & 0xffff0000u) * w[2 * i + 1];
-    h[i] = pk2(x0, x1);
-    const float r0 = x0 - __uint_as_float(h[i] << 16), r1 = x1 - __uint_as_float(h[i] & 0xffff0000u);
-    m[i] = pk2(r0, r1);
-    l[i] = pk2(r0 - __uint_as_float(m[i] << 16), r1 - __uint_as_float(m[i] & 0xffff0000u));
+    for (int i = 0; i < 4; ++i) {
+      float r0 = __uint_as_float(u[i] << 16) * w[2 * i];
+      float r1 = __uint_as_float(u[i] & 0xffff0000u) * w[2 * i + 1];
+#pragma unroll
+      for (int n = 0; n < kPieces; ++n) {
+        h[n][i] = pk2(r0, r1);
+        r0 -= __uint_as_float(h[n][i] << 16);
+        r1 -= __uint_as_float(h[n][i] & 0xffff0000u);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kPieces; ++n)
+      x[n] = __builtin_bit_cast(bf16x8, make_uint4(h[n][0], h[n][1], h[n][2], h[n][3]));
   }
-  return {__builtin_bit_cast(bf16x8, make_uint4(h[0], h[1], h[2], h[3])),
-          __builtin_bit_cast(bf16x8, make_uint4(m[0], m[1], m[2], m[3])),
-          __builtin_bit_cast(bf16x8, make_uint4(l[0], l[1], l[2], l[3]))};
-}
+};
 
 // Weight of token t of a chunk of len tokens in the state: front to back
 // lam^(len - 1 - t), back to front scale lam^(t + 1); zero past the end (where
@@ -222,104 +278,209 @@ __device__ __forceinline__ float weight(float g2, float scale, int t, int len) {
   return kBack ? scale * power(g2, t + 1) : power(g2, len - 1 - t);
 }
 
-// X <- lam^len X + b^T diag(w) c for one chunk in LDS.
-template <int D>
-__device__ __forceinline__ void gather_chunk(State<D>& X, float decay, const uint16_t* Bs, const uint4* cc,
-                                             const float* ws, int lane) {
-  const int g = lane >> 4, hi = lane >> 5;
+// X <- X + b^T diag(w) c for one chunk in LDS, 16 tokens a step. A step's
+// operands are read and split while the step before multiplies.
+template <int D, int kPieces>
+__device__ __forceinline__ void gather_chunk(State<D>& X, const uint16_t* Bs, const uint4* cc, const float* ws,
+                                             const Lane<D>& L, int hi) {
+  constexpr int KB = State<D>::KB;
+  const int ka = fresh(L.ka), kb = fresh(L.kb);
+  uint4 k[2][KB];
+  Split<kPieces> v[2];
+  auto read = [&](int s) {
 #pragma unroll
-  for (int kb = 0; kb < State<D>::KB; ++kb)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) X.x[kb][r] *= decay;
+    for (int i = 0; i < KB; ++i) k[s & 1][i] = column8(Bs + 16 * s * D, ka ^ (32 * i), kb ^ (32 * i));
+  };
+  read(0);
+  v[0].of(cc[0], ws + 8 * hi);
 #pragma unroll
   for (int s = 0; s < 4; ++s) {
-    const Split v = split(cc[s], ws + 16 * s + 8 * hi);
-#pragma unroll
-    for (int kb = 0; kb < State<D>::KB; ++kb) {
-      const bf16x8 k = b_col8(Bs, kPitch<D>, 16 * s + 8 * (g >> 1), 32 * kb + 16 * (g & 1), lane);
-      X.x[kb] = mfma32(k, v.lo, X.x[kb]);
-      X.x[kb] = mfma32(k, v.mid, X.x[kb]);
-      X.x[kb] = mfma32(k, v.hi, X.x[kb]);
+    if (s < 3) {
+      read(s + 1);
+      v[(s + 1) & 1].of(cc[s + 1], ws + 16 * (s + 1) + 8 * hi);
     }
+    // smallest pieces first; the state's tiles in turn, so that no product waits for the one before it
+#pragma unroll
+    for (int n = kPieces - 1; n >= 0; --n)
+#pragma unroll
+      for (int i = 0; i < KB; ++i) X.x[i] = mfma32(__builtin_bit_cast(bf16x8, k[s & 1][i]), v[s & 1].x[n], X.x[i]);
+    if (s < 3) {
+      // a product, then the vector instructions that fit beside it
+#pragma unroll
+      for (int i = 0; i < kPieces * KB; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, 24 / KB, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 template <int D>
-__device__ __forceinline__ void load_columns(uint4* cc, const uint16_t* Cs, int wave, int lane) {
-  const int g = lane >> 4;
+__device__ __forceinline__ void load_columns(uint4* cc, const uint16_t* Cs, const Lane<D>& L) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    cc[s] = lds_col8(Cs, kPitch<D>, 16 * s + 8 * (g >> 1), 32 * wave + 16 * (g & 1), lane);
+  for (int s = 0; s < 4; ++s) cc[s] = column8(Cs + 16 * s * D, L.va, L.vb);
+}
+
+// The n-th 16 x 16 tile of P of a wave, rows i, columns j: the 10 tiles on and on
+// one side of the diagonal, 3 or 5 to a wave, the first of them of one row i, so
+// that a's rows are read once for these. (With 4 waves, two tiles are formed twice,
+// which costs less than a branch.)
+struct Tile {
+  int i, j;
+};
+template <int NW>
+constexpr int kTilesOf = NW == 4 ? 3 : 5;
+template <int NW, bool kBack>
+__device__ __forceinline__ Tile tile_of(int wave, int n) {
+  int i, j;
+  if constexpr (NW == 4) {  // 33 32 31; 22 21 20; 11 10 30; 00 00 30 (its n = 0, 1 are the same tile)
+    i = n < 2 ? 3 - wave : wave < 2 ? 3 - wave : 3;
+    j = n < 2 ? max(3 - wave - n, 0) : wave < 2 ? 1 - wave : 0;
+  } else {  // 33 32 31 11 10; 22 21 20 30 00
+    i = n < 3 ? 3 - wave : wave == 0 ? 1 : n == 3 ? 3 : 0;
+    j = n < 3 ? 3 - wave - n : wave == 0 ? 4 - n : 0;
+  }
+  if (kBack) return {3 - i, 3 - j};
+  return {i, j};
 }
 
 }  // namespace
 
-// One workgroup per (segment, value head), one wave per 32 columns of the
-// state and the output.
-template <int D, bool kBack, bool kT, bool kWide>
-__global__ __launch_bounds__(2 * D, 2) void lin_pass_kernel(LinCut cut, const float* __restrict__ log_decay,
-                                                            float scale, LinPass p) {
-  constexpr int NW = D / 32, NT = 64 * NW;
-  const int hv = blockIdx.x % cut.HV, slot = blockIdx.x / cut.HV;
-  const Segment sg = find_segment(cut, slot);
-  if (unused(sg)) return;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+// One segment of one value head by one workgroup, one wave per 32 columns of
+// the state and the output.
+// The n-th (segment, value head): heads side by side, so that a token's whole row
+// is read at about one time, and a head's place moved by one from segment to
+// segment. Without that, an XCD (workgroups go to the 8 in turn) reads the same 256
+// bytes of every 2 KiB throughout, and two of the eight took 14 % longer than the
+// others: gradients of 2 x 8192 tokens, 32 heads, 300 us, and 286 with it.
+__device__ __forceinline__ void item(const LinCut& cut, int n, int& slot, int& hv) {
+  slot = n / cut.HV;
+  hv = (n + slot) % cut.HV;
+}
+
+template <int D>
+struct PassLds {
+  uint16_t As[kChunk * D], Bs[kChunk * D], Cs[kChunk * D];
+  uint16_t Ps[kChunk * kPPitch];
+  float ws[kChunk];
+};
+
+// kEnds: the segment is a whole sequence whose end state goes to p.io: it is
+// gathered to fp32's precision. Otherwise the carried state only meets a, rounded
+// to bf16, and 16 bits of what it gathers are enough (a third less matrix work);
+// what a sequence of several segments ends with is lin_join's.
+template <int D, bool kBack, bool kT, bool kWide, bool kEnds>
+__device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, const Segment& sg,
+                                         const float* __restrict__ log_decay, float scale, const LinPass& p,
+                                         PassLds<D>& lds) {
+  constexpr int NW = D / 32, NT = 64 * NW, kTiles = kTilesOf<NW>;
+  uint16_t *As = lds.As, *Bs = lds.Bs, *Cs = lds.Cs, *Ps = lds.Ps;
+  float* ws = lds.ws;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int l32 = lane & 31, hi = lane >> 5, l16 = lane & 15, q4 = lane >> 4;
   const float g2 = decay2(log_decay[hv]);
-
-  __shared__ __align__(16) uint16_t As[kChunk * kPitch<D>];
-  __shared__ __align__(16) uint16_t Bs[kChunk * kPitch<D>];
-  __shared__ __align__(16) uint16_t Cs[kChunk * kPitch<D>];
-  __shared__ __align__(16) uint16_t Ps[kChunk * kPPitch];
-  __shared__ __align__(16) float ws[kChunk];
 
   // P's tiles on the far side of the diagonal stay zero
   for (int i = tid; i < kChunk * kPPitch / 8; i += NT) reinterpret_cast<uint4*>(Ps)[i] = make_uint4(0, 0, 0, 0);
 
-  const bool first = kBack ? sg.t1 >= sg.eos : sg.index == 0;  // the first that the pass meets
-  const bool last = kBack ? sg.index == 0 : sg.t1 >= sg.eos;
-  const StateAt at = state_at(p.io, sg.seq, hv, cut.HV, D * D);
+  const StateAt state = state_at(p.io, sg.seq, hv, cut.HV, D * D);
   const int col = 32 * wave + l32;
   State<D> X;
-  (void)first;
-  X.template load<kT>(p.start ? p.start + ((size_t)slot * cut.HV + hv) * (D * D) : at.from, col, hi);
+  X.template load<kT>(p.start ? p.start + ((size_t)slot * cut.HV + hv) * (D * D) : state.from, col, hi);
 
-  const int chunks = (sg.t1 - sg.t0 + kChunk - 1) / kChunk;
+  const int chunks = chunks_of(sg);
+  // the decays of this lane's elements of P do not change from chunk to chunk
+  float pw[kTiles][4];
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) {
+    const Tile x = tile_of<NW, kBack>(wave, n);
+    const int d = 16 * (kBack ? x.j - x.i : x.i - x.j) + (kBack ? 4 * q4 - l16 : l16 - 4 * q4);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int e = kBack ? d + r : d - r;
+      pw[n][r] = e >= 0 ? scale * power(g2, e) : 0.f;
+    }
+  }
+  // the next chunk's rows are on their way while a chunk is computed
+  const Lane<D> L(lane, wave);
+  RowRegs<D, NT> ra, rb, rc;
+  const uint16_t *ap = head_of<D>(p.a, hv), *bp = head_of<D>(p.b, hv), *cp = head_of<D>(p.c, hv);
+  const int la = ra.lane_byte(p.a.stride, tid), lb = rb.lane_byte(p.b.stride, tid), lc = rc.lane_byte(p.c.stride, tid);
+  const int sa = (int)(ra.kRows * p.a.stride * 2), sb = (int)(rb.kRows * p.b.stride * 2), sc = (int)(rc.kRows * p.c.stride * 2);
+  // one of the next chunk's 12 pieces; past the segment's end they are zeros that nothing reads
+  __amdgpu_buffer_rsrc_t na, nb, nc;
+  auto next = [&](int i) {
+    const int64_t t0 = sg.t0 + (int64_t)(kBack ? chunks - 1 - i : i) * kChunk;
+    const int len = i < chunks ? min(kChunk, sg.t1 - (int)t0) : 0;
+    na = chunk_rows<D>(ap, p.a.stride, t0, len);
+    nb = chunk_rows<D>(bp, p.b.stride, t0, len);
+    nc = chunk_rows<D>(cp, p.c.stride, t0, len);
+  };
+  constexpr int kLoads = 3 * RowRegs<D, NT>::kPieces;
+  auto request = [&](int j) {
+    const int piece = j / 3;
+    if (j % 3 == 0) ra.load(piece, na, la, sa);
+    if (j % 3 == 1) rb.load(piece, nb, lb, sb);
+    if (j % 3 == 2) rc.load(piece, nc, lc, sc);
+  };
+  using Out = typename std::conditional<kWide, float, uint16_t>::type;
+  const int orow = cut.HV * D * (int)sizeof(Out);  // bytes of a token's output row
+  const int ob = l32 * orow + (kWide ? (32 * wave + 4 * hi) * 4 : (32 * wave + 8 * hi) * 2);
+  next(0);
+#pragma unroll
+  for (int j = 0; j < kLoads; ++j) request(j);
   for (int i = 0; i < chunks; ++i) {
-    const int c = kBack ? chunks - 1 - i : i;
-    const int64_t t0 = sg.t0 + c * kChunk;
+    const int64_t t0 = sg.t0 + (kBack ? chunks - 1 - i : i) * kChunk;
     const int len = min(kChunk, sg.t1 - (int)t0);
-    RowRegs<D, NT> ra, rb, rc;
-    ra.load(p.a, t0, len, hv, tid);
-    rb.load(p.b, t0, len, hv, tid);
-    rc.load(p.c, t0, len, hv, tid);
-    __syncthreads();  // the last chunk's readers are done
+    lds_barrier();  // the last chunk's readers are done
     ra.store(As, tid);
     rb.store(Bs, tid);
     rc.store(Cs, tid);
     if (tid < kChunk) ws[tid] = weight<kBack>(g2, scale, tid, len);
-    __syncthreads();
+    lds_barrier();
+    next(i + 1);
 
     // P[i][j] = scale lam^|i - j| a_i . b_j, in 16 x 16 tiles on and beside the
-    // diagonal, as P^T tiles so that a lane holds 4 consecutive j of one i
+    // diagonal, as P^T tiles so that a lane holds 4 consecutive j of one i. The
+    // next chunk's requests go out between the tiles and the steps below: all at
+    // once they would hold the wave up for longer than a tile takes.
+    const int r16 = fresh(L.row16);
+    f32x4 pt[kTiles];
+    {
+      // the tiles' rows of a: the first tiles' one i, then another for each
+      constexpr int kFirst = NW == 4 ? 2 : 3;
+      auto group = [](int n) { return n < kFirst ? 0 : n - kFirst + 1; };
+      bf16x8 arow[kTiles - kFirst + 1][D / 32], brow[kTiles][D / 32];
 #pragma unroll
-    for (int n = 0; n < 16 / NW; ++n) {
-      const int tile = wave + NW * n, ti = tile >> 2, tj = tile & 3;
-      if (kBack ? tj < ti : tj > ti) continue;
-      f32x4 acc = zero4();
+      for (int n = 0; n < kTiles; ++n) {
+        const Tile x = tile_of<NW, kBack>(wave, n);
+        pt[n] = zero4();
 #pragma unroll
-      for (int s = 0; s < D / 32; ++s)
-        acc = mfma(ld8(Bs + (16 * tj + l16) * kPitch<D> + 32 * s + 8 * q4),
-                   ld8(As + (16 * ti + l16) * kPitch<D> + 32 * s + 8 * q4), acc);
-      const int pi = 16 * ti + l16, pj = 16 * tj + 4 * q4;
+        for (int s = 0; s < D / 32; ++s) brow[n][s] = ld8(Bs + 16 * D * x.j + (r16 ^ (32 * s)));
+        if (n == 0 || n >= kFirst) {
+#pragma unroll
+          for (int s = 0; s < D / 32; ++s) arow[group(n)][s] = ld8(As + 16 * D * x.i + (r16 ^ (32 * s)));
+        }
+        __builtin_amdgcn_sched_barrier(0);  // all reads are on their way before the first product waits for one
+      }
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) pt[n] = mfma(brow[n][s], arow[group(n)][s], pt[n]);
+        if (s < kTiles) request(s);
+      }
+#pragma unroll
+      for (int s = D / 32; s < kTiles; ++s) request(s);
+    }
+    auto put = [&](int n) {  // a finished tile times its decays, in bf16
+      const Tile x = tile_of<NW, kBack>(wave, n);
       float w[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = kBack ? pj + r - pi : pi - pj - r;
-        w[r] = d >= 0 ? acc[r] * (scale * power(g2, d)) : 0.f;
-      }
-      *reinterpret_cast<uint2*>(Ps + pi * kPPitch + pj) = pack4_bf16(w[0], w[1], w[2], w[3]);
-    }
+      for (int r = 0; r < 4; ++r) w[r] = pw[n][r] != 0.f ? pt[n][r] * pw[n][r] : 0.f;
+      *reinterpret_cast<uint2*>(Ps + (16 * x.i + l16) * kPPitch + 16 * x.j + 4 * q4) = pack4_bf16(w[0], w[1], w[2], w[3]);
+    };
 
     // the state's part of the output, transposed: rows are columns of c
     f32x16 o[2];
@@ -327,15 +488,26 @@ __global__ __launch_bounds__(2 * D, 2) void lin_pass_kernel(LinCut cut, const fl
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) o[tb][r] = 0.f;
+    const int r32 = fresh(L.row32);
+    bf16x8 q[2][2];  // read one step ahead
+    auto read = [&](int s) {
 #pragma unroll
-    for (int kb = 0; kb < State<D>::KB; ++kb)
+      for (int tb = 0; tb < 2; ++tb) q[s & 1][tb] = ld8(As + 32 * D * tb + (r32 ^ (16 * s)));
+    };
+    constexpr int kSteps = D / 16, kLeft = kLoads - kTiles;
+    read(0);
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const bf16x8 x = X.operand(kb, m);
+    for (int s = 0; s < kSteps; ++s) {
+      if (s + 1 < kSteps) read(s + 1);
+      const bf16x8 x = X.operand(s >> 1, s & 1);
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
-          o[tb] = mfma32(x, ld8(As + (32 * tb + l32) * kPitch<D> + 32 * kb + 16 * m + 8 * hi), o[tb]);
-      }
+      for (int tb = 0; tb < 2; ++tb) o[tb] = mfma32(x, q[s & 1][tb], o[tb]);
+#pragma unroll
+      for (int n = s * kTiles / kSteps; n < (s + 1) * kTiles / kSteps; ++n) put(n);
+#pragma unroll
+      for (int j = kTiles + s * kLeft / kSteps; j < kTiles + (s + 1) * kLeft / kSteps; ++j) request(j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) {
       const int t = 32 * tb + l32;
@@ -344,115 +516,193 @@ __global__ __launch_bounds__(2 * D, 2) void lin_pass_kernel(LinCut cut, const fl
       for (int r = 0; r < 16; ++r) o[tb][r] *= f;
     }
     uint4 cc[4];
-    load_columns<D>(cc, Cs, wave, lane);
-    __syncthreads();  // P is there
+    load_columns<D>(cc, Cs, L);
+    lds_barrier();  // P is there
+    bf16x8 pr[2][4];
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (kBack ? s < 2 * tb : s >= 2 * tb + 2) continue;
-        o[tb] = mfma32(__builtin_bit_cast(bf16x8, cc[s]),
-                       ld8(Ps + (32 * tb + l32) * kPPitch + 16 * s + 8 * hi), o[tb]);
-      }
+      for (int s = 0; s < 4; ++s)
+        if (kBack ? s >= 2 * tb : s < 2 * tb + 2) pr[tb][s] = ld8(Ps + (32 * tb + l32) * kPPitch + 16 * s + 8 * hi);
+    X.decay(power(g2, len));  // beside these reads and products
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        if (kBack ? s >= 2 * tb : s < 2 * tb + 2) o[tb] = mfma32(__builtin_bit_cast(bf16x8, cc[s]), pr[tb][s], o[tb]);
 
-    // row t = 32 tb + lane % 32; register 4 j + i is column 8 j + 4 (lane / 32) + i
+    // row t = 32 tb + lane % 32; register 4 j + i is column 8 j + 4 (lane / 32) + i. Rows past the chunk's end are
+    // past the buffer's, whose stores the hardware drops.
+    Out* const out = static_cast<Out*>(p.out) + (t0 * cut.HV + hv) * D;
+    const __amdgpu_buffer_rsrc_t ro =
+        __builtin_amdgcn_make_buffer_rsrc(out, 0, (len - 1) * orow + D * (int)sizeof(Out), kBufferWord3);
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) {
-      const int t = 32 * tb + l32;
-      const size_t row = ((size_t)(t0 + t) * cut.HV + hv) * D + 32 * wave;
-      if (t < len) {
-        if constexpr (kWide) {
-          float* out = static_cast<float*>(p.out) + row;
+      const f32x16& v = o[tb];
+      const int byte = ob + 32 * tb * orow;
+      if constexpr (kWide) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<f32x4*>(out + 8 * j + 4 * hi) =
-                f32x4{o[tb][4 * j], o[tb][4 * j + 1], o[tb][4 * j + 2], o[tb][4 * j + 3]};
-        }
-      }
-      if constexpr (!kWide) {
+        for (int j = 0; j < 4; ++j)
+          store_b128(__builtin_bit_cast(uint4, f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]}), ro, byte + 32 * j);
+      } else {
         // the half-waves exchange 4 columns, so that a lane stores 8 in a row
-        uint16_t* out = static_cast<uint16_t*>(p.out) + row;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const f32x16& v = o[tb];
           const auto x = __builtin_amdgcn_permlane32_swap(pk2(v[8 * m], v[8 * m + 1]), pk2(v[8 * m + 4], v[8 * m + 5]), false, false);
           const auto y = __builtin_amdgcn_permlane32_swap(pk2(v[8 * m + 2], v[8 * m + 3]), pk2(v[8 * m + 6], v[8 * m + 7]), false, false);
-          if (t < len) *reinterpret_cast<uint4*>(out + 16 * m + 8 * hi) = make_uint4(x[0], y[0], x[1], y[1]);
+          store_b128(make_uint4(x[0], y[0], x[1], y[1]), ro, byte + 32 * m);
         }
       }
     }
-    gather_chunk<D>(X, power(g2, len), Bs, cc, ws, lane);
+    gather_chunk<D, kEnds ? 3 : 2>(X, Bs, cc, ws, L, hi);
   }
-  if (last && at.to) X.template store<kT>(at.to, col, hi);
+  if (kEnds && state.to) X.template store<kT>(state.to, col, hi);
 }
 
-// What a segment adds to the state, from a zero start.
-template <int D, bool kBack>
-__global__ __launch_bounds__(2 * D, 2) void lin_gather_kernel(LinCut cut, const float* __restrict__ log_decay,
-                                                              float scale, LinRows b, LinRows c,
-                                                              float* __restrict__ states) {
-  constexpr int NW = D / 32, NT = 64 * NW;
-  const int hv = blockIdx.x % cut.HV, slot = blockIdx.x / cut.HV;
+template <int D>
+__global__ __launch_bounds__(2 * D, 2) void lin_out_kernel(LinCut cut, const float* __restrict__ log_decay,
+                                                           float scale, LinPass p) {
+  __shared__ __align__(16) PassLds<D> lds;
+  int slot, hv;
+  item(cut, blockIdx.x, slot, hv);
   const Segment sg = find_segment(cut, slot);
-  if (unused(sg) || (kBack ? sg.index == 0 : sg.t1 >= sg.eos)) return;  // nothing follows it
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  if (unused(sg)) return;
+  if (whole(sg)) lin_pass<D, false, false, false, true>(cut, slot, hv, sg, log_decay, scale, p, lds);
+  else lin_pass<D, false, false, false, false>(cut, slot, hv, sg, log_decay, scale, p, lds);
+}
+
+// What a segment adds to the state, from a zero start: sum over its tokens of
+// w_t b_t c_t^T, w_t = lam^(tokens after t) (back to front: scale lam^(tokens
+// from the segment's start through t)). The chunks of the largest weights come
+// first, and the rest are not read once every further weight is zero in fp32
+// (lam^n = 0 from e^-104 on), as it soon is for quickly forgetting heads.
+template <int D, bool kBack>
+__device__ __forceinline__ void lin_gather(const LinCut& cut, int slot, int hv, const float* __restrict__ log_decay,
+                                           float scale, const LinRows& b, const LinRows& c,
+                                           bool ends, float* __restrict__ states, PassLds<D>& lds) {
+  constexpr int NW = D / 32, NT = 64 * NW;
+  uint16_t *Bs = lds.Bs, *Cs = lds.Cs;
+  float* ws = lds.ws;
+  const Segment sg = find_segment(cut, slot);
+  if (unused(sg) || whole(sg) || (!ends && (kBack ? sg.index == 0 : sg.t1 >= sg.eos))) return;  // nothing needs it
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const float g2 = decay2(log_decay[hv]);
-  __shared__ __align__(16) uint16_t Bs[kChunk * kPitch<D>];
-  __shared__ __align__(16) uint16_t Cs[kChunk * kPitch<D>];
-  __shared__ __align__(16) float ws[kChunk];
   State<D> X;
   X.template load<false>(nullptr, 0, 0);
-  const int chunks = (sg.t1 - sg.t0 + kChunk - 1) / kChunk;
-  for (int i = 0; i < chunks; ++i) {
-    const int ch = kBack ? chunks - 1 - i : i;
-    const int64_t t0 = sg.t0 + ch * kChunk;
+  int chunks = chunks_of(sg);
+  // 2^-150 is the first power that rounds to zero
+  if (g2 < 0.f) chunks = min(chunks, (int)fminf(150.f / (-g2 * kChunk), 1e6f) + 2);
+  const Lane<D> L(lane, wave);
+  RowRegs<D, NT> rb, rc;
+  const uint16_t *bp = head_of<D>(b, hv), *cp = head_of<D>(c, hv);
+  const int lb = rb.lane_byte(b.stride, tid), lc = rc.lane_byte(c.stride, tid);
+  const int all = chunks_of(sg);
+  auto start = [&](int i) { return sg.t0 + (kBack ? i : all - 1 - i) * kChunk; };
+  auto request = [&](int i) {
+    const int64_t t0 = start(i);
     const int len = min(kChunk, sg.t1 - (int)t0);
-    RowRegs<D, NT> rb, rc;
-    rb.load(b, t0, len, hv, tid);
-    rc.load(c, t0, len, hv, tid);
-    __syncthreads();
+    const __amdgpu_buffer_rsrc_t nb = chunk_rows<D>(bp, b.stride, t0, len), nc = chunk_rows<D>(cp, c.stride, t0, len);
+#pragma unroll
+    for (int j = 0; j < RowRegs<D, NT>::kPieces; ++j) {
+      rb.load(j, nb, lb, (int)(rb.kRows * b.stride * 2));
+      rc.load(j, nc, lc, (int)(rc.kRows * c.stride * 2));
+    }
+  };
+  if (chunks > 0) request(0);
+  for (int i = 0; i < chunks; ++i) {
+    lds_barrier();
     rb.store(Bs, tid);
     rc.store(Cs, tid);
-    if (tid < kChunk) ws[tid] = weight<kBack>(g2, scale, tid, len);
-    __syncthreads();
+    if (tid < kChunk) {
+      const int t = start(i) + tid;
+      ws[tid] = t >= sg.t1 ? 0.f : kBack ? scale * power(g2, t - sg.t0 + 1) : power(g2, sg.t1 - 1 - t);
+    }
+    lds_barrier();
+    if (i + 1 < chunks) request(i + 1);
     uint4 cc[4];
-    load_columns<D>(cc, Cs, wave, lane);
-    gather_chunk<D>(X, power(g2, len), Bs, cc, ws, lane);
+    load_columns<D>(cc, Cs, L);
+    gather_chunk<D, 3>(X, Bs, cc, ws, L, lane >> 5);
   }
   X.template store<false>(states + ((size_t)slot * cut.HV + hv) * (D * D), 32 * wave + (lane & 31), lane >> 5);
 }
 
-// Front to back along each sequence's segments (or back to front): a thread
-// carries 4 values of one state.
 template <int D, bool kBack>
-__global__ __launch_bounds__(256) void lin_join_kernel(LinCut cut, bool gathered,
-                                                       const float* __restrict__ log_decay, StateRef io,
+__global__ __launch_bounds__(2 * D, 2) void lin_gather_kernel(LinCut cut, const float* __restrict__ log_decay,
+                                                              float scale, LinRows b, LinRows c, bool ends,
+                                                              float* __restrict__ states) {
+  __shared__ __align__(16) PassLds<D> lds;
+  int slot, hv;
+  item(cut, blockIdx.x, slot, hv);
+  lin_gather<D, kBack>(cut, slot, hv, log_decay, scale, b, c, ends, states, lds);
+}
+
+// The three gradients' passes in one launch. Workgroups go to the 8 XCDs in
+// turn; a segment's three are 8 apart, so that they run on one XCD at one time and
+// the rows that dv's and dk's passes both walk come from its L2 the second time.
+template <int D, bool kWide>
+__global__ __launch_bounds__(2 * D, 2) void lin_grad_kernel(LinCut cut, const float* __restrict__ log_decay,
+                                                            float scale, LinPass dq, LinPass dv, LinPass dk) {
+  __shared__ __align__(16) PassLds<D> lds;
+  const int nth = blockIdx.x >> 3, part = nth % 3, at = nth / 3 * 8 + (blockIdx.x & 7);
+  if (at >= cut.slots * cut.HV) return;
+  int slot, hv;
+  item(cut, at, slot, hv);
+  const Segment sg = find_segment(cut, slot);
+  if (unused(sg)) return;
+  if (part == 1) lin_pass<D, true, true, kWide, false>(cut, slot, hv, sg, log_decay, scale, dk, lds);
+  else if (part == 2) lin_pass<D, false, true, kWide, false>(cut, slot, hv, sg, log_decay, scale, dq, lds);
+  else if (whole(sg)) lin_pass<D, true, false, false, true>(cut, slot, hv, sg, log_decay, scale, dv, lds);
+  else lin_pass<D, true, false, false, false>(cut, slot, hv, sg, log_decay, scale, dv, lds);
+}
+
+// Front to back along each sequence's segments (or back to front): a thread
+// carries 4 values of one state, and leaves the end of a sequence of several
+// segments where io says.
+template <int D, bool kBack>
+__global__ __launch_bounds__(64) void lin_join_kernel(LinCut cut, const float* __restrict__ log_decay, StateRef io,
                                                        float* __restrict__ states) {
-  constexpr int kBlocks = D * D / 1024;
+  constexpr int kBlocks = D * D / 256;
   const int piece = blockIdx.x % kBlocks, hv = blockIdx.x / kBlocks % cut.HV;
   const int seq = blockIdx.x / (kBlocks * cut.HV);
   const int bos = min(max(cut.cu[seq], 0), cut.T), eos = min(max(cut.cu[seq + 1], bos), cut.T);
   const int first = bos / cut.S + seq;
   const int n = max((eos - bos + cut.S - 1) / cut.S, 1);
-  const int e = piece * 1024 + threadIdx.x * 4;
-  const StateAt at = state_at(io, seq, hv, cut.HV, D * D);
+  const int e = piece * 256 + threadIdx.x * 4;
+  const StateAt state = state_at(io, seq, hv, cut.HV, D * D);
   const float g2 = decay2(log_decay[hv]);
   f32x4 x = zero4();
-  if (at.from) x = *reinterpret_cast<const f32x4*>(at.from + e);
-  for (int i = 0; i < n; ++i) {
-    const int s = kBack ? n - 1 - i : i;
-    float* p = states + ((size_t)(first + s) * cut.HV + hv) * (D * D) + e;
-    f32x4 add = zero4();
-    if (gathered && i + 1 < n) add = *reinterpret_cast<const f32x4*>(p);
-    *reinterpret_cast<f32x4*>(p) = x;
-    const float d = power(g2, min(cut.S, eos - bos - s * cut.S));
+  if (state.from) x = *reinterpret_cast<const f32x4*>(state.from + e);
+  const int m = n == 1 ? 0 : state.to ? n : n - 1;  // segments whose sums are there
+  auto place = [&](int i) { return states + ((size_t)(first + (kBack ? n - 1 - i : i)) * cut.HV + hv) * (D * D) + e; };
+  constexpr int kAhead = 8;  // segments requested together
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    f32x4 add[kAhead];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] = d * x[r] + add[r];
+    for (int j = 0; j < kAhead; ++j) {
+      add[j] = zero4();
+      if (i0 + j < m) add[j] = *reinterpret_cast<const f32x4*>(place(i0 + j));
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j, s = kBack ? n - 1 - i : i;
+      if (i < n) {
+        *reinterpret_cast<f32x4*>(place(i)) = x;
+        const float d = power(g2, min(cut.S, eos - bos - s * cut.S));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = d * x[r] + add[j][r];
+      }
+    }
   }
+  if (n > 1 && state.to) *reinterpret_cast<f32x4*>(state.to + e) = x;
 }
 
+// out[t][h] = sum over the key head's G value heads of wide[t][h G + i], for
+// dq and dk (blockIdx.y).
 __global__ __launch_bounds__(256) void lin_fold_kernel(int64_t n, int DH, int G, int D,
-                                                       const float* __restrict__ wide, uint16_t* __restrict__ out) {
+                                                       const float* __restrict__ wq, const float* __restrict__ wk,
+                                                       uint16_t* __restrict__ dq, uint16_t* __restrict__ dk) {
+  const float* wide = blockIdx.y ? wk : wq;
+  uint16_t* out = blockIdx.y ? dk : dq;
   // n pieces of 4 outputs; DH = H * D outputs a token
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t e = i * 4, t = e / DH;
@@ -468,70 +718,59 @@ __global__ __launch_bounds__(256) void lin_fold_kernel(int64_t n, int DH, int G,
   }
 }
 
-namespace {
+// D = 128 or 64, and a flag that is a template argument
+#define LIN_LAUNCH1(kernel, f, grid, ...)                                                                \
+  do {                                                                                                   \
+    const dim3 lin_grid(grid), lin_block(2 * D);                                                         \
+    if (D == 128 && (f)) hipLaunchKernelGGL((kernel<128, true>), lin_grid, lin_block, 0, s, __VA_ARGS__);  \
+    else if (D == 128) hipLaunchKernelGGL((kernel<128, false>), lin_grid, lin_block, 0, s, __VA_ARGS__);   \
+    else if (f) hipLaunchKernelGGL((kernel<64, true>), lin_grid, lin_block, 0, s, __VA_ARGS__);            \
+    else hipLaunchKernelGGL((kernel<64, false>), lin_grid, lin_block, 0, s, __VA_ARGS__);                  \
+  } while (0)
 
-template <int D, bool kBack, bool kT, bool kWide>
-hipError_t pass(const LinCut& cut, const float* log_decay, float scale, const LinPass& p, hipStream_t s) {
-  hipLaunchKernelGGL((lin_pass_kernel<D, kBack, kT, kWide>), dim3((unsigned)cut.slots * (unsigned)cut.HV),
-                     dim3(2 * D), 0, s, cut, log_decay, scale, p);
-  return hipGetLastError();
-}
-
-template <int D>
-hipError_t pass_of(LinKind kind, bool wide, const LinCut& cut, const float* log_decay, float scale,
-                   const LinPass& p, hipStream_t s) {
-  switch (kind) {
-    case LinKind::kOut: return pass<D, false, false, false>(cut, log_decay, scale, p, s);
-    case LinKind::kDq:
-      return wide ? pass<D, false, true, true>(cut, log_decay, scale, p, s)
-                  : pass<D, false, true, false>(cut, log_decay, scale, p, s);
-    case LinKind::kDv: return pass<D, true, false, false>(cut, log_decay, scale, p, s);
-    default:
-      return wide ? pass<D, true, true, true>(cut, log_decay, scale, p, s)
-                  : pass<D, true, true, false>(cut, log_decay, scale, p, s);
-  }
-}
-
-}  // namespace
-
-hipError_t launch_lin_pass(LinKind kind, bool wide, int D, const LinCut& cut, const float* log_decay,
-                           float scale, const LinPass& p, hipStream_t s) {
-  return D == 128 ? pass_of<128>(kind, wide, cut, log_decay, scale, p, s)
-                  : pass_of<64>(kind, wide, cut, log_decay, scale, p, s);
-}
-
-hipError_t launch_lin_gather(bool back, int D, const LinCut& cut, const float* log_decay, float scale,
-                             const LinRows& b, const LinRows& c, float* states, hipStream_t s) {
+hipError_t launch_lin_out(int D, const LinCut& cut, const float* log_decay, float scale, const LinPass& p,
+                          hipStream_t s) {
   const dim3 grid((unsigned)cut.slots * (unsigned)cut.HV), block(2 * D);
-  if (D == 128 && back)
-    hipLaunchKernelGGL((lin_gather_kernel<128, true>), grid, block, 0, s, cut, log_decay, scale, b, c, states);
-  else if (D == 128)
-    hipLaunchKernelGGL((lin_gather_kernel<128, false>), grid, block, 0, s, cut, log_decay, scale, b, c, states);
-  else if (back)
-    hipLaunchKernelGGL((lin_gather_kernel<64, true>), grid, block, 0, s, cut, log_decay, scale, b, c, states);
+  if (D == 128)
+    hipLaunchKernelGGL((lin_out_kernel<128>), grid, block, 0, s, cut, log_decay, scale, p);
   else
-    hipLaunchKernelGGL((lin_gather_kernel<64, false>), grid, block, 0, s, cut, log_decay, scale, b, c, states);
+    hipLaunchKernelGGL((lin_out_kernel<64>), grid, block, 0, s, cut, log_decay, scale, p);
   return hipGetLastError();
 }
 
-hipError_t launch_lin_join(bool back, bool gathered, int D, const LinCut& cut, const float* log_decay,
-                           const StateRef& io, float* states, hipStream_t s) {
-  const dim3 grid((unsigned)cut.N * (unsigned)cut.HV * (unsigned)(D * D / 1024)), block(256);
-  if (D == 128 && back)
-    hipLaunchKernelGGL((lin_join_kernel<128, true>), grid, block, 0, s, cut, gathered, log_decay, io, states);
-  else if (D == 128)
-    hipLaunchKernelGGL((lin_join_kernel<128, false>), grid, block, 0, s, cut, gathered, log_decay, io, states);
-  else if (back)
-    hipLaunchKernelGGL((lin_join_kernel<64, true>), grid, block, 0, s, cut, gathered, log_decay, io, states);
-  else
-    hipLaunchKernelGGL((lin_join_kernel<64, false>), grid, block, 0, s, cut, gathered, log_decay, io, states);
+hipError_t launch_lin_grad(int D, bool wide, const LinCut& cut, const float* log_decay, float scale,
+                           const LinPass& dq, const LinPass& dv, const LinPass& dk, hipStream_t s) {
+  LIN_LAUNCH1(lin_grad_kernel, wide, ((unsigned)cut.slots * (unsigned)cut.HV + 7) / 8 * 24, cut, log_decay, scale,
+              dq, dv, dk);
   return hipGetLastError();
 }
 
-hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wide, uint16_t* out, hipStream_t s) {
+hipError_t launch_lin_gather(int D, bool back, const LinCut& cut, const float* log_decay, float scale,
+                             const LinRows& b, const LinRows& c, bool ends, float* states, hipStream_t s) {
+  LIN_LAUNCH1(lin_gather_kernel, back, (unsigned)cut.slots * (unsigned)cut.HV, cut, log_decay, scale, b, c, ends,
+              states);
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_join(int D, bool back, const LinCut& cut, const float* log_decay, const StateRef& io,
+                           float* states, hipStream_t s) {
+  const dim3 grid((unsigned)cut.N * (unsigned)cut.HV * (unsigned)(D * D / 256)), block(64);
+  if (D == 128 && back)
+    hipLaunchKernelGGL((lin_join_kernel<128, true>), grid, block, 0, s, cut, log_decay, io, states);
+  else if (D == 128)
+    hipLaunchKernelGGL((lin_join_kernel<128, false>), grid, block, 0, s, cut, log_decay, io, states);
+  else if (back)
+    hipLaunchKernelGGL((lin_join_kernel<64, true>), grid, block, 0, s, cut, log_decay, io, states);
+  else
+    hipLaunchKernelGGL((lin_join_kernel<64, false>), grid, block, 0, s, cut, log_decay, io, states);
+  return hipGetLastError();
+}
+
+hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wq, const float* wk, uint16_t* dq, uint16_t* dk,
+                           hipStream_t s) {
   const int64_t n = (int64_t)T * H * D / 4;
   const unsigned blocks = (unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
-  hipLaunchKernelGGL(lin_fold_kernel, dim3(blocks), dim3(256), 0, s, n, H * D, G, D, wide, out);
+  hipLaunchKernelGGL(lin_fold_kernel, dim3(blocks, 2), dim3(256), 0, s, n, H * D, G, D, wq, wk, dq, dk);
   return hipGetLastError();
 }
 

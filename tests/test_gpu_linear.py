@@ -286,3 +286,19 @@ def test_the_binding_refuses_what_does_not_fit():
             f()
             print("accepted", i)
     assert not pool.any()
+
+
+def test_the_host_boundaries_change_no_bit():
+    """They only spare launches where no sequence is cut."""
+    for lens in ([256, 200, 1], [700, 3, 257]):
+        x = inputs(lens, 2, 2, 64, seed=12)
+        d = dev(x)
+        want = run(x, d)
+        o, hT, saved = gdn.linear_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["cu"], h0=d["h0"], save_for_backward=True)
+        g = gdn.linear_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["cu"], saved, d["dO"], dhT=d["dhT"])
+        o2, hT2, _ = gdn.linear_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["cu"], h0=d["h0"])
+        o3, none, _ = gdn.linear_fwd(d["q"], d["k"], d["v"], d["log_decay"], d["cu"], h0=d["h0"], output_final_state=False)
+        g2 = gdn.linear_bwd(d["q"], d["k"], d["v"], d["log_decay"], d["cu"], saved, d["dO"], dhT=d["dhT"], want_dh0=False)
+        assert all(torch.equal(want[n], y) for n, y in dict(o=o, hT=hT, **g).items())
+        assert torch.equal(o2, o) and torch.equal(hT2, hT) and torch.equal(o3, o) and none is None
+        assert all(torch.equal(g2[n], g[n]) for n in ("dq", "dk", "dv")) and g2["dh0"] is None
