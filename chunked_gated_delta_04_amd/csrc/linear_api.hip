@@ -257,7 +257,7 @@ GDN_API int gdn_linear_step(const gdn_linear_problem* p, const uint16_t* q, cons
                             void* stream) {
   gdn_status st = check_linear(p);
   if (st != GDN_OK) return st;
-  if (p->T != p->N || slots < 0 || (int64_t)p->N * p->HV > kMaxBlocks) return GDN_ERR_SHAPE;
+  if (p->T != p->N || slots < 0 || (int64_t)p->N * p->HV * 4 > kMaxBlocks) return GDN_ERR_SHAPE;
   st = check_token_args(p, q, k, v, log_decay, o);
   if (st != GDN_OK) return st;
   if (p->N > 0 && (!state_pool || !ssm_state_indices)) return GDN_ERR_NULL;

@@ -64,21 +64,28 @@ __device__ __forceinline__ void load_at(const T* row, int c, int D, float* x) {
     for (int i = 0; i < V; ++i) x[i] = 0.f;
 }
 
-// e4m3 of v, to nearest even; NaN stays
-__device__ __forceinline__ float into_range(float v) {
-  const float c = __builtin_amdgcn_fmed3f(v, -kE4m3Max, kE4m3Max);
-  return v != v ? v : c;
+// 448 a / m as a division rounds it, from r = 448 / m: the remainder of a first
+// quotient, exact by fma, corrects it. bf16 and fp16 rows give quotients that lie
+// exactly between two e4m3 values, which a quotient off by one fp32 step would round
+// to the wrong one. At most 448 for |a| <= m.
+__device__ __forceinline__ float quotient(float a, float m, float r, float rm) {
+  const float q = a * r;
+  const float p = q * m;
+  const float rem = fmaf(a, kE4m3Max, -p) - fmaf(q, m, -p);
+  const float c = fmaf(rem, rm, q);
+  return c == c ? c : q;  // m infinite: the remainder is no number
 }
+// e4m3 of values of at most 448 in magnitude, to nearest even; NaN stays
 template <int V>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float* x) {
   if constexpr (V == 1) {
-    *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(into_range(x[0]), 0.f, 0, false);
+    *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[0], 0.f, 0, false);
   } else {
     uint32_t w[V / 4];
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-      int u = __builtin_amdgcn_cvt_pk_fp8_f32(into_range(x[4 * i]), into_range(x[4 * i + 1]), 0, false);
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(into_range(x[4 * i + 2]), into_range(x[4 * i + 3]), u, true);
+      int u = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
+      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], u, true);
     }
     if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
@@ -119,68 +126,70 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
   sum = reduce_row<GROUP, false>(sum, part[0]);
   const float rstd = 1.f / sqrtf(sum / (float)D + a.eps);
   if (a.rstd && on && t == 0) a.rstd[row] = rstd;
+  // v <- s (weight + unit); y is that times rstd
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = column<V, GROUP>(p, t);
-    float w[V];
-    if (a.weight) load_at<T, V>(static_cast<const T*>(a.weight), c, D, w);
+    if (a.weight) {
+      float w[V];
+      load_at<T, V>(static_cast<const T*>(a.weight), c, D, w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[p][i] *= a.weight ? rstd * (w[i] + a.unit) : rstd;
-    if (a.y && on && c < D) store_n<T, V>(static_cast<T*>(a.y) + row * D + c, v[p]);
+      for (int i = 0; i < V; ++i) v[p][i] *= w[i] + a.unit;
+    }
+    if (a.y && on && c < D) {
+      float y[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = v[p][i] * rstd;
+      store_n<T, V>(static_cast<T*>(a.y) + row * D + c, y);
+    }
   }
   if (!a.y8) return;
+  // Scales from the largest |v| of their columns: rstd cancels in y / scale, so
+  // the quotients are formed from v (products of two short numbers, exact where x
+  // has 16 bits) and only the scale itself takes rstd.
   float top[P];  // of each piece
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     top[p] = 0.f;
+    if (rstd > 0.f) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) top[p] = nmax(top[p], fabsf(v[p][i]));
-  }
-  if (a.group == D) {
-    float m = 0.f;
+      for (int i = 0; i < V; ++i) top[p] = fmaxf(top[p], fabsf(v[p][i]));
+    } else {  // infinities or NaN among the row (or a sum past fp32): y's own largest, NaN if one is
 #pragma unroll
-    for (int p = 0; p < P; ++p) m = nmax(m, top[p]);
-    m = nmax(reduce_row<GROUP, true>(m, part[1]), kTiny);
-    const float scale = m / kE4m3Max;
-    if (on && t == 0) a.scales[row] = scale;
-#pragma unroll
-    for (int p = 0; p < P; ++p) top[p] = scale;
-  } else {
-    const int groups = (D + 127) / 128;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int c = column<V, GROUP>(p, t);
-      float m;
-      if constexpr (V > 1) {
-        constexpr int L = 128 / V;  // lanes of 128 columns
-        if constexpr (GROUP >= L) m = reduce_lanes<L, true>(top[p]);
-        else {  // the row's threads hold 128 columns in several pieces
-          m = top[0];
-#pragma unroll
-          for (int r = 1; r < P; ++r) m = nmax(m, top[r]);
-          m = reduce_lanes<GROUP, true>(m);
-        }
-      } else if constexpr (GROUP < 64) {
-        m = top[0];
-#pragma unroll
-        for (int r = 1; r < P; ++r) m = nmax(m, top[r]);
-        m = reduce_lanes<GROUP, true>(m);
-      } else {
-        m = reduce_lanes<64, true>(nmax(top[p & ~1], top[p | 1]));
-      }
-      m = nmax(m, kTiny) / kE4m3Max;
-      if (on && c < D && c % 128 == 0) a.scales[row * groups + c / 128] = m;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[p][i] /= m;
+      for (int i = 0; i < V; ++i) top[p] = nmax(top[p], fabsf(v[p][i] * rstd));
     }
+  }
+  const float up = rstd > 0.f ? rstd : 1.f;
+  const float least = kTiny / up;
+  const int groups = (D + 127) / 128;
+  float whole = 0.f;
+  if (a.group == D) {
+#pragma unroll
+    for (int p = 0; p < P; ++p) whole = nmax(whole, top[p]);
+    whole = nmax(reduce_row<GROUP, true>(whole, part[1]), least);
+    if (on && t == 0) a.scales[row] = whole * up / kE4m3Max;
   }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = column<V, GROUP>(p, t);
-    if (a.group == D) {
+    float m = whole;
+    if (a.group != D) {
+      if constexpr (V > 1 && GROUP >= 128 / V) {
+        m = reduce_lanes<128 / V, true>(top[p]);
+      } else if constexpr (V == 1 && GROUP >= 64) {
+        m = reduce_lanes<64, true>(nmax(top[p & ~1], top[p | 1]));
+      } else {  // the row's threads hold its 128 columns or fewer in several pieces
+        m = top[0];
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[p][i] /= top[p];
+        for (int r = 1; r < P; ++r) m = nmax(m, top[r]);
+        m = reduce_lanes<GROUP, true>(m);
+      }
+      m = nmax(m, least);
+      if (on && c < D && c % 128 == 0) a.scales[row * groups + c / 128] = m * up / kE4m3Max;
     }
+    const float r = kE4m3Max / m, rm = 1.f / m;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[p][i] = quotient(rstd > 0.f ? v[p][i] : v[p][i] * rstd, m, r, rm);
     if (on && c < D) store_e4m3<V>(a.y8 + row * D + c, v[p]);
   }
 }
@@ -191,15 +200,19 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
   __shared__ float part[2][GROUP > 64 ? GROUP / 64 : 1];
   const int t = threadIdx.x % GROUP, D = a.D;
   const int first = blockIdx.x * kRows + threadIdx.x / GROUP;  // this group's first row; it takes every step-th
+  // the weights stay in registers, but for 1024 threads, which have too few
+  constexpr bool kHold = GROUP < 1024;
   float w[P][V], acc[P][V];
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
+  auto weights = [&](int p) {
     if (a.weight) load_at<T, V>(static_cast<const T*>(a.weight), column<V, GROUP>(p, t), D, w[p]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[p][i] = a.weight ? w[p][i] + a.unit : 1.f;
-      acc[p][i] = 0.f;
-    }
+    for (int i = 0; i < V; ++i) w[p][i] = a.weight ? w[p][i] + a.unit : 1.f;
+  };
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    if (kHold) weights(p);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[p][i] = 0.f;
   }
   int odd = 0;
   for (int base = blockIdx.x * kRows; base < a.rows; base += step, odd ^= 1) {
@@ -214,6 +227,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
       const int c = column<V, GROUP>(p, t);
       load_at<T, V>(s, c, D, n[p]);
       load_at<T, V>(dy, c, D, g[p]);
+      if (!kHold) weights(p);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         n[p][i] *= rstd;
@@ -245,19 +259,31 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
   }
 }
 
-// dweight[c] = sum of the partials' column c: 4 threads a column, in a fixed order
-__global__ __launch_bounds__(256) void rmsnorm_fold_kernel(int n, int D, const float* __restrict__ partial,
-                                                           float* __restrict__ dweight) {
-  __shared__ float sums[16][17];
-  const int l = threadIdx.x & 15, part = threadIdx.x >> 4, c = blockIdx.x * 16 + l;
+// dweight[c] = sum of the partials' column c: 32 threads a column, each every
+// 32nd partial in order, then the 32 sums in order.
+__global__ __launch_bounds__(1024) void rmsnorm_fold_kernel(int n, int D, const float* __restrict__ partial,
+                                                            float* __restrict__ dweight) {
+  constexpr int kCols = 32, kParts = 1024 / kCols, kAhead = 8;
+  __shared__ float sums[kParts][kCols + 1];
+  const int l = threadIdx.x % kCols, part = threadIdx.x / kCols, c = blockIdx.x * kCols + l;
   float s = 0.f;
-  if (c < D)
-    for (int i = part; i < n; i += 16) s += partial[(int64_t)i * D + c];
+  if (c < D) {
+    for (int i0 = part; i0 < n; i0 += kParts * kAhead) {
+      float x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kParts;
+        x[j] = i < n ? partial[(int64_t)i * D + c] : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) s += x[j];
+    }
+  }
   sums[part][l] = s;
   __syncthreads();
   if (part == 0 && c < D) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += sums[i][l];
+    for (int i = 1; i < kParts; ++i) s += sums[i][l];
     dweight[c] = s;
   }
 }
@@ -274,8 +300,11 @@ Shape shape_of(int D) {
   if (D <= 1024) return {64, 16};
   if (D <= 2048) return {256, 8};
   if (D <= 4096) return {256, 16};
-  if (D <= 8192) return {256, 32};
-  return {512, 32};
+  if (D <= 5120) return {320, 16};
+  if (D <= 6144) return {384, 16};
+  if (D <= 8192) return {512, 16};
+  if (D <= 12288) return {768, 16};
+  return {1024, 16};
 }
 int rows_at_once(int D) {
   const int g = shape_of(D).group;
@@ -290,8 +319,11 @@ hipError_t with_shape(int D, F&& f) {
     case 1024: return f.template operator()<T, V, 64, 16>();
     case 2048: return f.template operator()<T, V, 256, 8>();
     case 4096: return f.template operator()<T, V, 256, 16>();
-    case 8192: return f.template operator()<T, V, 256, 32>();
-    default: return f.template operator()<T, V, 512, 32>();
+    case 5120: return f.template operator()<T, V, 320, 16>();
+    case 6144: return f.template operator()<T, V, 384, 16>();
+    case 8192: return f.template operator()<T, V, 512, 16>();
+    case 12288: return f.template operator()<T, V, 768, 16>();
+    default: return f.template operator()<T, V, 1024, 16>();
   }
 }
 template <typename F>
@@ -304,7 +336,7 @@ hipError_t with_type(Elem type, bool wide, int D, F&& f) {
 }
 
 int64_t blocks_of(int rows, int D) { return ((int64_t)rows + rows_at_once(D) - 1) / rows_at_once(D); }
-constexpr int kBwdBlocks = 1024;
+constexpr int kBwdBlocks = 1024;  // 16384 x 4096 rows: 109 us, and 120 with 768, 158 with 512
 
 struct Fwd {
   const NormArgs& a;
@@ -345,7 +377,7 @@ hipError_t launch_rmsnorm_bwd(Elem type, bool wide, const NormGradArgs& a, hipSt
     if (e != hipSuccess) return e;
   }
   if (a.dweight) {
-    hipLaunchKernelGGL(rmsnorm_fold_kernel, dim3((a.D + 15) / 16), dim3(256), 0, s, norm_partials(a.rows, a.D), a.D,
+    hipLaunchKernelGGL(rmsnorm_fold_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, s, norm_partials(a.rows, a.D), a.D,
                        a.partial, a.dweight);
     return hipGetLastError();
   }

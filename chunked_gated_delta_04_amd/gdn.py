@@ -632,7 +632,7 @@ def _dev(t, shape, dtype, name, dev):
     """Device pointer of a contiguous tensor of this shape on this device (None -> NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
@@ -646,14 +646,14 @@ def _dev(t, shape, dtype, name, dev):
 def _rows(t, dtype, name, dev):
     """Device pointer and token stride (0: dense) of a [tokens, heads, columns] tensor whose heads
     are dense rows: a tensor of its own or a slice of a wider buffer's rows."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     n, h, d = t.shape
     sn, sh, sd = t.stride()
-    if n == 0:
-        return None, 0
     if (sd != 1 and d > 1) or (sh != d and h > 1) or (sn < h * d and n > 1):
         raise ValueError(f"{name} must have dense heads and tokens apart, got strides {t.stride()}")
     return t.data_ptr(), sn if n > 1 and sn != h * d else 0
@@ -665,30 +665,24 @@ def _on_device(t, name):
     return t.device
 
 
-class _Run:
-    """The device and stream of a call: `stream` (a torch stream or a raw handle), or the device's
-    current one. Inside it, both are current."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, dev, stream):
-        self.dev, self.more = dev, None
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.handle = (stream or torch.cuda.current_stream(dev)).cuda_stream
-        if stream is not None:
-            self.more = torch.cuda.stream(stream)
-        elif dev.index != torch.cuda.current_device():
-            self.more = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self.more is not None:
-            self.more.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.more is not None:
-            self.more.__exit__(*exc)
+def _on_stream(dev, stream, call):
+    """call(stream handle) with the tensors' device current, on `stream` (a torch stream or a raw
+    handle), which is then current too, or by default on the device's current stream."""
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return call(_raw_stream(dev.index))
+        with torch.cuda.device(dev):
+            return call(_raw_stream(dev.index))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 # ---------------------------------------------------------------- linear attention
@@ -699,17 +693,15 @@ def make_linear_problem(N, T, H, HV, D, cu_seqlens=None, cu_seqlens_host=None, s
                         q_stride=0, k_stride=0, v_stride=0):
     """Build the gdn_linear_problem descriptor (K = V = D). cu_seqlens: int32 device tensor [N+1];
     cu_seqlens_host: optional int32 CPU tensor [N+1] (both kept alive by the caller)."""
-    p = GdnLinearProblem()
-    p.N, p.T, p.H, p.HV, p.K, p.V, p.scale = N, T, H, HV, D, D, scale
-    p.q_stride, p.k_stride, p.v_stride = q_stride, k_stride, v_stride
+    cu = host = None
     if cu_seqlens is not None:
-        p.cu_seqlens = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens",
-                            _on_device(cu_seqlens, "cu_seqlens"))
+        cu = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens",
+                  _on_device(cu_seqlens, "cu_seqlens"))
     if cu_seqlens_host is not None:
         if cu_seqlens_host.numel() != N + 1:
             raise ValueError(f"cu_seqlens_host must hold {N + 1} boundaries")
-        p.cu_seqlens_host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
-    return p
+        host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
+    return GdnLinearProblem(N, T, H, HV, D, D, scale, cu, host, q_stride, k_stride, v_stride)
 
 
 def gdn_linear_saved_size(problem):
@@ -757,6 +749,10 @@ def _buffer(t, name, dev):
     return t.data_ptr()
 
 
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
 def _alloc_bytes(n, dev):
     return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
 
@@ -771,16 +767,17 @@ def linear_fwd(q, k, v, log_decay, cu_seqlens, h0=None, scale=0.0, cu_seqlens_ho
     dev, p, ptrs = _linear_call(q, k, v, log_decay, cu_seqlens, cu_seqlens_host, scale)
     N, T, HV, D = p.N, p.T, p.HV, p.K
     h0p = _dev(h0, (N, HV, D, D), _f32, "h0", dev)
-    with _Run(dev, stream) as s:
+
+    def call(s):
         o = torch.empty(T, HV, D, dtype=_bf16, device=dev)
         hT = torch.empty(N, HV, D, D, dtype=_f32, device=dev) if output_final_state else None
         saved = _alloc_bytes(gdn_linear_saved_size(p), dev) if save_for_backward else None
         ws = None if save_for_backward else _alloc_bytes(gdn_linear_fwd_workspace_size(p), dev)
-        st = _lib.gdn_linear_fwd(ctypes.byref(p), *ptrs, h0p, o.data_ptr(),
-                                 _buffer(hT, "hT", dev), _buffer(saved, "saved", dev),
-                                 _buffer(ws, "workspace", dev), _bytes(ws), s)
-    _check(st, "gdn_linear_fwd")
-    return o, hT, saved
+        _check(_lib.gdn_linear_fwd(ctypes.byref(p), *ptrs, h0p, o.data_ptr(), _at(hT), _at(saved),
+                                   _at(ws), _bytes(ws), s), "gdn_linear_fwd")
+        return o, hT, saved
+
+    return _on_stream(dev, stream, call)
 
 
 def linear_fwd_paged(q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indices,
@@ -797,15 +794,16 @@ def linear_fwd_paged(q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indic
             _dev(ssm_state_indices, (N,), torch.int32, "ssm_state_indices", dev),
             _dev(has_initial_state, (N,), torch.int32, "has_initial_state", dev),
             _host_ptr(indices_host, "indices_host"))
-    with _Run(dev, stream) as s:
+
+    def call(s):
         o = torch.empty(T, HV, D, dtype=_bf16, device=dev)
         saved = _alloc_bytes(gdn_linear_saved_size(p), dev) if save_for_backward else None
         ws = None if save_for_backward else _alloc_bytes(gdn_linear_fwd_workspace_size(p), dev)
-        st = _lib.gdn_linear_fwd_paged(ctypes.byref(p), *ptrs, *more, o.data_ptr(),
-                                       _buffer(saved, "saved", dev),
-                                       _buffer(ws, "workspace", dev), _bytes(ws), s)
-    _check(st, "gdn_linear_fwd_paged")
-    return o, saved
+        _check(_lib.gdn_linear_fwd_paged(ctypes.byref(p), *ptrs, *more, o.data_ptr(), _at(saved),
+                                         _at(ws), _bytes(ws), s), "gdn_linear_fwd_paged")
+        return o, saved
+
+    return _on_stream(dev, stream, call)
 
 
 def linear_bwd(q, k, v, log_decay, cu_seqlens, saved, dO, dhT=None, scale=0.0,
@@ -819,16 +817,18 @@ def linear_bwd(q, k, v, log_decay, cu_seqlens, saved, dO, dhT=None, scale=0.0,
                          f"{gdn_linear_saved_size(p)} (gdn_linear_saved_size)")
     more = (_buffer(saved, "saved", dev), _dev(dO, (T, HV, D), _bf16, "dO", dev),
             _dev(dhT, (N, HV, D, D), _f32, "dhT", dev))
-    with _Run(dev, stream) as s:
+
+    def call(s):
         dq, dk = (torch.empty(T, H, D, dtype=_bf16, device=dev) for _ in range(2))
         dv = torch.empty(T, HV, D, dtype=_bf16, device=dev)
         dh0 = torch.empty(N, HV, D, D, dtype=_f32, device=dev) if want_dh0 else None
         ws = _alloc_bytes(gdn_linear_bwd_workspace_size(p), dev)
-        st = _lib.gdn_linear_bwd(ctypes.byref(p), *ptrs, *more, dq.data_ptr(), dk.data_ptr(),
-                                 dv.data_ptr(), _buffer(dh0, "dh0", dev),
-                                 _buffer(ws, "workspace", dev), _bytes(ws), s)
-    _check(st, "gdn_linear_bwd")
-    return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
+        _check(_lib.gdn_linear_bwd(ctypes.byref(p), *ptrs, *more, dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), _at(dh0), _at(ws), _bytes(ws), s),
+               "gdn_linear_bwd")
+        return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
+
+    return _on_stream(dev, stream, call)
 
 
 def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=None, scale=0.0,
@@ -843,11 +843,14 @@ def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=
     more = (_dev(state_pool, (slots, HV, D, D), _f32, "state_pool", dev), slots,
             _dev(ssm_state_indices, (N,), torch.int32, "ssm_state_indices", dev),
             _host_ptr(indices_host, "indices_host"))
-    with _Run(dev, stream) as s:
+
+    def call(s):
         o = torch.empty(N, HV, D, dtype=_bf16, device=dev)
-        st = _lib.gdn_linear_step(ctypes.byref(p), *ptrs, *more, o.data_ptr(), s)
-    _check(st, "gdn_linear_step")
-    return o
+        _check(_lib.gdn_linear_step(ctypes.byref(p), *ptrs, *more, o.data_ptr(), s),
+               "gdn_linear_step")
+        return o
+
+    return _on_stream(dev, stream, call)
 
 
 # ---------------------------------------------------------------- rotary positions and the norm
@@ -874,42 +877,46 @@ def _rotary(call, q, k, inv_freq, positions, cu_seqlens, offsets, cu_seqlens_hos
             mscale, q_out, k_out, stream, back):
     dev = _on_device(q, "q")
     T, HQ, D = q.shape
-    p = GdnRotaryProblem()
-    p.T, p.HQ, p.D, p.R = T, HQ, D, 2 * inv_freq.numel()
-    p.dtype, p.interleaved, p.mscale = _elem(q, "q"), bool(interleaved), mscale
-    if k is not None and (k.shape[0] != T or k.shape[2] != D):
-        raise ValueError(f"k must be [{T}, HK, {D}], got {tuple(k.shape)}")
-    p.HK = k.shape[1] if k is not None else 0
+    HK = 0
+    if k is not None:
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"k must be [{T}, HK, {D}], got {tuple(k.shape)}")
+        HK = k.shape[1]
+    pos = cu = host = off = None
+    N = 0
     if positions is not None:
-        p.positions = _dev(positions, (T,), torch.int32, "positions", dev)
+        pos = _dev(positions, (T,), torch.int32, "positions", dev)
     elif cu_seqlens is None:
         raise ValueError("positions or cu_seqlens are needed")
     else:
-        N = p.N = cu_seqlens.numel() - 1
-        p.cu_seqlens = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", dev)
-        p.offsets = _dev(offsets, (N,), torch.int32, "offsets", dev)
+        N = cu_seqlens.numel() - 1
+        cu = _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", dev)
+        off = _dev(offsets, (N,), torch.int32, "offsets", dev)
         if cu_seqlens_host is not None:
             if cu_seqlens_host.numel() != N + 1:
                 raise ValueError(f"cu_seqlens_host must hold {N + 1} boundaries")
-            p.cu_seqlens_host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
+            host = _host_ptr(cu_seqlens_host, "cu_seqlens_host")
+    p = GdnRotaryProblem(T, HQ, HK, D, 2 * inv_freq.numel(), bool(interleaved), _elem(q, "q"),
+                         mscale, pos, N, cu, host, off)
     freq = _dev(inv_freq, (inv_freq.numel(),), _f32, "inv_freq", dev)
     qp, qs = _rows(q, q.dtype, "q", dev)
     kp, ks = _rows(k, q.dtype, "k", dev) if k is not None else (None, 0)
-    with _Run(dev, stream) as s:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        if q_out.shape != q.shape or (k is not None and k_out.shape != k.shape):
+
+    def launch(s):
+        qr = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+        kr = torch.empty(k.shape, dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
+        if qr.shape != q.shape or (k is not None and kr.shape != k.shape):
             raise ValueError("q_out and k_out must have the shapes of q and k")
-        qo, qos = _rows(q_out, q.dtype, "q_out", dev)
-        ko, kos = _rows(k_out, q.dtype, "k_out", dev) if k is not None else (None, 0)
+        qo, qos = _rows(qr, q.dtype, "q_out", dev)
+        ko, kos = _rows(kr, q.dtype, "k_out", dev) if k is not None else (None, 0)
         if back:
             p.q_out_stride, p.k_out_stride, p.q_stride, p.k_stride = qs, ks, qos, kos
         else:
             p.q_stride, p.k_stride, p.q_out_stride, p.k_out_stride = qs, ks, qos, kos
-        st = call(ctypes.byref(p), freq, qp, kp, qo, ko, s)
-    return st, q_out, k_out
+        _check(call(ctypes.byref(p), freq, qp, kp, qo, ko, s), "gdn_rotary_bwd" if back else "gdn_rotary")
+        return qr, kr if k is not None else None
+
+    return _on_stream(dev, stream, launch)
 
 
 def rotary(q, k, inv_freq, positions=None, cu_seqlens=None, offsets=None, cu_seqlens_host=None,
@@ -918,34 +925,30 @@ def rotary(q, k, inv_freq, positions=None, cu_seqlens=None, offsets=None, cu_seq
     dense or slices of a wider buffer's rows; inv_freq [R / 2] fp32. Positions [T] int32, or each
     token's place in its sequence by cu_seqlens [N+1] plus offsets [N]. q_out, k_out: where the
     results go (q and k themselves: in place), by default new tensors. Returns (q_out, k_out)."""
-    st, qo, ko = _rotary(_lib.gdn_rotary, q, k, inv_freq, positions, cu_seqlens, offsets,
-                         cu_seqlens_host, interleaved, mscale, q_out, k_out, stream, False)
-    _check(st, "gdn_rotary")
-    return qo, ko
+    return _rotary(_lib.gdn_rotary, q, k, inv_freq, positions, cu_seqlens, offsets,
+                   cu_seqlens_host, interleaved, mscale, q_out, k_out, stream, False)
 
 
 def rotary_bwd(dq_out, dk_out, inv_freq, positions=None, cu_seqlens=None, offsets=None,
                cu_seqlens_host=None, interleaved=False, mscale=1.0, dq=None, dk=None, stream=None):
     """Gradients of rotary (gdn_rotary_bwd): (dq, dk) from those of its outputs."""
-    st, qo, ko = _rotary(_lib.gdn_rotary_bwd, dq_out, dk_out, inv_freq, positions, cu_seqlens,
-                         offsets, cu_seqlens_host, interleaved, mscale, dq, dk, stream, True)
-    _check(st, "gdn_rotary_bwd")
-    return qo, ko
+    return _rotary(_lib.gdn_rotary_bwd, dq_out, dk_out, inv_freq, positions, cu_seqlens,
+                   offsets, cu_seqlens_host, interleaved, mscale, dq, dk, stream, True)
 
 
 def _norm_rows(t, dtype, shape, name, dev):
     """Pointer and row stride (0: dense) of a [rows, D] tensor whose rows are dense."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
     rows, D = shape
-    if rows == 0:
-        return None, 0
     sr, sd = t.stride()
     if (sd != 1 and D > 1) or (sr < D and rows > 1):
         raise ValueError(f"{name} must have dense rows apart, got strides {t.stride()}")
@@ -954,9 +957,7 @@ def _norm_rows(t, dtype, shape, name, dev):
 
 def _norm_problem(x, weight, unit_offset, eps, group, dev):
     rows, D = x.shape
-    p = GdnRmsnormProblem()
-    p.rows, p.D, p.dtype, p.eps = rows, D, _elem(x, "x"), eps
-    p.unit_offset, p.group = bool(unit_offset), group
+    p = GdnRmsnormProblem(rows, D, _elem(x, "x"), bool(unit_offset), group, eps, 0, 0)
     return p, _dev(weight, (D,), x.dtype, "weight", dev)
 
 
@@ -973,27 +974,32 @@ def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-6, unit_offset=False, quan
     p, wp = _norm_problem(x, weight, unit_offset, eps, 128 if quant == 128 else 0, dev)
     xp, p.x_stride = _norm_rows(x, x.dtype, (rows, D), "x", dev)
     rp, p.residual_stride = _norm_rows(residual, x.dtype, (rows, D), "residual", dev)
-    want_y = quant is None if want_y is None else want_y
-    if not want_y and quant is None:
+    if want_y is False and quant is None:
         raise ValueError("nothing to compute: want_y is False and quant is None")
-    out = {}
-    with _Run(dev, stream) as s:
+
+    def call(s):
+        out = {}
+        so = y = y8 = scales = r = None
         if residual is not None:
-            out["residual_out"] = torch.empty(rows, D, dtype=x.dtype, device=dev) if residual_out is None else residual_out
-        if want_y:
-            out["y"] = torch.empty(rows, D, dtype=x.dtype, device=dev)
+            t = torch.empty(rows, D, dtype=x.dtype, device=dev) if residual_out is None else residual_out
+            out["residual_out"], so = t, _dev(t, (rows, D), x.dtype, "residual_out", dev)
+        if want_y or quant is None:
+            t = out["y"] = torch.empty(rows, D, dtype=x.dtype, device=dev)
+            y = t.data_ptr()
         if quant is not None:
-            out["y8"] = torch.empty(rows, D, dtype=torch.float8_e4m3fn, device=dev)
+            t = out["y8"] = torch.empty(rows, D, dtype=torch.float8_e4m3fn, device=dev)
+            y8 = t.data_ptr()
             shape = (rows,) if quant == "row" else (rows, (D + 127) // 128)
-            out["scales"] = torch.empty(shape, dtype=_f32, device=dev)
+            t = out["scales"] = torch.empty(shape, dtype=_f32, device=dev)
+            scales = t.data_ptr()
         if want_rstd:
-            out["rstd"] = torch.empty(rows, dtype=_f32, device=dev)
-        get = lambda n: out[n].data_ptr() if n in out else None  # noqa: E731
-        so = _dev(out.get("residual_out"), (rows, D), x.dtype, "residual_out", dev)
-        st = _lib.gdn_rmsnorm_fwd(ctypes.byref(p), xp, rp, wp, so, get("y"), get("y8"),
-                                  get("scales"), get("rstd"), s)
-    _check(st, "gdn_rmsnorm_fwd")
-    return out
+            t = out["rstd"] = torch.empty(rows, dtype=_f32, device=dev)
+            r = t.data_ptr()
+        _check(_lib.gdn_rmsnorm_fwd(ctypes.byref(p), xp, rp, wp, so, y, y8, scales, r, s),
+               "gdn_rmsnorm_fwd")
+        return out
+
+    return _on_stream(dev, stream, call)
 
 
 def gdn_rmsnorm_bwd_workspace_size(problem):
@@ -1012,12 +1018,13 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual_out=None, unit_offset=False, want
     dsp = _dev(dresidual_out, (rows, D), dy.dtype, "dresidual_out", dev)
     rp = _dev(rstd, (rows,), _f32, "rstd", dev)
     want_dweight = weight is not None if want_dweight is None else want_dweight
-    with _Run(dev, stream) as st_:
+
+    def call(stream_):
         dx = torch.empty(rows, D, dtype=dy.dtype, device=dev)
         dw = torch.empty(D, dtype=_f32, device=dev) if want_dweight else None
         ws = _alloc_bytes(gdn_rmsnorm_bwd_workspace_size(p), dev) if want_dweight else None
-        st = _lib.gdn_rmsnorm_bwd(ctypes.byref(p), sp, wp, rp, dyp, dsp, dx.data_ptr(),
-                                  _buffer(dw, "dweight", dev), _buffer(ws, "workspace", dev),
-                                  _bytes(ws), st_)
-    _check(st, "gdn_rmsnorm_bwd")
-    return dict(dx=dx, dweight=dw)
+        _check(_lib.gdn_rmsnorm_bwd(ctypes.byref(p), sp, wp, rp, dyp, dsp, dx.data_ptr(), _at(dw),
+                                    _at(ws), _bytes(ws), stream_), "gdn_rmsnorm_bwd")
+        return dict(dx=dx, dweight=dw)
+
+    return _on_stream(dev, stream, call)

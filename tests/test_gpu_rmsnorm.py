@@ -167,3 +167,35 @@ def test_the_binding_refuses_what_does_not_fit():
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("quant", ["row", 128])
+def test_e4m3_ties_go_to_even(dtype, quant):
+    """Whole numbers whose scaled values lie exactly between two e4m3 values (7 x 6 = 42 between 40 and 44): the division's
+    fp32 rounding decides none of them, whatever the row's norm."""
+    gen = torch.Generator().manual_seed(8)
+    for top in (64, 112, 100, 37):
+        x = torch.randint(-top, top + 1, (64, 640), generator=gen).to(dtype)
+        x[:, ::128] = top
+        w = torch.full((640,), 0.75, dtype=dtype)
+        out = gdn.rmsnorm_fwd(x.cuda(), w.cuda(), quant=quant)
+        v = torch.from_numpy(f64(x) * 448 / top)
+        want = v.to(torch.float32)
+        exact = want.double() == v  # representable quotients, the ties among them
+        assert torch.equal(out["y8"].cpu().float()[exact], want.to(torch.float8_e4m3fn).float()[exact])
+        assert exact.float().mean() > 0.01
+
+
+def test_overflowing_and_tiny_rows():
+    x = torch.zeros(4, 256, device="cuda")
+    x[0] = 1e30                # the sum of squares is past fp32: y is zero
+    x[1, 3] = 1e-30            # eps rules
+    x[2, :128], x[2, 128:] = 1.0, 1e-30
+    out = gdn.rmsnorm_fwd(x, quant=128, want_y=True, eps=1e-6)
+    assert not out["y"][0].any() and not out["y8"][0].float().any()
+    y, _ = Y.rmsnorm(f64(x)[1:], None)
+    sc = Y.scales(y, 128)
+    assert np.allclose(f64(out["scales"])[1:], sc, rtol=2.0 ** -18, atol=0)
+    assert bool((out["y8"][1].float()[[3]] == 448).all()) or y[0, 3] < 2.0 ** -100
+    assert bool((out["y8"][2].float()[:128] == 448).all()) and bool(out["y8"].float().isfinite().all())
