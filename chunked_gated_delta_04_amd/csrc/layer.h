@@ -102,6 +102,8 @@ struct NormGradArgs {
   void* dx;
   float *dweight, *partial;  // partial: [norm_partials, D], or null without dweight
 };
+// threads of the forward's launch
+int64_t norm_threads(int rows, int D);
 // row groups that each sum one partial of dweight
 int norm_partials(int rows, int D);
 hipError_t launch_rmsnorm_bwd(Elem type, bool wide, const NormGradArgs& a, hipStream_t s);

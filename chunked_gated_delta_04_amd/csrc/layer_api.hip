@@ -15,6 +15,7 @@ using namespace gdn;
 namespace {
 
 constexpr int kRotaryMaxD = 1024;
+constexpr int kRotaryMaxT = 1 << 25;
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
 
 int size_of(int dtype) { return dtype == GDN_FP32 ? 4 : 2; }
@@ -33,6 +34,7 @@ gdn_status check_rotary(const gdn_rotary_problem* p) {
   if (bad_stride(p->q_stride, dq) || bad_stride(p->q_out_stride, dq) || bad_stride(p->k_stride, dk) ||
       bad_stride(p->k_out_stride, dk))
     return GDN_ERR_SHAPE;
+  if (p->T > kRotaryMaxT) return GDN_ERR_SHAPE;  // threads of one launch
   if (!p->positions) {
     if (p->N == 0 && p->T != 0) return GDN_ERR_SHAPE;
     if (p->cu_seqlens_host) {
@@ -87,6 +89,7 @@ gdn_status check_norm(const gdn_rmsnorm_problem* p) {
       (p->unit_offset != 0 && p->unit_offset != 1))
     return GDN_ERR_UNSUPPORTED;
   if (bad_stride(p->x_stride, p->D) || bad_stride(p->residual_stride, p->D)) return GDN_ERR_SHAPE;
+  if (norm_threads(p->rows, p->D) >= (int64_t)1 << 32) return GDN_ERR_SHAPE;  // of one launch
   return GDN_OK;
 }
 

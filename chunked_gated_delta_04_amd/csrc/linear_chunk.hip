@@ -123,8 +123,8 @@ struct RowRegs {
   __device__ __forceinline__ void load(int i, __amdgpu_buffer_rsrc_t rows, int lane_byte, int step_bytes) {
     x[i] = load_b128(rows, lane_byte + i * step_bytes);
   }
-  static __device__ __forceinline__ int lane_byte(int64_t stride, int tid) {
-    return (int)(tid / (D / 8) * stride * 2) + tid % (D / 8) * 16;
+  static __device__ __forceinline__ int lane_byte(int stride, int tid) {
+    return tid / (D / 8) * stride * 2 + tid % (D / 8) * 16;
   }
   __device__ __forceinline__ void store(uint16_t* tile, int tid) const {
     const int off = at<D>(tid / (D / 8), tid % (D / 8) * 8);  // kRows is a multiple of 16
@@ -140,9 +140,9 @@ __device__ __forceinline__ const uint16_t* head_of(const LinRows& r, int hv) {
 
 // The rows of len tokens from t0 on (none: an empty resource), of a head whose columns of token 0 are at p.
 template <int D>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, int64_t stride, int64_t t0, int len) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + t0 * stride, 0,
-                                           len > 0 ? (int)(((len - 1) * stride + D) * 2) : 0, kBufferWord3);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, int stride, int t0, int len) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + (int64_t)t0 * stride, 0,
+                                           len > 0 ? ((len - 1) * stride + D) * 2 : 0, kBufferWord3);
 }
 
 // A value that the compiler must not keep computed things of across the loop:
@@ -348,8 +348,6 @@ __device__ __forceinline__ Tile tile_of(int wave, int n) {
 
 }  // namespace
 
-// One segment of one value head by one workgroup, one wave per 32 columns of
-// the state and the output.
 // The n-th (segment, value head): heads side by side, so that a token's whole row
 // is read at about one time, and a head's place moved by one from segment to
 // segment. Without that, an XCD (workgroups go to the 8 in turn) reads the same 256
@@ -367,6 +365,14 @@ struct PassLds {
   float ws[kChunk];
 };
 
+// One segment of one value head by one workgroup, one wave per 32 columns of the
+// state and the output, two workgroups to a CU. Alone on a CU a 64-token step of
+// D = 128 takes 6400 clocks (7200 with kEnds): rows into LDS 730, P 960, the state's
+// part of the output 900, P's 490, output and gathering the rest; with all CUs busy,
+// 16 steps of two workgroups a CU take 90 us from L2 and 117 us from HBM, whose 6
+// TB/s are then the bound. Waves of 16 columns, four to a SIMD, read b^T and a twice as
+// often: no faster (a step alone 7700 clocks, the gradients of 2 x 8192 tokens
+// 297 us for 286).
 // kEnds: the segment is a whole sequence whose end state goes to p.io: it is
 // gathered to fp32's precision. Otherwise the carried state only meets a, rounded
 // to bf16, and 16 bits of what it gathers are enough (a third less matrix work);
@@ -407,16 +413,17 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
   const Lane<D> L(lane, wave);
   RowRegs<D, NT> ra, rb, rc;
   const uint16_t *ap = head_of<D>(p.a, hv), *bp = head_of<D>(p.b, hv), *cp = head_of<D>(p.c, hv);
-  const int la = ra.lane_byte(p.a.stride, tid), lb = rb.lane_byte(p.b.stride, tid), lc = rc.lane_byte(p.c.stride, tid);
-  const int sa = (int)(ra.kRows * p.a.stride * 2), sb = (int)(rb.kRows * p.b.stride * 2), sc = (int)(rc.kRows * p.c.stride * 2);
+  const int ga = (int)p.a.stride, gb = (int)p.b.stride, gc = (int)p.c.stride;  // checked: below 2^23
+  const int la = ra.lane_byte(ga, tid), lb = rb.lane_byte(gb, tid), lc = rc.lane_byte(gc, tid);
+  const int sa = ra.kRows * ga * 2, sb = rb.kRows * gb * 2, sc = rc.kRows * gc * 2;
   // one of the next chunk's 12 pieces; past the segment's end they are zeros that nothing reads
   __amdgpu_buffer_rsrc_t na, nb, nc;
   auto next = [&](int i) {
-    const int64_t t0 = sg.t0 + (int64_t)(kBack ? chunks - 1 - i : i) * kChunk;
-    const int len = i < chunks ? min(kChunk, sg.t1 - (int)t0) : 0;
-    na = chunk_rows<D>(ap, p.a.stride, t0, len);
-    nb = chunk_rows<D>(bp, p.b.stride, t0, len);
-    nc = chunk_rows<D>(cp, p.c.stride, t0, len);
+    const int n = max(min(i, chunks - 1), 0), t0 = sg.t0 + (kBack ? chunks - 1 - n : n) * kChunk;
+    const int len = i < chunks ? min(kChunk, sg.t1 - t0) : 0;
+    na = chunk_rows<D>(ap, ga, t0, len);
+    nb = chunk_rows<D>(bp, gb, t0, len);
+    nc = chunk_rows<D>(cp, gc, t0, len);
   };
   constexpr int kLoads = 3 * RowRegs<D, NT>::kPieces;
   auto request = [&](int j) {
@@ -432,8 +439,8 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) request(j);
   for (int i = 0; i < chunks; ++i) {
-    const int64_t t0 = sg.t0 + (kBack ? chunks - 1 - i : i) * kChunk;
-    const int len = min(kChunk, sg.t1 - (int)t0);
+    const int t0 = sg.t0 + (kBack ? chunks - 1 - i : i) * kChunk;
+    const int len = min(kChunk, sg.t1 - t0);
     lds_barrier();  // the last chunk's readers are done
     ra.store(As, tid);
     rb.store(Bs, tid);
@@ -533,7 +540,7 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
 
     // row t = 32 tb + lane % 32; register 4 j + i is column 8 j + 4 (lane / 32) + i. Rows past the chunk's end are
     // past the buffer's, whose stores the hardware drops.
-    Out* const out = static_cast<Out*>(p.out) + (t0 * cut.HV + hv) * D;
+    Out* const out = static_cast<Out*>(p.out) + ((int64_t)t0 * cut.HV + hv) * D;
     const __amdgpu_buffer_rsrc_t ro =
         __builtin_amdgcn_make_buffer_rsrc(out, 0, (len - 1) * orow + D * (int)sizeof(Out), kBufferWord3);
 #pragma unroll
@@ -595,17 +602,17 @@ __device__ __forceinline__ void lin_gather(const LinCut& cut, int slot, int hv, 
   const Lane<D> L(lane, wave);
   RowRegs<D, NT> rb, rc;
   const uint16_t *bp = head_of<D>(b, hv), *cp = head_of<D>(c, hv);
-  const int lb = rb.lane_byte(b.stride, tid), lc = rc.lane_byte(c.stride, tid);
+  const int gb = (int)b.stride, gc = (int)c.stride;
+  const int lb = rb.lane_byte(gb, tid), lc = rc.lane_byte(gc, tid);
   const int all = chunks_of(sg);
   auto start = [&](int i) { return sg.t0 + (kBack ? i : all - 1 - i) * kChunk; };
   auto request = [&](int i) {
-    const int64_t t0 = start(i);
-    const int len = min(kChunk, sg.t1 - (int)t0);
-    const __amdgpu_buffer_rsrc_t nb = chunk_rows<D>(bp, b.stride, t0, len), nc = chunk_rows<D>(cp, c.stride, t0, len);
+    const int t0 = start(i), len = min(kChunk, sg.t1 - t0);
+    const __amdgpu_buffer_rsrc_t nb = chunk_rows<D>(bp, gb, t0, len), nc = chunk_rows<D>(cp, gc, t0, len);
 #pragma unroll
     for (int j = 0; j < RowRegs<D, NT>::kPieces; ++j) {
-      rb.load(j, nb, lb, (int)(rb.kRows * b.stride * 2));
-      rc.load(j, nc, lc, (int)(rc.kRows * c.stride * 2));
+      rb.load(j, nb, lb, rb.kRows * gb * 2);
+      rc.load(j, nc, lc, rc.kRows * gc * 2);
     }
   };
   if (chunks > 0) request(0);

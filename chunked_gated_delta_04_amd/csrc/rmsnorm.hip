@@ -200,19 +200,15 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
   __shared__ float part[2][GROUP > 64 ? GROUP / 64 : 1];
   const int t = threadIdx.x % GROUP, D = a.D;
   const int first = blockIdx.x * kRows + threadIdx.x / GROUP;  // this group's first row; it takes every step-th
-  // the weights stay in registers, but for 1024 threads, which have too few
-  constexpr bool kHold = GROUP < 1024;
   float w[P][V], acc[P][V];
-  auto weights = [&](int p) {
-    if (a.weight) load_at<T, V>(static_cast<const T*>(a.weight), column<V, GROUP>(p, t), D, w[p]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) w[p][i] = a.weight ? w[p][i] + a.unit : 1.f;
-  };
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (kHold) weights(p);
+    if (a.weight) load_at<T, V>(static_cast<const T*>(a.weight), column<V, GROUP>(p, t), D, w[p]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[p][i] = 0.f;
+    for (int i = 0; i < V; ++i) {
+      w[p][i] = a.weight ? w[p][i] + a.unit : 1.f;
+      acc[p][i] = 0.f;
+    }
   }
   int odd = 0;
   for (int base = blockIdx.x * kRows; base < a.rows; base += step, odd ^= 1) {
@@ -227,7 +223,6 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
       const int c = column<V, GROUP>(p, t);
       load_at<T, V>(s, c, D, n[p]);
       load_at<T, V>(dy, c, D, g[p]);
-      if (!kHold) weights(p);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         n[p][i] *= rstd;
@@ -361,6 +356,11 @@ struct Bwd {
 };
 
 }  // namespace
+
+int64_t norm_threads(int rows, int D) {
+  const int g = shape_of(D).group;
+  return blocks_of(rows, D) * (g > 256 ? g : 256);
+}
 
 int norm_partials(int rows, int D) {
   const int64_t b = blocks_of(rows, D);

@@ -458,7 +458,9 @@ size_t gdn_linear_bwd_workspace_size(const gdn_linear_problem* p);
  *             when no backward follows (fp32 states that parts of the
  *             sequences start from, in an order internal to this library).
  * A sequence of length 0 gets hT = h0 (or 0); T = 0 is valid. Rows of o at or
- * past cu_seqlens[N] are left as they were.
+ * past cu_seqlens[N] are left as they were. No output overlaps an input. With
+ * cu_seqlens_host the call leaves out launches that the lengths do not need; the
+ * results are the same bits.
  * Errors: GDN_ERR_NULL (p, or q, k, v, o when T > 0, log_decay or cu_seqlens
  * when N > 0), GDN_ERR_SHAPE (extents or strides), GDN_ERR_UNSUPPORTED,
  * GDN_ERR_SEQLENS, GDN_ERR_ALIGN, GDN_ERR_WORKSPACE, GDN_ERR_HIP. */
@@ -514,7 +516,7 @@ typedef enum { GDN_BF16 = 0, GDN_FP16 = 1, GDN_FP32 = 2 } gdn_dtype;
  *   (a, b) -> mscale (a cos - b sin, a sin + b cos),
  * where pair j is columns (j, j + R/2), or (2 j, 2 j + 1) when interleaved.
  * The other D - R columns are copied. Angles are formed in fp64.
- *   T           tokens (T >= 0)
+ *   T           tokens (0 <= T <= 2^25)
  *   HQ, HK      heads of q and k (HK = 0: no k)
  *   D, R        columns of a head (at most 1024) and how many of them turn
  *               (even, 2 <= R <= D)
@@ -579,7 +581,7 @@ int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, 
  *   y = s / sqrt(mean(s^2) + eps) * (weight + unit),
  * s rounded to dtype: it is what the residual stream holds and what the
  * backward reads. The norm and its outputs come from that s in fp32.
- *   rows, D     rows >= 0, 1 <= D <= 16384
+ *   rows, D     rows >= 0 (at most 2^24 of up to 5120 columns, 2^22 of any), 1 <= D <= 16384
  *   dtype       gdn_dtype of x, residual, weight, residual_out, y and of the
  *               gradients in and out
  *   unit_offset 1: the weight is stored around zero (unit = 1); 0: unit = 0

@@ -302,3 +302,29 @@ def test_the_host_boundaries_change_no_bit():
         assert all(torch.equal(want[n], y) for n, y in dict(o=o, hT=hT, **g).items())
         assert torch.equal(o2, o) and torch.equal(hT2, hT) and torch.equal(o3, o) and none is None
         assert all(torch.equal(g2[n], g[n]) for n in ("dq", "dk", "dv")) and g2["dh0"] is None
+
+
+def test_no_tokens_and_no_sequences():
+    for lens in ([0, 0], []):
+        x = inputs(lens, 2, 4, 128, seed=1)
+        got = run(x)
+        assert torch.equal(got["hT"].cpu(), x["h0"]) and torch.equal(got["dh0"].cpu(), x["dhT"])
+        assert all(got[n].shape[0] == 0 for n in ("o", "dq", "dk", "dv"))
+    o = gdn.linear_step(*(torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda"),) * 3, torch.zeros(2, device="cuda"),
+                        torch.zeros(3, 2, 64, 64, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert o.shape == (0, 2, 64)
+
+
+def test_many_sequences():
+    """More sequences than one wave's probes of the boundaries, and than their square; the first, the last and empty ones."""
+    lens = [0, 3] + [1, 0] * 2600 + [300, 0, 0]
+    x = inputs(lens, 1, 1, 64, seed=2)
+    got = run(x)
+    keep = {k: x[k][-320:] for k in ("q", "k", "v", "dO")} | dict(
+        log_decay=x["log_decay"], cu=torch.tensor([0] + list(range(1, 21)) + [320], dtype=torch.int32),
+        h0=torch.cat([x["h0"][:-3][-40::2], x["h0"][-3:-2]]), dhT=torch.cat([x["dhT"][:-3][-40::2], x["dhT"][-3:-2]]))
+    part = {k: got[k][-320:] for k in ("o", "dq", "dk", "dv")}
+    part |= {k: torch.cat([got[k][:-3][-40::2], got[k][-3:-2]]) for k in ("hT", "dh0")}
+    check(part, keep)
+    empty = [i for i, n in enumerate(lens) if n == 0]
+    assert torch.equal(got["hT"][empty].cpu(), x["h0"][empty]) and torch.equal(got["dh0"][empty].cpu(), x["dhT"][empty])

@@ -143,3 +143,18 @@ def test_the_binding_refuses_what_does_not_fit():
     for error, call in bad:
         with pytest.raises(error):
             call()
+
+
+def test_many_sequences():
+    lens = [0, 3] + [1, 0] * 2600 + [30, 0]
+    gen = torch.Generator().manual_seed(3)
+    q = rows(sum(lens), 1, 16, torch.float32, gen, 0)
+    f = gdn.rotary_inv_freq(16, device="cuda")[0]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    past = torch.randint(0, 5000, (len(lens),), generator=gen, dtype=torch.int32)
+    out, none = gdn.rotary(q, None, f, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), offsets=past.cuda())
+    pos = Y.positions(cu.tolist(), past.tolist())
+    close(out, f64(q), Y.rotary(f64(q), pos, f64(f), False), 1.0)
+    assert none is None
+    empty, _ = gdn.rotary(q[:0], None, f, positions=torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert empty.shape == (0, 1, 16)

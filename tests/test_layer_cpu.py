@@ -39,7 +39,8 @@ def rotary(G, back=False, host=None, ptr=None, **over):
 def test_rotary_refuses(G, back):
     assert (G._lib.gdn_rotary_bwd if back else G._lib.gdn_rotary)(None, FAKE, FAKE, FAKE, FAKE, FAKE, None) == NULL
     for bad in (dict(T=-1), dict(HQ=0), dict(HK=-1), dict(D=0), dict(N=-1), dict(N=0), dict(q_stride=255),
-                dict(k_stride=127), dict(q_out_stride=-256), dict(k_out_stride=1 << 31), dict(HQ=1 << 24)):
+                dict(k_stride=127), dict(q_out_stride=-256), dict(k_out_stride=1 << 31), dict(HQ=1 << 24),
+                dict(T=(1 << 25) + 1)):
         assert rotary(G, back, **bad) == SHAPE, bad
     for bad in (dict(R=0), dict(R=31), dict(R=66), dict(R=-2), dict(D=1026), dict(interleaved=2), dict(dtype=3),
                 dict(dtype=-1)):
@@ -69,7 +70,7 @@ def norm(G, back=False, ptr=None, n=1 << 40, **over):
 @pytest.mark.parametrize("back", [False, True])
 def test_norm_refuses(G, back):
     for bad in (dict(rows=-1), dict(D=0), dict(D=-5), dict(x_stride=63), dict(x_stride=-64), dict(residual_stride=1),
-                dict(x_stride=1 << 31)):
+                dict(x_stride=1 << 31), dict(rows=1 << 24, D=8192), dict(rows=(1 << 31) - 1, D=5120)):
         assert norm(G, back, **bad) == SHAPE, bad
     for bad in (dict(D=16385), dict(dtype=3), dict(dtype=-1), dict(group=64), dict(group=-1), dict(unit_offset=2)):
         assert norm(G, back, **bad) == UNSUPPORTED, bad
