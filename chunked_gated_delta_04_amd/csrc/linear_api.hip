@@ -30,10 +30,21 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 // is its problem's (the boundaries stay on the device). Cutting a sequence costs
 // two launches, a second reading of k and v and 16 D^2 bytes a segment and head,
 // and makes items that run side by side.
-//   Few chains (sequences x value heads): 512 to 1023 items, two to a CU; at
-// least 256 tokens each. 1 x 8192 tokens, 8 heads of 128: 47 us with 256
-// tokens, 55 with 512, 352 uncut; 2 x 8192, 32 heads: 204 us with 1024, 268 with
-// 256, 439 uncut.
+//   Few chains (sequences x value heads): twice as long, from 128 tokens on, while
+// that leaves `fill` items, of some 256 (D = 128) or 512 that run at once. Short
+// segments make more states than they save time, so fewer items are enough for
+// them. One sequence, 16 heads of 128, forward and backward, us:
+//     tokens    128   256   512  1024  2048 a segment
+//       1024     56    65
+//       3000    104    92   109
+//       6000    179   148   141   184
+//      12288    352   284   257   262   365
+//      24576          538   470   469   506
+//      65536               1192  1136  1097
+// and 16 heads of 64:
+//       2048     44    51    69
+//      10000    120   100   106   128
+//      24576          228   201   224   257
 //   Chains enough to fill the chip, and short: no cut in sequences of the mean
 // length. 16 x 1024, 8 heads: 56 us uncut, 78 with 256; 16 x 2048, 32 heads: 258
 // uncut, 406 with 1024; but 4 x 4096, 32 heads: 237 uncut, 204 with 1024. The
@@ -45,8 +56,9 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 // with 4096).
 int64_t segment_tokens(const gdn_linear_problem* p) {
   const int64_t work = (int64_t)p->T * p->HV, chains = (int64_t)p->N * p->HV;
-  int64_t S = 256;
-  while (S < 4096 && S * 2 * 512 <= work) S *= 2;
+  const auto fill = [&](int64_t S) { return p->K == 128 ? (S <= 1024 ? 176 : 400) : (S <= 256 ? 208 : 448); };
+  int64_t S = 128;
+  while (S < 4096 && 2 * S * fill(2 * S) <= work) S *= 2;
   const int64_t mean = p->N > 0 ? ((int64_t)p->T + p->N - 1) / p->N : 0;
   if (chains >= 128 && mean <= 2048) {
     const bool full = p->K == 128;
@@ -83,7 +95,7 @@ gdn_status check_pack(const gdn_linear_problem* p) {
   const gdn_status st = check_linear(p);
   if (st != GDN_OK) return st;
   const int64_t slots = (int64_t)p->T / segment_tokens(p) + p->N;
-  if (segment_tokens(p) > INT32_MAX || 2 * slots * p->HV + 16 > kMaxBlocks ||
+  if (2 * slots * p->HV + 16 > kMaxBlocks ||
       (int64_t)p->N * p->HV * (p->K * p->V / 256) > 4 * kMaxBlocks)
     return GDN_ERR_SHAPE;
   if (p->cu_seqlens_host) {

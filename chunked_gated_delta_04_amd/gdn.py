@@ -902,19 +902,24 @@ def _rotary(call, q, k, inv_freq, positions, cu_seqlens, offsets, cu_seqlens_hos
     qp, qs = _rows(q, q.dtype, "q", dev)
     kp, ks = _rows(k, q.dtype, "k", dev) if k is not None else (None, 0)
 
+    def result(t, heads, name):
+        """(tensor, pointer, token stride) of one output: t, or a new one without it."""
+        if t is None:
+            t = torch.empty(T, heads, D, dtype=q.dtype, device=dev)
+            return t, t.data_ptr(), 0
+        if t.shape != (T, heads, D):
+            raise ValueError(f"{name} must have the shape {(T, heads, D)}, got {tuple(t.shape)}")
+        return (t, *_rows(t, q.dtype, name, dev))
+
     def launch(s):
-        qr = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-        kr = torch.empty(k.shape, dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
-        if qr.shape != q.shape or (k is not None and kr.shape != k.shape):
-            raise ValueError("q_out and k_out must have the shapes of q and k")
-        qo, qos = _rows(qr, q.dtype, "q_out", dev)
-        ko, kos = _rows(kr, q.dtype, "k_out", dev) if k is not None else (None, 0)
+        qr, qo, qos = result(q_out, HQ, "dq" if back else "q_out")
+        kr, ko, kos = result(k_out, HK, "dk" if back else "k_out") if k is not None else (None, None, 0)
         if back:
             p.q_out_stride, p.k_out_stride, p.q_stride, p.k_stride = qs, ks, qos, kos
         else:
             p.q_stride, p.k_stride, p.q_out_stride, p.k_out_stride = qs, ks, qos, kos
         _check(call(ctypes.byref(p), freq, qp, kp, qo, ko, s), "gdn_rotary_bwd" if back else "gdn_rotary")
-        return qr, kr if k is not None else None
+        return qr, kr
 
     return _on_stream(dev, stream, launch)
 
@@ -990,7 +995,7 @@ def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-6, unit_offset=False, quan
             t = out["y8"] = torch.empty(rows, D, dtype=torch.float8_e4m3fn, device=dev)
             y8 = t.data_ptr()
             shape = (rows,) if quant == "row" else (rows, (D + 127) // 128)
-            t = out["scales"] = torch.empty(shape, dtype=_f32, device=dev)
+            t = out["scales"] = torch.empty(*shape, dtype=_f32, device=dev)
             scales = t.data_ptr()
         if want_rstd:
             t = out["rstd"] = torch.empty(rows, dtype=_f32, device=dev)
