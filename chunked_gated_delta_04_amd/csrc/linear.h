@@ -19,9 +19,9 @@ struct LinRows {
 // and T / S + N slots hold every pack. S is a multiple of the 64-token chunk.
 struct LinCut {
   const int32_t* cu;
-  int N, T, HV;
-  int S;      // tokens per segment
-  int slots;  // T / S + N
+  int N, T, HV, G;  // G value heads to a key head
+  int S;            // tokens per segment
+  int slots;        // T / S + N
 };
 
 // One pass over the chunks of every segment, front to back or back to front:

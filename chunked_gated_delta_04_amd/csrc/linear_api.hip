@@ -88,14 +88,14 @@ gdn_status check_linear(const gdn_linear_problem* p) {
 
 LinCut cut_of(const gdn_linear_problem* p) {
   const int64_t S = segment_tokens(p);
-  return {p->cu_seqlens, p->N, p->T, p->HV, (int)S, (int)(p->T / S + p->N)};
+  return {p->cu_seqlens, p->N, p->T, p->HV, p->HV / p->H, (int)S, (int)(p->T / S + p->N)};
 }
 
 gdn_status check_pack(const gdn_linear_problem* p) {
   const gdn_status st = check_linear(p);
   if (st != GDN_OK) return st;
   const int64_t slots = (int64_t)p->T / segment_tokens(p) + p->N;
-  if (2 * slots * p->HV + 16 > kMaxBlocks ||
+  if (2 * (slots + 8) * p->HV > kMaxBlocks ||
       (int64_t)p->N * p->HV * (p->K * p->V / 256) > 4 * kMaxBlocks)
     return GDN_ERR_SHAPE;
   if (p->cu_seqlens_host) {

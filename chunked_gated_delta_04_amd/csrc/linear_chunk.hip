@@ -348,14 +348,29 @@ __device__ __forceinline__ Tile tile_of(int wave, int n) {
 
 }  // namespace
 
-// The n-th (segment, value head): heads side by side, so that a token's whole row
-// is read at about one time, and a head's place moved by one from segment to
-// segment. Without that, an XCD (workgroups go to the 8 in turn) reads the same 256
-// bytes of every 2 KiB throughout, and two of the eight took 14 % longer than the
-// others: gradients of 2 x 8192 tokens, 32 heads, 300 us, and 286 with it.
-__device__ __forceinline__ void item(const LinCut& cut, int n, int& slot, int& hv) {
-  slot = n / cut.HV;
-  hv = (n + slot) % cut.HV;
+// What workgroup n works on: a segment, a value head, and one of `parts` passes
+// (-1: nothing, at the grid's end).
+//   Workgroups go to the 8 XCDs in turn. Those that read the same rows, the passes
+// of a segment and the value heads of a key head, are 8 apart, so that they run on
+// one XCD at one time and share its L2: a forward over 32768 tokens of 16 key and 32
+// value heads reads 591 MB, and 852 with the value heads on XCDs of their own.
+//   Key heads are side by side, so that a token's whole row is read at about one
+// time, and a head's place moves by one from segment to segment. Without that, an
+// XCD reads the same 256 bytes of every 2 KiB throughout, and two of the eight took
+// 14 % longer than the others: gradients of 2 x 8192 tokens, 32 heads, 300 us, and
+// 286 with it.
+struct Item {
+  int slot, hv, part;
+};
+__device__ __forceinline__ Item item_of(const LinCut& cut, int n, int parts) {
+  const int H = cut.HV / cut.G, sharing = parts * cut.G;
+  const int nth = n >> 3, r = nth % sharing, m = nth / sharing * 8 + (n & 7);
+  if (m >= cut.slots * H) return {-1, 0, 0};
+  const int slot = m / H;
+  return {slot, (m + slot) % H * cut.G + r / parts, r % parts};
+}
+unsigned items_grid(const LinCut& cut, int parts) {
+  return ((unsigned)cut.slots * (unsigned)(cut.HV / cut.G) + 7) / 8 * 8 * (unsigned)(parts * cut.G);
 }
 
 template <int D>
@@ -441,6 +456,9 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
   for (int i = 0; i < chunks; ++i) {
     const int t0 = sg.t0 + (kBack ? chunks - 1 - i : i) * kChunk;
     const int len = min(kChunk, sg.t1 - t0);
+    // Ahead of the other workgroup's wave until P is there: while it gathers, this one
+    // gets to its next products (gradients of 2 x 8192 tokens, 32 heads, 287 -> 267 us).
+    __builtin_amdgcn_s_setprio(1);
     lds_barrier();  // the last chunk's readers are done
     ra.store(As, tid);
     rb.store(Bs, tid);
@@ -524,6 +542,7 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
     }
     uint4 cc[4];
     load_columns<D>(cc, Cs, L);
+    __builtin_amdgcn_s_setprio(0);
     lds_barrier();  // P is there
     bf16x8 pr[2][4];
 #pragma unroll
@@ -570,12 +589,12 @@ template <int D>
 __global__ __launch_bounds__(2 * D, 2) void lin_out_kernel(LinCut cut, const float* __restrict__ log_decay,
                                                            float scale, LinPass p) {
   __shared__ __align__(16) PassLds<D> lds;
-  int slot, hv;
-  item(cut, blockIdx.x, slot, hv);
-  const Segment sg = find_segment(cut, slot);
+  const Item it = item_of(cut, blockIdx.x, 1);
+  if (it.slot < 0) return;
+  const Segment sg = find_segment(cut, it.slot);
   if (unused(sg)) return;
-  if (whole(sg)) lin_pass<D, false, false, false, true>(cut, slot, hv, sg, log_decay, scale, p, lds);
-  else lin_pass<D, false, false, false, false>(cut, slot, hv, sg, log_decay, scale, p, lds);
+  if (whole(sg)) lin_pass<D, false, false, false, true>(cut, it.slot, it.hv, sg, log_decay, scale, p, lds);
+  else lin_pass<D, false, false, false, false>(cut, it.slot, it.hv, sg, log_decay, scale, p, lds);
 }
 
 // What a segment adds to the state, from a zero start: sum over its tokens of
@@ -638,22 +657,19 @@ __global__ __launch_bounds__(2 * D, 2) void lin_gather_kernel(LinCut cut, const 
                                                               float scale, LinRows b, LinRows c, bool ends,
                                                               float* __restrict__ states) {
   __shared__ __align__(16) PassLds<D> lds;
-  int slot, hv;
-  item(cut, blockIdx.x, slot, hv);
-  lin_gather<D, kBack>(cut, slot, hv, log_decay, scale, b, c, ends, states, lds);
+  const Item it = item_of(cut, blockIdx.x, 1);
+  if (it.slot >= 0) lin_gather<D, kBack>(cut, it.slot, it.hv, log_decay, scale, b, c, ends, states, lds);
 }
 
-// The three gradients' passes in one launch. Workgroups go to the 8 XCDs in
-// turn; a segment's three are 8 apart, so that they run on one XCD at one time and
-// the rows that dv's and dk's passes both walk come from its L2 the second time.
+// The three gradients' passes in one launch (see item_of): the rows that dv's and
+// dk's passes both walk come from the L2 the second time.
 template <int D, bool kWide>
 __global__ __launch_bounds__(2 * D, 2) void lin_grad_kernel(LinCut cut, const float* __restrict__ log_decay,
                                                             float scale, LinPass dq, LinPass dv, LinPass dk) {
   __shared__ __align__(16) PassLds<D> lds;
-  const int nth = blockIdx.x >> 3, part = nth % 3, at = nth / 3 * 8 + (blockIdx.x & 7);
-  if (at >= cut.slots * cut.HV) return;
-  int slot, hv;
-  item(cut, at, slot, hv);
+  const Item it = item_of(cut, blockIdx.x, 3);
+  if (it.slot < 0) return;
+  const int slot = it.slot, hv = it.hv, part = it.part;
   const Segment sg = find_segment(cut, slot);
   if (unused(sg)) return;
   if (part == 1) lin_pass<D, true, true, kWide, false>(cut, slot, hv, sg, log_decay, scale, dk, lds);
@@ -737,7 +753,7 @@ __global__ __launch_bounds__(256) void lin_fold_kernel(int64_t n, int DH, int G,
 
 hipError_t launch_lin_out(int D, const LinCut& cut, const float* log_decay, float scale, const LinPass& p,
                           hipStream_t s) {
-  const dim3 grid((unsigned)cut.slots * (unsigned)cut.HV), block(2 * D);
+  const dim3 grid(items_grid(cut, 1)), block(2 * D);
   if (D == 128)
     hipLaunchKernelGGL((lin_out_kernel<128>), grid, block, 0, s, cut, log_decay, scale, p);
   else
@@ -747,14 +763,14 @@ hipError_t launch_lin_out(int D, const LinCut& cut, const float* log_decay, floa
 
 hipError_t launch_lin_grad(int D, bool wide, const LinCut& cut, const float* log_decay, float scale,
                            const LinPass& dq, const LinPass& dv, const LinPass& dk, hipStream_t s) {
-  LIN_LAUNCH1(lin_grad_kernel, wide, ((unsigned)cut.slots * (unsigned)cut.HV + 7) / 8 * 24, cut, log_decay, scale,
+  LIN_LAUNCH1(lin_grad_kernel, wide, items_grid(cut, 3), cut, log_decay, scale,
               dq, dv, dk);
   return hipGetLastError();
 }
 
 hipError_t launch_lin_gather(int D, bool back, const LinCut& cut, const float* log_decay, float scale,
                              const LinRows& b, const LinRows& c, bool ends, float* states, hipStream_t s) {
-  LIN_LAUNCH1(lin_gather_kernel, back, (unsigned)cut.slots * (unsigned)cut.HV, cut, log_decay, scale, b, c, ends,
+  LIN_LAUNCH1(lin_gather_kernel, back, items_grid(cut, 1), cut, log_decay, scale, b, c, ends,
               states);
   return hipGetLastError();
 }

@@ -487,7 +487,8 @@ int gdn_linear_fwd_paged(const gdn_linear_problem* p, const uint16_t* q, const u
  *   dq, dk    bf16 [T, H, K]; dv bf16 [T, HV, V] (dense)
  *   dh0       fp32 [N, HV, V, K] cotangent of h0, or NULL to skip
  * The value heads of one key head are summed into dq, dk in fp32 in a fixed
- * order; no atomics. Errors: as gdn_linear_fwd, GDN_ERR_NULL for saved, dO,
+ * order; no atomics. No output overlaps an input or another output (dh0 is not
+ * dhT). Errors: as gdn_linear_fwd, GDN_ERR_NULL for saved, dO,
  * dq, dk, dv. */
 int gdn_linear_bwd(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,
                    const uint16_t* v, const float* log_decay, const void* saved,
@@ -581,7 +582,8 @@ int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, 
  *   y = s / sqrt(mean(s^2) + eps) * (weight + unit),
  * s rounded to dtype: it is what the residual stream holds and what the
  * backward reads. The norm and its outputs come from that s in fp32.
- *   rows, D     rows >= 0 (at most 2^24 of up to 5120 columns, 2^22 of any), 1 <= D <= 16384
+ *   rows, D     1 <= D <= 16384; rows >= 0, below 2^24 up to D = 4096, 2^23 up
+ *               to 8192, 2^22 above
  *   dtype       gdn_dtype of x, residual, weight, residual_out, y and of the
  *               gradients in and out
  *   unit_offset 1: the weight is stored around zero (unit = 1); 0: unit = 0
