@@ -52,7 +52,7 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 // an item 3.6 us (2.0 with D = 64) while every item has a CU (half a CU) to
 // itself; cut, 35 us and 7 passes over rows at 5 TB/s. Means over 2048 are left
 // out: where the lengths differ, the longest sequence's items then end long after
-// the others (12 sequences of 492 to 7435 tokens, 32 heads: 376 us with 2048, 487
+// the others (12 sequences of 492 to 7435 tokens, 32 heads: 361 us with 2048, 469
 // with 4096).
 int64_t segment_tokens(const gdn_linear_problem* p) {
   const int64_t work = (int64_t)p->T * p->HV, chains = (int64_t)p->N * p->HV;

@@ -304,15 +304,6 @@ __device__ __forceinline__ void gather_chunk(State<D>& X, const uint16_t* Bs, co
     for (int n = kPieces - 1; n >= 0; --n)
 #pragma unroll
       for (int i = 0; i < KB; ++i) X.x[i] = mfma32(__builtin_bit_cast(bf16x8, k[s & 1][i]), v[s & 1].x[n], X.x[i]);
-    if (s < 3) {
-      // a product, then the vector instructions that fit beside it
-#pragma unroll
-      for (int i = 0; i < kPieces * KB; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x2, 24 / KB, 0);
-      }
-    }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -383,11 +374,14 @@ struct PassLds {
 // One segment of one value head by one workgroup, one wave per 32 columns of the
 // state and the output, two workgroups to a CU. Alone on a CU a 64-token step of
 // D = 128 takes 6400 clocks (7200 with kEnds): rows into LDS 730, P 960, the state's
-// part of the output 900, P's 490, output and gathering the rest; with all CUs busy,
-// 16 steps of two workgroups a CU take 90 us from L2 and 117 us from HBM, whose 6
-// TB/s are then the bound. Waves of 16 columns, four to a SIMD, read b^T and a twice as
-// often: no faster (a step alone 7700 clocks, the gradients of 2 x 8192 tokens
-// 297 us for 286).
+// part of the output 900, P's 490, output and gathering the rest. Two to a CU take
+// 5200 to 5600 a step, in which a SIMD's matrix unit is busy for 1920 (34 %), its
+// vector unit for 1750 (31 %) and the CU's LDS for 2250 (40 %): the bound is how well
+// two waves a SIMD fill each other's waits, and beside it HBM: o of 2 x 8192 tokens,
+// 32 heads, takes 112 us (570 MB, 5.1 TB/s), the three gradients 267 us (1.4 GB, 5.2
+// TB/s). A third workgroup does not fit (244 VGPRs). Waves of 16 columns, four to a
+// SIMD, read b^T and a twice as often: no faster (a step alone 7700 clocks, these
+// gradients 297 us for 286).
 // kEnds: the segment is a whole sequence whose end state goes to p.io: it is
 // gathered to fp32's precision. Otherwise the carried state only meets a, rounded
 // to bf16, and 16 bits of what it gathers are enough (a third less matrix work);
@@ -601,7 +595,9 @@ __global__ __launch_bounds__(2 * D, 2) void lin_out_kernel(LinCut cut, const flo
 // w_t b_t c_t^T, w_t = lam^(tokens after t) (back to front: scale lam^(tokens
 // from the segment's start through t)). The chunks of the largest weights come
 // first, and the rest are not read once every further weight is zero in fp32
-// (lam^n = 0 from e^-104 on), as it soon is for quickly forgetting heads.
+// (lam^n = 0 from e^-104 on), as it soon is for quickly forgetting heads. Bound by
+// HBM: 16384 tokens, 32 heads, 60 to 66 us for 262 MB (4.2 TB/s; 16 steps, the first
+// of which waits for its rows).
 template <int D, bool kBack>
 __device__ __forceinline__ void lin_gather(const LinCut& cut, int slot, int hv, const float* __restrict__ log_decay,
                                            float scale, const LinRows& b, const LinRows& c,
@@ -680,7 +676,8 @@ __global__ __launch_bounds__(2 * D, 2) void lin_grad_kernel(LinCut cut, const fl
 
 // Front to back along each sequence's segments (or back to front): a thread
 // carries 4 values of one state, and leaves the end of a sequence of several
-// segments where io says.
+// segments where io says. 512 segment states, read and written: 14 us, 5 TB/s. (16
+// segments requested together serialised the loads: slower.)
 template <int D, bool kBack>
 __global__ __launch_bounds__(64) void lin_join_kernel(LinCut cut, const float* __restrict__ log_decay, StateRef io,
                                                        float* __restrict__ states) {
@@ -720,7 +717,9 @@ __global__ __launch_bounds__(64) void lin_join_kernel(LinCut cut, const float* _
 }
 
 // out[t][h] = sum over the key head's G value heads of wide[t][h G + i], for
-// dq and dk (blockIdx.y).
+// dq and dk (blockIdx.y). Bound by HBM: 16384 tokens, 16 key and 32 value heads, 127
+// us, 5.3 TB/s. The value heads' parts are fp32: rounding each to bf16 would add an
+// error of the size of the result's own.
 __global__ __launch_bounds__(256) void lin_fold_kernel(int64_t n, int DH, int G, int D,
                                                        const float* __restrict__ wq, const float* __restrict__ wk,
                                                        uint16_t* __restrict__ dq, uint16_t* __restrict__ dk) {
