@@ -177,7 +177,7 @@ GDN_API int gdn_rmsnorm_fwd(const gdn_rmsnorm_problem* p, const void* x, const v
 }
 
 GDN_API size_t gdn_rmsnorm_bwd_workspace_size(const gdn_rmsnorm_problem* p) {
-  return check_norm(p) == GDN_OK ? (size_t)norm_partials(p->rows, p->D) * p->D * sizeof(float) : 0;
+  return check_norm(p) == GDN_OK ? (size_t)norm_partials(p->rows, p->D) * norm_pitch(p->D) * sizeof(float) : 0;
 }
 
 GDN_API int gdn_rmsnorm_bwd(const gdn_rmsnorm_problem* p, const void* s, const void* weight, const float* rstd,

@@ -49,22 +49,35 @@ __device__ __forceinline__ float reduce_row(float x, float* part) {
   return x;
 }
 
-// The first column of a thread's piece p of V columns. 16 bytes at a time, the
-// row's threads side by side; element by element, a wave takes 128 columns at
-// a time, so that a scale's 128 columns belong to one wave.
+// The first column of a thread's piece p of V columns (16 bytes of the tensor's
+// type), a row's threads side by side.
 template <int V, int GROUP>
 __device__ __forceinline__ int column(int p, int t) {
-  if constexpr (V > 1) return (p * GROUP + t) * V;
-  else if constexpr (GROUP < 64) return p * GROUP + t;
-  else return ((p >> 1) * (GROUP / 64) + (t >> 6)) * 128 + (p & 1) * 64 + (t & 63);
+  return (p * GROUP + t) * V;
 }
 
-template <typename T, int V>
+// V columns of a row from c on; those past D are zeros, and not stored. kWide: D is
+// a multiple of V and everything is aligned to 16 bytes. Rows of any other length or
+// alignment go 16 bytes at a time all the same (load_any). 16384 x 4095, forward and
+// backward: 236 us, and 659 element by element.
+template <typename T, int V, bool kWide>
 __device__ __forceinline__ void load_at(const T* row, int c, int D, float* x) {
-  if (c < D) load_n<T, V>(row + c, x);
-  else
+  if constexpr (kWide) {
+    if (c < D) load_n<T, V>(row + c, x);
+    else
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = 0.f;
+      for (int i = 0; i < V; ++i) x[i] = 0.f;
+  } else {
+    load_any<T, V>(row, c, D, x);
+  }
+}
+template <typename T, int V, bool kWide>
+__device__ __forceinline__ void store_at(T* row, int c, int D, const float* x) {
+  if constexpr (kWide) {
+    if (c < D) store_n<T, V>(row + c, x);
+  } else {
+    store_any<T, V>(row, c, D, x);
+  }
 }
 
 // 448 a / m as a division rounds it, from r = 448 / m: the remainder of a first
@@ -79,25 +92,26 @@ __device__ __forceinline__ float quotient(float a, float m, float r, float rm) {
   return c == c ? c : q;  // m infinite: the remainder is no number
 }
 // e4m3 of values of at most 448 in magnitude, to nearest even; NaN stays
-template <int V>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* x) {
-  if constexpr (V == 1) {
-    *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[0], 0.f, 0, false);
-  } else {
-    uint32_t w[V / 4];
+template <int V, bool kWide>
+__device__ __forceinline__ void store_e4m3(uint8_t* row, int c, int D, const float* x) {
+  uint32_t w[V / 4];
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      int u = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], u, true);
-    }
-    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(p) = w[0];
+  for (int i = 0; i < V / 4; ++i) {
+    int u = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], u, true);
+  }
+  if (kWide ? c < D : c + V <= D) {
+    __builtin_memcpy(kWide ? __builtin_assume_aligned(row + c, V) : row + c, w, V);
+  } else if (!kWide) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i < D) row[c + i] = (uint8_t)(w[i / 4] >> 8 * (i % 4));
   }
 }
 
 }  // namespace
 
-template <typename T, int V, int GROUP, int E>
+template <typename T, int V, bool kWide, int GROUP, int E>
 __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(NormArgs a) {
   constexpr int P = E / V, NT = GROUP > 256 ? GROUP : 256, kRows = NT / GROUP;
   __shared__ float part[2][GROUP > 64 ? GROUP / 64 : 1];
@@ -108,7 +122,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
   float v[P][V];
   float sum = 0.f;
 #pragma unroll
-  for (int p = 0; p < P; ++p) load_at<T, V>(x, column<V, GROUP>(p, t), D, v[p]);
+  for (int p = 0; p < P; ++p) load_at<T, V, kWide>(x, column<V, GROUP>(p, t), D, v[p]);
   if (a.residual) {
     const T* r = static_cast<const T*>(a.residual) + (on ? row : 0) * a.residual_stride;
     T* so = static_cast<T*>(a.residual_out) + row * D;
@@ -116,10 +130,10 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     for (int p = 0; p < P; ++p) {
       const int c = column<V, GROUP>(p, t);
       float y[V];
-      load_at<T, V>(r, c, D, y);
+      load_at<T, V, kWide>(r, c, D, y);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[p][i] = to_f32(from_f32<T>(v[p][i] + y[i]));
-      if (on && c < D) store_n<T, V>(so + c, v[p]);
+      if (on) store_at<T, V, kWide>(so, c, D, v[p]);
     }
   }
 #pragma unroll
@@ -135,15 +149,15 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     const int c = column<V, GROUP>(p, t);
     if (a.weight) {
       float w[V];
-      load_at<T, V>(static_cast<const T*>(a.weight), c, D, w);
+      load_at<T, V, kWide>(static_cast<const T*>(a.weight), c, D, w);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[p][i] *= w[i] + a.unit;
     }
-    if (a.y && on && c < D) {
+    if (a.y && on) {
       float y[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) y[i] = v[p][i] * rstd;
-      store_n<T, V>(static_cast<T*>(a.y) + row * D + c, y);
+      store_at<T, V, kWide>(static_cast<T*>(a.y) + row * D, c, D, y);
     }
   }
   if (!a.y8) return;
@@ -177,10 +191,8 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     const int c = column<V, GROUP>(p, t);
     float m = whole;
     if (a.group != D) {
-      if constexpr (V > 1 && GROUP >= 128 / V) {
+      if constexpr (GROUP >= 128 / V) {
         m = reduce_lanes<128 / V, true>(top[p]);
-      } else if constexpr (V == 1 && GROUP >= 64) {
-        m = reduce_lanes<64, true>(nmax(top[p & ~1], top[p | 1]));
       } else {  // the row's threads hold its 128 columns or fewer in several pieces
         m = top[0];
 #pragma unroll
@@ -193,11 +205,11 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     const float r = kE4m3Max / m, rm = 1.f / m;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[p][i] = quotient(rstd > 0.f ? v[p][i] : v[p][i] * rstd, m, r, rm);
-    if (on && c < D) store_e4m3<V>(a.y8 + row * D + c, v[p]);
+    if (on) store_e4m3<V, kWide>(a.y8 + row * D, c, D, v[p]);
   }
 }
 
-template <typename T, int V, int GROUP, int E>
+template <typename T, int V, bool kWide, int GROUP, int E>
 __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(NormGradArgs a, int step) {
   constexpr int P = E / V, NT = GROUP > 256 ? GROUP : 256, kRows = NT / GROUP;
   __shared__ float part[2][GROUP > 64 ? GROUP / 64 : 1];
@@ -206,7 +218,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
   float w[P][V], acc[P][V];
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    if (a.weight) load_at<T, V>(static_cast<const T*>(a.weight), column<V, GROUP>(p, t), D, w[p]);
+    if (a.weight) load_at<T, V, kWide>(static_cast<const T*>(a.weight), column<V, GROUP>(p, t), D, w[p]);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       w[p][i] = a.weight ? w[p][i] + a.unit : 1.f;
@@ -224,8 +236,8 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       const int c = column<V, GROUP>(p, t);
-      load_at<T, V>(s, c, D, n[p]);
-      load_at<T, V>(dy, c, D, g[p]);
+      load_at<T, V, kWide>(s, c, D, n[p]);
+      load_at<T, V, kWide>(dy, c, D, g[p]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         n[p][i] *= rstd;
@@ -240,20 +252,20 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_bwd_kernel(
     for (int p = 0; p < P; ++p) {
       const int c = column<V, GROUP>(p, t);
       float z[V];
-      if (a.ds) load_at<T, V>(ds, c, D, z);
+      if (a.ds) load_at<T, V, kWide>(ds, c, D, z);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = rstd * (g[p][i] - n[p][i] * dot);
         z[i] = a.ds ? d + z[i] : d;
       }
-      if (on && c < D) store_n<T, V>(static_cast<T*>(a.dx) + row * D + c, z);
+      if (on) store_at<T, V, kWide>(static_cast<T*>(a.dx) + row * D, c, D, z);
     }
   }
   if (!a.partial) return;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = column<V, GROUP>(p, t);
-    if (c < D) store_n<float, V>(a.partial + (int64_t)first * D + c, acc[p]);
+    if (c < D) store_n<float, V>(a.partial + (int64_t)first * norm_pitch(D) + c, acc[p]);
   }
 }
 
@@ -271,7 +283,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_fold_kernel(int n, int D, const 
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int i = i0 + j * kParts;
-        x[j] = i < n ? partial[(int64_t)i * D + c] : 0.f;
+        x[j] = i < n ? partial[(int64_t)i * norm_pitch(D) + c] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) s += x[j];
@@ -309,27 +321,27 @@ int rows_at_once(int D) {
   return g < 256 ? 256 / g : 1;
 }
 
-template <typename T, int V, typename F>
+template <typename T, int V, bool kWide, typename F>
 hipError_t with_shape(int D, F&& f) {
   switch (shape_of(D).group * shape_of(D).each) {
-    case 128: return f.template operator()<T, V, 16, 8>();
-    case 512: return f.template operator()<T, V, 64, 8>();
-    case 1024: return f.template operator()<T, V, 64, 16>();
-    case 2048: return f.template operator()<T, V, 256, 8>();
-    case 4096: return f.template operator()<T, V, 256, 16>();
-    case 5120: return f.template operator()<T, V, 320, 16>();
-    case 6144: return f.template operator()<T, V, 384, 16>();
-    case 8192: return f.template operator()<T, V, 512, 16>();
-    case 12288: return f.template operator()<T, V, 768, 16>();
-    default: return f.template operator()<T, V, 1024, 16>();
+    case 128: return f.template operator()<T, V, kWide, 16, 8>();
+    case 512: return f.template operator()<T, V, kWide, 64, 8>();
+    case 1024: return f.template operator()<T, V, kWide, 64, 16>();
+    case 2048: return f.template operator()<T, V, kWide, 256, 8>();
+    case 4096: return f.template operator()<T, V, kWide, 256, 16>();
+    case 5120: return f.template operator()<T, V, kWide, 320, 16>();
+    case 6144: return f.template operator()<T, V, kWide, 384, 16>();
+    case 8192: return f.template operator()<T, V, kWide, 512, 16>();
+    case 12288: return f.template operator()<T, V, kWide, 768, 16>();
+    default: return f.template operator()<T, V, kWide, 1024, 16>();
   }
 }
 template <typename F>
 hipError_t with_type(Elem type, bool wide, int D, F&& f) {
   switch (type) {
-    case Elem::kBf16: return wide ? with_shape<Bf16, 8>(D, f) : with_shape<Bf16, 1>(D, f);
-    case Elem::kFp16: return wide ? with_shape<Fp16, 8>(D, f) : with_shape<Fp16, 1>(D, f);
-    default: return wide ? with_shape<float, 4>(D, f) : with_shape<float, 1>(D, f);
+    case Elem::kBf16: return wide ? with_shape<Bf16, 8, true>(D, f) : with_shape<Bf16, 8, false>(D, f);
+    case Elem::kFp16: return wide ? with_shape<Fp16, 8, true>(D, f) : with_shape<Fp16, 8, false>(D, f);
+    default: return wide ? with_shape<float, 4, true>(D, f) : with_shape<float, 4, false>(D, f);
   }
 }
 
@@ -339,9 +351,9 @@ constexpr int kBwdBlocks = 1024;  // 16384 x 4096 rows: 109 us, and 120 with 768
 struct Fwd {
   const NormArgs& a;
   hipStream_t s;
-  template <typename T, int V, int GROUP, int E>
+  template <typename T, int V, bool kWide, int GROUP, int E>
   hipError_t operator()() {
-    hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, V, GROUP, E>), dim3((unsigned)blocks_of(a.rows, a.D)),
+    hipLaunchKernelGGL((rmsnorm_fwd_kernel<T, V, kWide, GROUP, E>), dim3((unsigned)blocks_of(a.rows, a.D)),
                        dim3(GROUP > 256 ? GROUP : 256), 0, s, a);
     return hipGetLastError();
   }
@@ -349,10 +361,10 @@ struct Fwd {
 struct Bwd {
   const NormGradArgs& a;
   hipStream_t s;
-  template <typename T, int V, int GROUP, int E>
+  template <typename T, int V, bool kWide, int GROUP, int E>
   hipError_t operator()() {
     const int blocks = norm_partials(a.rows, a.D) / rows_at_once(a.D);
-    hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, V, GROUP, E>), dim3(blocks), dim3(GROUP > 256 ? GROUP : 256), 0, s,
+    hipLaunchKernelGGL((rmsnorm_bwd_kernel<T, V, kWide, GROUP, E>), dim3(blocks), dim3(GROUP > 256 ? GROUP : 256), 0, s,
                        a, blocks * rows_at_once(a.D));
     return hipGetLastError();
   }

@@ -17,10 +17,10 @@ namespace gdn {
 
 namespace {
 
-// Tokens per workgroup where one token's pieces would leave most of its 256 threads
-// idle (at most 64 pieces; one wave then makes a token's angles). 16384 tokens of 4 +
-// 1 heads of 64 columns, 20 pieces: 8.1 us, and 12.2 with one token; 32 + 32 heads
-// of 128, 512 pieces: 113 us, and 100 with one; 256 tokens of these: 7.5 and 4.3.
+// Tokens per workgroup where one token's units would leave most of its 256 threads
+// idle (at most 64 units; one wave then makes a token's angles). 16384 tokens of 4 +
+// 1 heads of 64 columns, 20 units: 8.1 us, and 12.2 with one token; 32 + 32 heads
+// of 128, 512 units: 113 us, and 100 with one; 256 tokens of these: 7.5 and 4.3.
 constexpr int kTok = 4;
 
 struct TokenAt {
@@ -44,50 +44,70 @@ __device__ __forceinline__ TokenAt token_at(const RotaryArgs& a, int t) {
   return {(int64_t)(t - b) + (a.offsets ? a.offsets[lo] : 0), t >= b && t < a.cu[lo + 1]};
 }
 
-// columns of a turning unit
+// Units of a head row, 16 bytes (V columns) each: those of the turning columns, or
+// of their first half, whose unit takes the same columns of the second half with it,
+// and those of the copied columns.
 template <int V, bool kInter>
-constexpr int columns_of = kInter ? (V > 1 ? V : 2) : 2 * V;
+__host__ __device__ __forceinline__ int turning_units(int R) {
+  return ((kInter ? R : R / 2) + V - 1) / V;
+}
+template <int V>
+__host__ __device__ __forceinline__ int copied_units(int D, int R) {
+  return (D - R + V - 1) / V;
+}
 
-// Unit u of a head row: V pairs (two loads of V columns, or with interleaved
-// pairs one load of V columns), or V copied columns.
-template <typename T, int V, bool kInter>
-__device__ __forceinline__ void unit(const T* in, T* out, const float2* cs, int u, int turning, int R) {
-  if (u < turning) {
-    if constexpr (kInter) {
-      constexpr int W = columns_of<V, true>;
-      float x[W], y[W];
-      load_n<T, W>(in + u * W, x);
-#pragma unroll
-      for (int i = 0; i < W; i += 2) {
-        const float2 c = cs[(u * W + i) / 2];
-        y[i] = x[i] * c.x - x[i + 1] * c.y;
-        y[i + 1] = x[i] * c.y + x[i + 1] * c.x;
-      }
-      store_n<T, W>(out + u * W, y);
-    } else {
-      float x0[V], x1[V], y0[V], y1[V];
-      load_n<T, V>(in + u * V, x0);
-      load_n<T, V>(in + R / 2 + u * V, x1);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 c = cs[u * V + i];
-        y0[i] = x0[i] * c.x - x1[i] * c.y;
-        y1[i] = x0[i] * c.y + x1[i] * c.x;
-      }
-      store_n<T, V>(out + u * V, y0);
-      store_n<T, V>(out + R / 2 + u * V, y1);
-    }
-  } else {
+template <typename T, int V, bool kWide>
+__device__ __forceinline__ void load_unit(const T* row, int c, int n, float* x) {
+  if constexpr (kWide) load_n<T, V>(row + c, x);
+  else load_any<T, V>(row, c, n, x);
+}
+template <typename T, int V, bool kWide>
+__device__ __forceinline__ void store_unit(T* row, int c, int n, const float* x) {
+  if constexpr (kWide) store_n<T, V>(row + c, x);
+  else store_any<T, V>(row, c, n, x);
+}
+
+// Unit u of a head row. (In place, load_any may read columns that another unit is
+// writing; it drops those.)
+template <typename T, int V, bool kInter, bool kWide>
+__device__ __forceinline__ void unit(const T* in, T* out, const float2* cs, int u, int turning, int D, int R) {
+  if (u >= turning) {
+    const int c = (u - turning) * V;
     float x[V];
-    const int c = R + (u - turning) * V;
-    load_n<T, V>(in + c, x);
-    store_n<T, V>(out + c, x);
+    load_unit<T, V, kWide>(in + R, c, D - R, x);
+    store_unit<T, V, kWide>(out + R, c, D - R, x);
+    return;
+  }
+  const int c = u * V;
+  const auto turn = [&](int j) { return cs[kWide ? j : min(j, R / 2 - 1)]; };
+  if constexpr (kInter) {
+    float x[V], y[V];
+    load_unit<T, V, kWide>(in, c, R, x);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 t = turn(u * (V / 2) + i / 2);
+      y[i] = x[i] * t.x - x[i + 1] * t.y;
+      y[i + 1] = x[i] * t.y + x[i + 1] * t.x;
+    }
+    store_unit<T, V, kWide>(out, c, R, y);
+  } else {
+    float x0[V], x1[V], y0[V], y1[V];
+    load_unit<T, V, kWide>(in, c, R / 2, x0);
+    load_unit<T, V, kWide>(in + R / 2, c, R / 2, x1);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 t = turn(c + i);
+      y0[i] = x0[i] * t.x - x1[i] * t.y;
+      y1[i] = x0[i] * t.y + x1[i] * t.x;
+    }
+    store_unit<T, V, kWide>(out, c, R / 2, y0);
+    store_unit<T, V, kWide>(out + R / 2, c, R / 2, y1);
   }
 }
 
 }  // namespace
 
-template <typename T, int V, bool kInter, int kTokens>
+template <typename T, int V, bool kInter, bool kWide, int kTokens>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
   extern __shared__ float2 cs[];  // [kTokens][R / 2]
   __shared__ bool live[kTokens];
@@ -106,8 +126,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     }
   }
   __syncthreads();
-  constexpr int W = columns_of<V, kInter>;
-  const int turning = a.R / W, units = turning + (a.D - a.R) / V;
+  const int turning = turning_units<V, kInter>(a.R), units = turning + copied_units<V>(a.D, a.R);
   const int heads = a.q.heads + a.k.heads, n = units * heads;
   for (int i = tid; i < n * kTokens; i += 256) {
     const int tok = i / n, rest = i - tok * n, head = rest / units, u = rest - head * units;
@@ -119,29 +138,28 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
     const T* in = static_cast<const T*>(r.in) + t * r.in_stride + (int64_t)h * a.D;
     T* out = static_cast<T*>(r.out) + t * r.out_stride + (int64_t)h * a.D;
     if (u >= turning && in == out) continue;  // in place: nothing to copy
-    unit<T, V, kInter>(in, out, cs + tok * pairs, u, turning, a.R);
+    unit<T, V, kInter, kWide>(in, out, cs + tok * pairs, u, turning, a.D, a.R);
   }
 }
 
 namespace {
 
-template <typename T, int V, bool kInter>
+template <typename T, bool kInter, bool kWide>
 hipError_t rotary_of(const RotaryArgs& a, hipStream_t s) {
+  constexpr int V = 16 / sizeof(T);
   const size_t lds = sizeof(float2) * (a.R / 2);
-  constexpr int W = columns_of<V, kInter>;
-  const int64_t pieces = (int64_t)(a.R / W + (a.D - a.R) / V) * (a.q.heads + a.k.heads);
-  if (pieces * kTok <= 256)
-    hipLaunchKernelGGL((rotary_kernel<T, V, kInter, kTok>), dim3((a.T + kTok - 1) / kTok), dim3(256), kTok * lds, s, a);
+  const int64_t units = turning_units<V, kInter>(a.R) + copied_units<V>(a.D, a.R);
+  if (units * (a.q.heads + a.k.heads) * kTok <= 256)
+    hipLaunchKernelGGL((rotary_kernel<T, V, kInter, kWide, kTok>), dim3((a.T + kTok - 1) / kTok), dim3(256), kTok * lds, s, a);
   else
-    hipLaunchKernelGGL((rotary_kernel<T, V, kInter, 1>), dim3(a.T), dim3(256), lds, s, a);
+    hipLaunchKernelGGL((rotary_kernel<T, V, kInter, kWide, 1>), dim3(a.T), dim3(256), lds, s, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t rotary_type(bool inter, bool wide, const RotaryArgs& a, hipStream_t s) {
-  constexpr int V = 16 / sizeof(T);
-  if (inter) return wide ? rotary_of<T, V, true>(a, s) : rotary_of<T, 1, true>(a, s);
-  return wide ? rotary_of<T, V, false>(a, s) : rotary_of<T, 1, false>(a, s);
+  if (inter) return wide ? rotary_of<T, true, true>(a, s) : rotary_of<T, true, false>(a, s);
+  return wide ? rotary_of<T, false, true>(a, s) : rotary_of<T, false, false>(a, s);
 }
 
 }  // namespace

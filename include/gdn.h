@@ -533,9 +533,8 @@ typedef enum { GDN_BF16 = 0, GDN_FP16 = 1, GDN_FP32 = 2 } gdn_dtype;
  *   strides     elements from one token to the next (its heads are dense), 0
  *               for dense rows; below 2^31
  * In place is allowed (q_out = q with the same stride, likewise k); otherwise
- * an output overlaps no input. Rows of 16-byte aligned pieces (pointers,
- * strides, D and the turning half) are read 16 bytes at a time, any others
- * element by element. */
+ * an output overlaps no input. Fastest with rows of 16-byte aligned pieces
+ * (pointers, strides, D and the turning half). */
 typedef struct {
   int32_t T, HQ, HK, D, R, interleaved, dtype;
   float mscale;

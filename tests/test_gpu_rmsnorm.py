@@ -117,6 +117,31 @@ def test_in_place_and_nothing_leaks_between_rows():
     assert bool(got["scales"][keep].isfinite().all()) and bool(got["y8"][5].float().isnan().all())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("D", [1, 3, 7, 9, 131, 1325, 4094])
+def test_odd_rows_in_place_end_where_they_end(D, dtype):
+    """The last piece of an odd row: in place as out of place, and nothing behind the last row is written."""
+    rows = 21
+    x, r = make(rows, D, dtype, 1), make(rows, D, dtype, 2)
+    want = gdn.rmsnorm_fwd(x, residual=r, quant=128, want_y=True, want_rstd=True)
+    for offset in (0, 1):
+        buf = torch.full((rows * D + 40,), 7.0, dtype=dtype, device="cuda")
+        a = buf[offset:offset + rows * D].view(rows, D)
+        a.copy_(x)
+        got = gdn.rmsnorm_fwd(a, residual=r, residual_out=a, quant=128, want_y=True, want_rstd=True)
+        assert torch.equal(a, want["residual_out"])
+        for n in ("y", "scales", "rstd"):
+            assert torch.equal(got[n], want[n]), n
+        assert torch.equal(got["y8"].view(torch.uint8), want["y8"].view(torch.uint8))
+        assert bool((buf[offset + rows * D:] == 7).all()) and bool((buf[:offset] == 7).all())
+    dy, w = make(rows, D, dtype, 3), make(1, D, dtype, 4)[0]
+    g = gdn.rmsnorm_bwd(dy, want["residual_out"], w, want["rstd"])
+    odd = torch.empty(rows * D + 1, dtype=dtype, device="cuda")[1:].view(rows, D)
+    odd.copy_(dy)
+    h = gdn.rmsnorm_bwd(odd, want["residual_out"], w, want["rstd"])
+    assert torch.equal(g["dx"], h["dx"]) and torch.equal(g["dweight"], h["dweight"])
+
+
 def test_empty_rows():
     x, w = torch.empty(0, 64, dtype=torch.float16, device="cuda"), torch.ones(64, dtype=torch.float16, device="cuda")
     out = gdn.rmsnorm_fwd(x, w, residual=x, quant=128, want_rstd=True)

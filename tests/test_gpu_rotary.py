@@ -158,3 +158,23 @@ def test_many_sequences():
     assert none is None
     empty, _ = gdn.rotary(q[:0], None, f, positions=torch.empty(0, dtype=torch.int32, device="cuda"))
     assert empty.shape == (0, 1, 16)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("D,R", [(90, 90), (65, 30), (11, 10), (3, 2), (40, 18), (257, 34)])
+def test_odd_heads_in_place_end_where_they_end(D, R, dtype, interleaved):
+    """The last piece of an odd head: in place as out of place, and nothing between the rows is written."""
+    T, H = 19, 3
+    gen = torch.Generator().manual_seed(D)
+    f = gdn.rotary_inv_freq(R, device="cuda")[0]
+    pos = torch.randint(0, 4000, (T,), generator=gen, dtype=torch.int32).cuda()
+    x = rows(T, H, D, dtype, gen, 0)
+    want, _ = gdn.rotary(x, None, f, positions=pos, interleaved=interleaved)
+    close(want, f64(x), Y.rotary(f64(x), pos.cpu().numpy(), f64(f), interleaved), 1.0)
+    for pad in (1, 5):
+        buf = torch.full((T, H * D + pad), 7.0, dtype=dtype, device="cuda")
+        a = buf[:, :H * D].unflatten(1, (H, D))
+        a.copy_(x)
+        gdn.rotary(a, None, f, positions=pos, q_out=a, interleaved=interleaved)
+        assert torch.equal(a, want) and bool((buf[:, H * D:] == 7).all())
