@@ -328,3 +328,39 @@ def test_many_sequences():
     check(part, keep)
     empty = [i for i, n in enumerate(lens) if n == 0]
     assert torch.equal(got["hT"][empty].cpu(), x["h0"][empty]) and torch.equal(got["dh0"][empty].cpu(), x["dhT"][empty])
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements of v, o, dO and dv: the last sequence's rows are those of the sequence alone."""
+    H, HV, D, tail = 2, 256, 128, 90
+    T = 65560 + tail
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    q, k = (torch.randn(T, H, D, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    v, dO = (torch.randn(T, HV, D, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    assert v.numel() > 2 ** 31
+    g = -torch.exp(torch.linspace(-6, 0, HV, device="cuda"))
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32, device="cuda")
+    o, hT, saved = gdn.linear_fwd(q, k, v, g, cu, save_for_backward=True)
+    b = gdn.linear_bwd(q, k, v, g, cu, saved, dO)
+    del saved
+    one = torch.tensor([0, tail], dtype=torch.int32, device="cuda")
+    q, k, v, dO = (x[-tail:].contiguous() for x in (q, k, v, dO))
+    o1, hT1, saved = gdn.linear_fwd(q, k, v, g, one, save_for_backward=True)
+    b1 = gdn.linear_bwd(q, k, v, g, one, saved, dO)
+    assert torch.equal(o[-tail:], o1) and torch.equal(hT[1:], hT1) and torch.equal(b["dh0"][1:], b1["dh0"])
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(b[n][-tail:], b1[n]), n
+
+
+def test_step_in_a_pool_past_32_bits():
+    HV, D, slots = 32, 128, 4100
+    pool = torch.empty(slots, HV, D, D, device="cuda")
+    assert pool.numel() > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.randn(2, HV, D, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    g = torch.full((HV,), -0.1, device="cuda")
+    small = torch.randn(3, HV, D, D, generator=gen, device="cuda")
+    pool[[1, slots - 1]] = small[1:]
+    o = gdn.linear_step(q, k, v, g, pool, torch.tensor([slots - 1, 1], dtype=torch.int32, device="cuda"))
+    want = gdn.linear_step(q, k, v, g, small, torch.tensor([2, 1], dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, want) and torch.equal(pool[[1, slots - 1]], small[1:])

@@ -224,3 +224,20 @@ def test_overflowing_and_tiny_rows():
     assert np.allclose(f64(out["scales"])[1:], sc, rtol=2.0 ** -18, atol=0)
     assert bool((out["y8"][1].float()[[3]] == 448).all()) or y[0, 3] < 2.0 ** -100
     assert bool((out["y8"][2].float()[:128] == 448).all()) and bool(out["y8"].float().isfinite().all())
+
+
+def test_rows_past_32_bits():
+    rows, D = 2 ** 19 + 7, 4100
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x, dy = (torch.randn(rows, D, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    assert x.numel() > 2 ** 31
+    w = torch.randn(D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    keep = 9
+    a = gdn.rmsnorm_fwd(x, w, quant=128, want_y=True, want_rstd=True)
+    b = gdn.rmsnorm_fwd(x[-keep:], w, quant=128, want_y=True, want_rstd=True)
+    for n in ("y", "scales", "rstd"):
+        assert torch.equal(a[n][-keep:], b[n]), n
+    assert torch.equal(a["y8"][-keep:].view(torch.uint8), b["y8"].view(torch.uint8))
+    g = gdn.rmsnorm_bwd(dy, x, w, a["rstd"])
+    h = gdn.rmsnorm_bwd(dy[-keep:], x[-keep:], w, b["rstd"])
+    assert torch.equal(g["dx"][-keep:], h["dx"]) and bool(g["dweight"].isfinite().all())

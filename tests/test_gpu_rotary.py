@@ -178,3 +178,15 @@ def test_odd_heads_in_place_end_where_they_end(D, R, dtype, interleaved):
         a.copy_(x)
         gdn.rotary(a, None, f, positions=pos, q_out=a, interleaved=interleaved)
         assert torch.equal(a, want) and bool((buf[:, H * D:] == 7).all())
+
+
+def test_rows_past_32_bits():
+    T, H, D = 2 ** 20 + 3, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(T, H, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    assert q.numel() > 2 ** 31
+    f = gdn.rotary_inv_freq(D, device="cuda")[0]
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    out, _ = gdn.rotary(q, None, f, positions=pos)
+    last, _ = gdn.rotary(q[-50:].contiguous(), None, f, positions=pos[-50:].contiguous())
+    assert torch.equal(out[-50:], last)
