@@ -57,8 +57,8 @@ hipError_t launch_lin_join(int D, bool back, const LinCut& cut, const float* log
                            float* states, hipStream_t stream);
 
 // dq[t][h] = sum over the key head's G value heads of wq[t][h G + i], to bf16; dk likewise.
-hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wq, const float* wk, uint16_t* dq,
-                           uint16_t* dk, hipStream_t stream);
+hipError_t launch_lin_fold(int D, const LinCut& cut, const float* wq, const float* wk, uint16_t* dq, uint16_t* dk,
+                           hipStream_t s);
 
 hipError_t launch_lin_step(int D, int N, int HV, float scale, const LinRows& q, const LinRows& k,
                            const LinRows& v, const float* log_decay, float* pool, int slots,

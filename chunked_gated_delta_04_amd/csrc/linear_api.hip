@@ -259,7 +259,7 @@ GDN_API int gdn_linear_bwd(const gdn_linear_problem* p, const uint16_t* q, const
     GDN_TRY(launch_lin_join(D, true, cut, log_decay, io, ends, s));
   }
   GDN_TRY(launch_lin_grad(D, wide, cut, log_decay, scale, pq, pv, pk, s));
-  if (wide && p->T > 0) GDN_TRY(launch_lin_fold(D, p->T, p->H, G, wq, wk, dq, dk, s));
+  if (wide && p->T > 0) GDN_TRY(launch_lin_fold(D, cut, wq, wk, dq, dk, s));
   return GDN_OK;
 }
 

@@ -720,12 +720,14 @@ __global__ __launch_bounds__(64) void lin_join_kernel(LinCut cut, const float* _
 // dq and dk (blockIdx.y). Bound by HBM: 16384 tokens, 16 key and 32 value heads, 127
 // us, 5.3 TB/s. The value heads' parts are fp32: rounding each to bf16 would add an
 // error of the size of the result's own.
-__global__ __launch_bounds__(256) void lin_fold_kernel(int64_t n, int DH, int G, int D,
+__global__ __launch_bounds__(256) void lin_fold_kernel(LinCut cut, int DH, int D,
                                                        const float* __restrict__ wq, const float* __restrict__ wk,
                                                        uint16_t* __restrict__ dq, uint16_t* __restrict__ dk) {
   const float* wide = blockIdx.y ? wk : wq;
   uint16_t* out = blockIdx.y ? dk : dq;
-  // n pieces of 4 outputs; DH = H * D outputs a token
+  const int G = cut.G;
+  // pieces of 4 outputs; DH = H * D outputs a token. Rows of no sequence have no parts and stay as they were.
+  const int64_t n = (int64_t)min(max(cut.cu[cut.N], 0), cut.T) * DH / 4;
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     const int64_t e = i * 4, t = e / DH;
     const int rest = (int)(e - t * DH), h = rest / D, d = rest - h * D;
@@ -788,11 +790,12 @@ hipError_t launch_lin_join(int D, bool back, const LinCut& cut, const float* log
   return hipGetLastError();
 }
 
-hipError_t launch_lin_fold(int D, int T, int H, int G, const float* wq, const float* wk, uint16_t* dq, uint16_t* dk,
+hipError_t launch_lin_fold(int D, const LinCut& cut, const float* wq, const float* wk, uint16_t* dq, uint16_t* dk,
                            hipStream_t s) {
-  const int64_t n = (int64_t)T * H * D / 4;
+  const int DH = cut.HV / cut.G * D;
+  const int64_t n = (int64_t)cut.T * DH / 4;
   const unsigned blocks = (unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
-  hipLaunchKernelGGL(lin_fold_kernel, dim3(blocks, 2), dim3(256), 0, s, n, H * D, G, D, wq, wk, dq, dk);
+  hipLaunchKernelGGL(lin_fold_kernel, dim3(blocks, 2), dim3(256), 0, s, cut, DH, D, wq, wk, dq, dk);
   return hipGetLastError();
 }
 

@@ -487,7 +487,8 @@ int gdn_linear_fwd_paged(const gdn_linear_problem* p, const uint16_t* q, const u
  *   dq, dk    bf16 [T, H, K]; dv bf16 [T, HV, V] (dense)
  *   dh0       fp32 [N, HV, V, K] cotangent of h0, or NULL to skip
  * The value heads of one key head are summed into dq, dk in fp32 in a fixed
- * order; no atomics. No output overlaps an input or another output (dh0 is not
+ * order; no atomics. Rows of dq, dk, dv at or past cu_seqlens[N] are left as
+ * they were. No output overlaps an input or another output (dh0 is not
  * dhT). Errors: as gdn_linear_fwd, GDN_ERR_NULL for saved, dO,
  * dq, dk, dv. */
 int gdn_linear_bwd(const gdn_linear_problem* p, const uint16_t* q, const uint16_t* k,

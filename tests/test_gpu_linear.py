@@ -213,6 +213,44 @@ def test_rows_behind_the_last_sequence_stay():
     assert torch.equal(o[:66], want) and bool((o[66:] == 7.0).all())
 
 
+@pytest.mark.parametrize("H", [2, 1])
+@pytest.mark.parametrize("lens", [[50, 16], [700, 3]])
+def test_gradients_of_rows_behind_the_last_sequence_stay(lens, H):
+    import ctypes
+    used, T = sum(lens), sum(lens) + 24
+    x = inputs(lens[:1] + [lens[1] + 24], H, 2, 64, seed=9)
+    d = dev(x)
+    cu = torch.tensor([0, lens[0], used], dtype=torch.int32, device="cuda")  # the last 24 rows belong to nobody
+    p = gdn.make_linear_problem(2, T, H, 2, 64, cu)
+    s = torch.cuda.current_stream().cuda_stream
+    saved, ws = (torch.full((n + 16,), 255, dtype=torch.uint8, device="cuda")  # NaN as fp32
+                 for n in (gdn.gdn_linear_saved_size(p), gdn.gdn_linear_bwd_workspace_size(p)))
+    o = torch.empty_like(d["v"])
+    ptrs = [ctypes.byref(p)] + [d[n].data_ptr() for n in ("q", "k", "v", "log_decay")]
+    assert gdn._lib.gdn_linear_fwd(*ptrs, None, o.data_ptr(), None, saved.data_ptr(), ws.data_ptr(), ws.numel(), s) == 0
+    dq, dk, dv = (torch.full_like(d[n], 7.0) for n in ("q", "k", "v"))
+    assert gdn._lib.gdn_linear_bwd(*ptrs, saved.data_ptr(), d["dO"].data_ptr(), None, dq.data_ptr(), dk.data_ptr(),
+                                   dv.data_ptr(), None, ws.data_ptr(), ws.numel(), s) == 0
+    q, k, v, dO = (d[n][:used] for n in ("q", "k", "v", "dO"))
+    _, _, saved = gdn.linear_fwd(q, k, v, d["log_decay"], cu, save_for_backward=True)
+    want = gdn.linear_bwd(q, k, v, d["log_decay"], cu, saved, dO)
+    for name, got in (("dq", dq), ("dk", dk), ("dv", dv)):
+        assert torch.equal(got[:used], want[name]) and bool((got[used:] == 7.0).all()), name
+
+
+def test_two_streams_at_once():
+    xs = [inputs([500, 64, 1, 3000], 2, 4, 64, seed=s) for s in (10, 11)]
+    ds = [dev(x) for x in xs]
+    want = [run(x, d) for x, d in zip(xs, ds)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = [run(x, d, stream=s) for x, d, s in zip(xs, ds, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(g[n], w[n]) for n in w)
+
+
 def test_nothing_leaks_between_sequences():
     x = inputs([70, 64, 70], 1, 1, 64, seed=6)
     d = dev(x)
