@@ -15,7 +15,7 @@ struct LinRows {
 
 // How a pack is cut into segments that run side by side: segment i of
 // sequence n covers tokens [i S, (i + 1) S) of it and has the slot
-// cu[n] / S + n + i, so that a slot's sequence follows from cu_seqlens alone
+// cu[n] / S + n + i, so that a segment's place follows from cu_seqlens alone
 // and T / S + N slots hold every pack. S is a multiple of the 64-token chunk.
 struct LinCut {
   const int32_t* cu;

@@ -38,32 +38,44 @@ __device__ __forceinline__ float decay2(float log_decay) {
 }
 __device__ __forceinline__ float power(float g2, int n) { return exp2_fast(g2 * (float)n); }
 
-// One segment: its sequence, the sequence's bounds and the segment's.
+// One segment: its sequence, the sequence's bounds and its own, its number in the
+// sequence and its slot.
 struct Segment {
-  int seq, bos, eos, t0, t1, index;
+  int seq, bos, eos, t0, t1, index, slot;
 };
 
-// The sequence of a segment slot: the last n whose first slot cu[n] / S + n is
-// at or before it, by all lanes of a wave together (64 probes a step).
+// The segment of number i in the order of the work: first the N sequences' first
+// ones, then the others by position. Segment j > 0 of sequence n has the number
+// N + cu[n] / S + j - 1, so its sequence is the last n with cu[n] / S at or before
+// i - N, found by all lanes of a wave together (64 probes a step). The numbers that
+// no segment has are among the last, and leave no gaps between the workgroups that
+// start together: 16 x 512 tokens, 8 heads of 128, forward and backward 104 us, and
+// 143 in the order of the slots, where every other one is empty.
 // Boundaries are clamped to [0, T], so a bad one never leads out of range.
-__device__ __forceinline__ Segment find_segment(const LinCut& c, int slot) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, cnt = c.N;
-  while (cnt > 1) {
-    const int step = (cnt + 63) >> 6;
-    const int at = lane * step;
-    bool ok = false;
-    if (at < cnt) ok = min(max(c.cu[lo + at], 0), c.T) / c.S + lo + at <= slot;
-    const int k = max(__popcll(__ballot(ok)) - 1, 0);
-    lo += k * step;
-    cnt = min(step, cnt - k * step);
+__device__ __forceinline__ Segment find_segment(const LinCut& c, int i) {
+  int lo = i;
+  if (i >= c.N) {
+    const int lane = threadIdx.x & 63;
+    int cnt = c.N;
+    lo = 0;
+    while (cnt > 1) {
+      const int step = (cnt + 63) >> 6;
+      const int at = lane * step;
+      bool ok = false;
+      if (at < cnt) ok = min(max(c.cu[lo + at], 0), c.T) / c.S <= i - c.N;
+      const int k = max(__popcll(__ballot(ok)) - 1, 0);
+      lo += k * step;
+      cnt = min(step, cnt - k * step);
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
   Segment s;
   s.seq = lo;
   s.bos = min(max(c.cu[lo], 0), c.T);
   s.eos = min(max(c.cu[lo + 1], s.bos), c.T);
-  s.index = slot - (s.bos / c.S + lo);
+  s.index = i < c.N ? 0 : i - c.N - s.bos / c.S + 1;
+  if (i >= c.N && s.index < 1) s.index = -1;  // bad boundaries
+  s.slot = s.bos / c.S + lo + s.index;
   const int64_t t0 = s.bos + (int64_t)s.index * c.S;
   s.t0 = (int)min(t0, (int64_t)c.T);
   s.t1 = (int)min(t0 + c.S, (int64_t)s.eos);
@@ -72,7 +84,7 @@ __device__ __forceinline__ Segment find_segment(const LinCut& c, int slot) {
 // whether it is its whole sequence
 __device__ __forceinline__ bool whole(const Segment& s) { return s.index == 0 && s.t1 >= s.eos; }
 __device__ __forceinline__ int chunks_of(const Segment& s) { return (s.t1 - s.t0 + kChunk - 1) / kChunk; }
-// whether the slot holds a segment: each sequence, an empty one too, has its first
+// whether the number has no segment: each sequence, an empty one too, has its first
 __device__ __forceinline__ bool unused(const Segment& s) {
   return s.index < 0 || (s.index > 0 && s.t0 >= s.eos);
 }
@@ -351,14 +363,14 @@ __device__ __forceinline__ Tile tile_of(int wave, int n) {
 // 14 % longer than the others: gradients of 2 x 8192 tokens, 32 heads, 300 us, and
 // 286 with it.
 struct Item {
-  int slot, hv, part;
+  int seg, hv, part;
 };
 __device__ __forceinline__ Item item_of(const LinCut& cut, int n, int parts) {
   const int H = cut.HV / cut.G, sharing = parts * cut.G;
   const int nth = n >> 3, r = nth % sharing, m = nth / sharing * 8 + (n & 7);
   if (m >= cut.slots * H) return {-1, 0, 0};
-  const int slot = m / H;
-  return {slot, (m + slot) % H * cut.G + r / parts, r % parts};
+  const int seg = m / H;
+  return {seg, (m + seg) % H * cut.G + r / parts, r % parts};
 }
 unsigned items_grid(const LinCut& cut, int parts) {
   return ((unsigned)cut.slots * (unsigned)(cut.HV / cut.G) + 7) / 8 * 8 * (unsigned)(parts * cut.G);
@@ -387,7 +399,7 @@ struct PassLds {
 // to bf16, and 16 bits of what it gathers are enough (a third less matrix work);
 // what a sequence of several segments ends with is lin_join's.
 template <int D, bool kBack, bool kT, bool kWide, bool kEnds>
-__device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, const Segment& sg,
+__device__ __forceinline__ void lin_pass(const LinCut& cut, int hv, const Segment& sg,
                                          const float* __restrict__ log_decay, float scale, const LinPass& p,
                                          PassLds<D>& lds) {
   constexpr int NW = D / 32, NT = 64 * NW, kTiles = kTilesOf<NW>;
@@ -403,7 +415,7 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int slot, int hv, co
   const StateAt state = state_at(p.io, sg.seq, hv, cut.HV, D * D);
   const int col = 32 * wave + l32;
   State<D> X;
-  X.template load<kT>(p.start ? p.start + ((size_t)slot * cut.HV + hv) * (D * D) : state.from, col, hi);
+  X.template load<kT>(p.start ? p.start + ((size_t)sg.slot * cut.HV + hv) * (D * D) : state.from, col, hi);
 
   const int chunks = chunks_of(sg);
   // the decays of this lane's elements of P do not change from chunk to chunk
@@ -584,11 +596,11 @@ __global__ __launch_bounds__(2 * D, 2) void lin_out_kernel(LinCut cut, const flo
                                                            float scale, LinPass p) {
   __shared__ __align__(16) PassLds<D> lds;
   const Item it = item_of(cut, blockIdx.x, 1);
-  if (it.slot < 0) return;
-  const Segment sg = find_segment(cut, it.slot);
+  if (it.seg < 0) return;
+  const Segment sg = find_segment(cut, it.seg);
   if (unused(sg)) return;
-  if (whole(sg)) lin_pass<D, false, false, false, true>(cut, it.slot, it.hv, sg, log_decay, scale, p, lds);
-  else lin_pass<D, false, false, false, false>(cut, it.slot, it.hv, sg, log_decay, scale, p, lds);
+  if (whole(sg)) lin_pass<D, false, false, false, true>(cut, it.hv, sg, log_decay, scale, p, lds);
+  else lin_pass<D, false, false, false, false>(cut, it.hv, sg, log_decay, scale, p, lds);
 }
 
 // What a segment adds to the state, from a zero start: sum over its tokens of
@@ -599,13 +611,13 @@ __global__ __launch_bounds__(2 * D, 2) void lin_out_kernel(LinCut cut, const flo
 // HBM: 16384 tokens, 32 heads, 60 to 66 us for 262 MB (4.2 TB/s; 16 steps, the first
 // of which waits for its rows).
 template <int D, bool kBack>
-__device__ __forceinline__ void lin_gather(const LinCut& cut, int slot, int hv, const float* __restrict__ log_decay,
+__device__ __forceinline__ void lin_gather(const LinCut& cut, int seg, int hv, const float* __restrict__ log_decay,
                                            float scale, const LinRows& b, const LinRows& c,
                                            bool ends, float* __restrict__ states, PassLds<D>& lds) {
   constexpr int NW = D / 32, NT = 64 * NW;
   uint16_t *Bs = lds.Bs, *Cs = lds.Cs;
   float* ws = lds.ws;
-  const Segment sg = find_segment(cut, slot);
+  const Segment sg = find_segment(cut, seg);
   if (unused(sg) || whole(sg) || (!ends && (kBack ? sg.index == 0 : sg.t1 >= sg.eos))) return;  // nothing needs it
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const float g2 = decay2(log_decay[hv]);
@@ -645,7 +657,7 @@ __device__ __forceinline__ void lin_gather(const LinCut& cut, int slot, int hv, 
     load_columns<D>(cc, Cs, L);
     gather_chunk<D, 3>(X, Bs, cc, ws, L, lane >> 5);
   }
-  X.template store<false>(states + ((size_t)slot * cut.HV + hv) * (D * D), 32 * wave + (lane & 31), lane >> 5);
+  X.template store<false>(states + ((size_t)sg.slot * cut.HV + hv) * (D * D), 32 * wave + (lane & 31), lane >> 5);
 }
 
 template <int D, bool kBack>
@@ -654,7 +666,7 @@ __global__ __launch_bounds__(2 * D, 2) void lin_gather_kernel(LinCut cut, const 
                                                               float* __restrict__ states) {
   __shared__ __align__(16) PassLds<D> lds;
   const Item it = item_of(cut, blockIdx.x, 1);
-  if (it.slot >= 0) lin_gather<D, kBack>(cut, it.slot, it.hv, log_decay, scale, b, c, ends, states, lds);
+  if (it.seg >= 0) lin_gather<D, kBack>(cut, it.seg, it.hv, log_decay, scale, b, c, ends, states, lds);
 }
 
 // The three gradients' passes in one launch (see item_of): the rows that dv's and
@@ -664,14 +676,14 @@ __global__ __launch_bounds__(2 * D, 2) void lin_grad_kernel(LinCut cut, const fl
                                                             float scale, LinPass dq, LinPass dv, LinPass dk) {
   __shared__ __align__(16) PassLds<D> lds;
   const Item it = item_of(cut, blockIdx.x, 3);
-  if (it.slot < 0) return;
-  const int slot = it.slot, hv = it.hv, part = it.part;
-  const Segment sg = find_segment(cut, slot);
+  if (it.seg < 0) return;
+  const int hv = it.hv, part = it.part;
+  const Segment sg = find_segment(cut, it.seg);
   if (unused(sg)) return;
-  if (part == 1) lin_pass<D, true, true, kWide, false>(cut, slot, hv, sg, log_decay, scale, dk, lds);
-  else if (part == 2) lin_pass<D, false, true, kWide, false>(cut, slot, hv, sg, log_decay, scale, dq, lds);
-  else if (whole(sg)) lin_pass<D, true, false, false, true>(cut, slot, hv, sg, log_decay, scale, dv, lds);
-  else lin_pass<D, true, false, false, false>(cut, slot, hv, sg, log_decay, scale, dv, lds);
+  if (part == 1) lin_pass<D, true, true, kWide, false>(cut, hv, sg, log_decay, scale, dk, lds);
+  else if (part == 2) lin_pass<D, false, true, kWide, false>(cut, hv, sg, log_decay, scale, dq, lds);
+  else if (whole(sg)) lin_pass<D, true, false, false, true>(cut, hv, sg, log_decay, scale, dv, lds);
+  else lin_pass<D, true, false, false, false>(cut, hv, sg, log_decay, scale, dv, lds);
 }
 
 // Front to back along each sequence's segments (or back to front): a thread
