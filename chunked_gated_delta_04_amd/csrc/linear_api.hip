@@ -45,15 +45,19 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 //       2048     44    51    69
 //      10000    120   100   106   128
 //      24576          228   201   224   257
-//   Chains enough to fill the chip, and short: no cut in sequences of the mean
-// length. 16 x 1024, 8 heads: 56 us uncut, 78 with 256; 16 x 2048, 32 heads: 258
-// uncut, 406 with 1024; but 4 x 4096, 32 heads: 237 uncut, 204 with 1024. The
-// two times compared are fits of such measurements: a step of 64 tokens takes
-// an item 3.6 us (2.0 with D = 64) while every item has a CU (half a CU) to
-// itself; cut, 35 us and 7 passes over rows at 5 TB/s. Means over 2048 are left
-// out: where the lengths differ, the longest sequence's items then end long after
-// the others (12 sequences of 492 to 7435 tokens, 32 heads: 361 us with 2048, 469
-// with 4096).
+//   Chains enough to fill half the chip, and short: no cut in sequences of the mean
+// length, where that takes less time by fits of these measurements (us, forward):
+//                     D = 128, uncut   cut   D = 64, uncut   cut
+//     16 x 1024,  8 heads         60    73              40    33
+//      4 x 2048, 32 heads        108   106              64    52
+//      8 x 2048, 32 heads        155   195              78    98
+//     16 x 2048, 32 heads        277   419             147   201
+// Uncut, a step of 64 tokens takes 3.0 us (1.9 with D = 64) while every chain has a
+// CU (half a CU) to itself, and 4.5 (2.15) with 256 chains and in proportion; cut, 15
+// us and 7 passes over rows at 5 TB/s. Means over 2048 are left out: where the
+// lengths differ, the longest sequence's items then end long after the others (12
+// sequences of 492 to 7435 tokens, 32 heads: 361 us with 2048, 469 with 4096; but 8 x
+// 4096, 32 heads, 360 and 284).
 int64_t segment_tokens(const gdn_linear_problem* p) {
   const int64_t work = (int64_t)p->T * p->HV, chains = (int64_t)p->N * p->HV;
   const auto fill = [&](int64_t S) { return p->K == 128 ? (S <= 1024 ? 176 : 400) : (S <= 256 ? 208 : 448); };
@@ -62,8 +66,9 @@ int64_t segment_tokens(const gdn_linear_problem* p) {
   const int64_t mean = p->N > 0 ? ((int64_t)p->T + p->N - 1) / p->N : 0;
   if (chains >= 128 && mean <= 2048) {
     const bool full = p->K == 128;
-    const double uncut = 10. + (double)mean / kChunk * (full ? 3.6 : 2.0) * std::max(1., (double)chains / (full ? 256 : 512));
-    const double cut = 35. + (double)work * p->K * 2 * 7 / 5e6;
+    const double step = std::max(full ? 3.0 : 1.9, (full ? 4.5 : 2.15) * (double)chains / 256);
+    const double uncut = 10. + (double)mean / kChunk * step;
+    const double cut = 15. + (double)work * p->K * 2 * 7 / 5e6;
     if (uncut < cut)
       while (S < mean) S *= 2;
   }
