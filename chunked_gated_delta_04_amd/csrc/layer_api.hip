@@ -15,7 +15,7 @@ using namespace gdn;
 namespace {
 
 constexpr int kRotaryMaxD = 1024;
-constexpr int kRotaryMaxT = 1 << 25;
+constexpr int kRotaryMaxT = 1 << 25;  // tokens of at most 4 launches
 constexpr int64_t kMaxStride = (int64_t)1 << 31;
 
 int size_of(int dtype) { return dtype == GDN_FP32 ? 4 : 2; }
@@ -34,7 +34,7 @@ gdn_status check_rotary(const gdn_rotary_problem* p) {
   if (bad_stride(p->q_stride, dq) || bad_stride(p->q_out_stride, dq) || bad_stride(p->k_stride, dk) ||
       bad_stride(p->k_out_stride, dk))
     return GDN_ERR_SHAPE;
-  if (p->T > kRotaryMaxT) return GDN_ERR_SHAPE;  // threads of one launch
+  if (p->T > kRotaryMaxT) return GDN_ERR_SHAPE;
   if (!p->positions) {
     if (p->N == 0 && p->T != 0) return GDN_ERR_SHAPE;
     if (p->cu_seqlens_host) {
