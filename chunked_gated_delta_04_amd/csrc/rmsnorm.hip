@@ -23,6 +23,10 @@ constexpr float kTiny = 0x1p-100f;
 
 // larger of two, NaN if one is
 __device__ __forceinline__ float nmax(float a, float b) { return a > b || a != a ? a : b; }
+// larger of m >= 0 and |x|, NaN if one is: magnitudes are in the order of their bits, NaN last
+__device__ __forceinline__ float magnitude(float m, float x) {
+  return __uint_as_float(max(__float_as_uint(m), __float_as_uint(fabsf(x))));
+}
 
 template <int W, bool kMax>
 __device__ __forceinline__ float reduce_lanes(float x) {
@@ -170,10 +174,10 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     top[p] = 0.f;
     if (rstd > 0.f) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) top[p] = fmaxf(top[p], fabsf(v[p][i]));
-    } else {  // infinities or NaN among the row (or a sum past fp32): y's own largest, NaN if one is
+      for (int i = 0; i < V; ++i) top[p] = magnitude(top[p], v[p][i]);
+    } else {  // infinities or NaN among the row (or a sum past fp32): y's own largest
 #pragma unroll
-      for (int i = 0; i < V; ++i) top[p] = nmax(top[p], fabsf(v[p][i] * rstd));
+      for (int i = 0; i < V; ++i) top[p] = magnitude(top[p], v[p][i] * rstd);
     }
   }
   const float up = rstd > 0.f ? rstd : 1.f;

@@ -599,7 +599,8 @@ int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, 
  *   y8, scales  NULL to skip, or e4m3 (OCP, finite) [rows, D] and fp32
  *               [rows] or, with group 128, [rows, ceil(D / 128)]: scale =
  *               max(largest |y| of its columns, 2^-100) / 448, y8 = y / scale
- *               rounded to nearest even, from y in fp32
+ *               rounded to nearest even, from y in fp32. A NaN among the
+ *               columns, of x or of the weight, is their scale and their y8.
  *   rstd        fp32 [rows] for the backward, or NULL
  * Errors: GDN_ERR_NULL (p; x, residual_out with a residual, y and y8 both,
  * scales with y8, when rows > 0), GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED (D,
