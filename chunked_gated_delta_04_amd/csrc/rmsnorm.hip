@@ -165,30 +165,34 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     }
   }
   if (!a.y8) return;
-  // Scales from the largest |v| of their columns: rstd cancels in y / scale, so
-  // the quotients are formed from v (products of two short numbers, exact where x
-  // has 16 bits) and only the scale itself takes rstd.
+  // Scales from the largest |v| of their columns: rstd = lift rest cancels in y /
+  // scale but for the power of two, so the quotients are formed from v lift (products
+  // of two short numbers, exact where x has 16 bits), and only the scale itself takes
+  // rest. The power keeps them at y's own size: v alone of a row that only a small eps
+  // lifts is too small for 448 / m. A row without a finite rstd > 0 (infinities or NaN
+  // in it, a sum past fp32, or zeros with eps = 0) goes by y itself.
+  const bool finite = rstd > 0.f && rstd < __builtin_inff();
+  const uint32_t bits = __float_as_uint(rstd);
+  const float lift = finite ? __uint_as_float(bits & 0x7f800000u) : rstd;
+  const float rest = finite ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : 1.f;
   float top[P];  // of each piece
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     top[p] = 0.f;
-    if (rstd > 0.f) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) top[p] = magnitude(top[p], v[p][i]);
-    } else {  // infinities or NaN among the row (or a sum past fp32): y's own largest
-#pragma unroll
-      for (int i = 0; i < V; ++i) top[p] = magnitude(top[p], v[p][i] * rstd);
+    for (int i = 0; i < V; ++i) {
+      v[p][i] *= lift;
+      top[p] = magnitude(top[p], v[p][i]);
     }
   }
-  const float up = rstd > 0.f ? rstd : 1.f;
-  const float least = kTiny / up;
+  const float least = kTiny / rest;
   const int groups = (D + 127) / 128;
   float whole = 0.f;
   if (a.group == D) {
 #pragma unroll
     for (int p = 0; p < P; ++p) whole = nmax(whole, top[p]);
     whole = nmax(reduce_row<GROUP, true>(whole, part[1]), least);
-    if (on && t == 0) a.scales[row] = whole * up / kE4m3Max;
+    if (on && t == 0) a.scales[row] = whole * rest / kE4m3Max;
   }
 #pragma unroll
   for (int p = 0; p < P; ++p) {
@@ -204,11 +208,11 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
         m = reduce_lanes<GROUP, true>(m);
       }
       m = nmax(m, least);
-      if (on && c < D && c % 128 == 0) a.scales[row * groups + c / 128] = m * up / kE4m3Max;
+      if (on && c < D && c % 128 == 0) a.scales[row * groups + c / 128] = m * rest / kE4m3Max;
     }
     const float r = kE4m3Max / m, rm = 1.f / m;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[p][i] = quotient(rstd > 0.f ? v[p][i] : v[p][i] * rstd, m, r, rm);
+    for (int i = 0; i < V; ++i) v[p][i] = quotient(v[p][i], m, r, rm);
     if (on) store_e4m3<V, kWide>(a.y8 + row * D, c, D, v[p]);
   }
 }

@@ -588,6 +588,7 @@ int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, 
  *               gradients in and out
  *   unit_offset 1: the weight is stored around zero (unit = 1); 0: unit = 0
  *   group       columns that share a scale of y8: 0 (the whole row) or 128
+ *   eps         >= 0; with 0 a row of zeros is 0 / 0: NaN in y, y8 and scales
  *   x_stride, residual_stride  elements from one row of x (and of s in the
  *               backward), of residual to the next, 0 for dense rows; the
  *               other tensors are dense

@@ -42,3 +42,42 @@ def test_a_weight_that_is_no_number_is_in_its_scale(rows, D, dtype, bad):
         assert torch.equal(got["y8"][:, :first].view(torch.uint8), want["y8"][:, :first].view(torch.uint8))
         if quant == 128:
             assert torch.equal(got["scales"][:, :at // 128], want["scales"][:, :at // 128])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("eps", [1e-12, 1e-20, 1e-30])
+@pytest.mark.parametrize("D", [64, 256, 301, 5120])
+def test_rows_that_a_small_eps_lifts(dtype, eps, D):
+    """Rows and groups of zeros give zeros and the least scale, tiny rows the values of their ratios."""
+    print(dtype, eps, D, file=sys.stderr, flush=True)
+    x = make(6, D, dtype, 3)
+    x[0] = 0
+    x[1], x[2] = x[1] * 2.0 ** -20, x[2] * 2.0 ** -24  # fp16's least values among them
+    x[2, 128:] = 0
+    x[3] = 0
+    x[3, D // 2] = 2.0 ** -24
+    x[4, :128] = 0
+    w = make(1, D, dtype, 4)[0].contiguous()
+    for weight in (None, w):
+        y, _ = Y.rmsnorm(f64(x), None if weight is None else f64(weight), eps)
+        for quant, group in (("row", 0), (128, 128)):
+            out = gdn.rmsnorm_fwd(x, weight, quant=quant, want_y=True, eps=eps)
+            within(out["y"], y)
+            sc = Y.scales(y, group)
+            within(out["scales"], sc)
+            v = y / (np.repeat(sc, 128, 1)[:, :D] if group else sc[:, None])
+            err = np.abs(f64(out["y8"].float()) - v)
+            assert (err <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10) * (1 + 2.0 ** -12)).all()
+            assert not out["y8"][0].float().any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_row_of_zeros_without_eps_is_no_number(dtype):
+    """0 / sqrt(0), in y, its scale and y8; the other rows stay."""
+    x = make(3, 200, dtype, 5)
+    x[1] = 0
+    for quant in ("row", 128):
+        out = gdn.rmsnorm_fwd(x, quant=quant, want_y=True, eps=0.0)
+        for n in ("y", "scales", "y8"):
+            t = out[n].float()
+            assert bool(t[1].isnan().all()) and bool(t[[0, 2]].isfinite().all()), n
