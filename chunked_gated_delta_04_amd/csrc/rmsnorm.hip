@@ -118,7 +118,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int c, int D, const flo
 template <typename T, int V, bool kWide, int GROUP, int E>
 __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(NormArgs a) {
   constexpr int P = E / V, NT = GROUP > 256 ? GROUP : 256, kRows = NT / GROUP;
-  __shared__ float part[2][GROUP > 64 ? GROUP / 64 : 1];
+  __shared__ float part[3][GROUP > 64 ? GROUP / 64 : 1];
   const int t = threadIdx.x % GROUP, D = a.D;
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / GROUP;
   const bool on = row < a.rows;  // rows of one workgroup meet at the shuffles
@@ -145,7 +145,19 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += v[p][i] * v[p][i];
   sum = reduce_row<GROUP, false>(sum, part[0]);
-  const float rstd = 1.f / sqrtf(sum / (float)D + a.eps);
+  float mean = sum / (float)D;
+  if (sum == __builtin_inff()) {  // past fp32, as the mean may not be: 2^-14 of it, D being at most 2^14
+    sum = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float z = v[p][i] * 0x1p-7f;
+        sum += z * z;
+      }
+    mean = reduce_row<GROUP, false>(sum, part[2]) * (0x1p14f / (float)D);
+  }
+  const float rstd = 1.f / sqrtf(mean + a.eps);
   if (a.rstd && on && t == 0) a.rstd[row] = rstd;
   // v <- s (weight + unit); y is that times rstd
 #pragma unroll

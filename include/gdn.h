@@ -582,6 +582,7 @@ int gdn_rotary_inv_freq(int32_t R, double base, int32_t scaling, double factor, 
  *   y = s / sqrt(mean(s^2) + eps) * (weight + unit),
  * s rounded to dtype: it is what the residual stream holds and what the
  * backward reads. The norm and its outputs come from that s in fp32.
+ * (A row whose mean(s^2) passes fp32, |s| about 1.8e19, has rstd = 0 and y = 0.)
  *   rows, D     1 <= D <= 16384; rows >= 0, below 2^24 up to D = 4096, 2^23 up
  *               to 8192, 2^22 above
  *   dtype       gdn_dtype of x, residual, weight, residual_out, y and of the

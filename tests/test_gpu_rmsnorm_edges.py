@@ -81,3 +81,26 @@ def test_a_row_of_zeros_without_eps_is_no_number(dtype):
         for n in ("y", "scales", "y8"):
             t = out[n].float()
             assert bool(t[1].isnan().all()) and bool(t[[0, 2]].isfinite().all()), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [1, 64, 333, 700, 4096, 16384])
+def test_rows_whose_sum_of_squares_is_past_fp32(dtype, D):
+    """The mean is in its range: 10^19 squared is 10^38. Rows beside them stay."""
+    x = make(5, D, dtype, 8)
+    want = gdn.rmsnorm_fwd(x, want_rstd=True, eps=0.0)
+    x[1], x[3] = x[1].sign() * 1e19, x[3].clamp(-4, 4) * 2e18
+    out = gdn.rmsnorm_fwd(x, quant=128, want_y=True, want_rstd=True, eps=0.0)
+    y, rstd = Y.rmsnorm(f64(x), None, 0.0)
+    within(out["y"], y)
+    within(out["rstd"], rstd)
+    within(out["scales"], Y.scales(y, 128))
+    for i in (0, 2, 4):
+        assert torch.equal(out["y"][i], want["y"][i]) and torch.equal(out["rstd"][i], want["rstd"][i])
+    # the backward from it
+    dy = make(5, D, dtype, 9).contiguous()
+    g = gdn.rmsnorm_bwd(dy, x, None, out["rstd"])
+    dx, _ = Y.rmsnorm_backward(f64(x), f64(dy), None, 0.0)
+    n = np.abs(f64(x)) * rstd[:, None]
+    size = rstd[:, None] * (np.abs(f64(dy)) + n * (np.abs(f64(dy)) * n).mean(1, keepdims=True))
+    within(g["dx"], dx, size)
