@@ -159,10 +159,20 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
   }
   const float rstd = 1.f / sqrtf(mean + a.eps);
   if (a.rstd && on && t == 0) a.rstd[row] = rstd;
-  // v <- s (weight + unit); y is that times rstd
+  // rstd = lift rest, lift a power of two and 1 <= rest < 2: v <- s lift (weight + unit)
+  // and y = v rest. The power takes a row to its own size before the weight does, so
+  // that the product passes fp32's range where y does and not before, and costs no
+  // rounding. A row without a finite rstd > 0 (infinities or NaN in it, a sum past fp32,
+  // or zeros with eps = 0) takes rstd itself for it.
+  const bool finite = rstd > 0.f && rstd < __builtin_inff();
+  const uint32_t bits = __float_as_uint(rstd);
+  const float lift = finite ? __uint_as_float(bits & 0x7f800000u) : rstd;
+  const float rest = finite ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : 1.f;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = column<V, GROUP>(p, t);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[p][i] *= lift;
     if (a.weight) {
       float w[V];
       load_at<T, V, kWide>(static_cast<const T*>(a.weight), c, D, w);
@@ -172,30 +182,20 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void rmsnorm_fwd_kernel(
     if (a.y && on) {
       float y[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = v[p][i] * rstd;
+      for (int i = 0; i < V; ++i) y[i] = v[p][i] * rest;
       store_at<T, V, kWide>(static_cast<T*>(a.y) + row * D, c, D, y);
     }
   }
   if (!a.y8) return;
-  // Scales from the largest |v| of their columns: rstd = lift rest cancels in y /
-  // scale but for the power of two, so the quotients are formed from v lift (products
-  // of two short numbers, exact where x has 16 bits), and only the scale itself takes
-  // rest. The power keeps them at y's own size: v alone of a row that only a small eps
-  // lifts is too small for 448 / m. A row without a finite rstd > 0 (infinities or NaN
-  // in it, a sum past fp32, or zeros with eps = 0) goes by y itself.
-  const bool finite = rstd > 0.f && rstd < __builtin_inff();
-  const uint32_t bits = __float_as_uint(rstd);
-  const float lift = finite ? __uint_as_float(bits & 0x7f800000u) : rstd;
-  const float rest = finite ? __uint_as_float((bits & 0x007fffffu) | 0x3f800000u) : 1.f;
+  // Scales from the largest |v| of their columns: rest cancels in y / scale, so the
+  // quotients are formed from v (products of two short numbers, exact where x has 16
+  // bits) and only the scale itself takes rest.
   float top[P];  // of each piece
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     top[p] = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[p][i] *= lift;
-      top[p] = magnitude(top[p], v[p][i]);
-    }
+    for (int i = 0; i < V; ++i) top[p] = magnitude(top[p], v[p][i]);
   }
   const float least = kTiny / rest;
   const int groups = (D + 127) / 128;

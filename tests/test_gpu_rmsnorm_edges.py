@@ -104,3 +104,26 @@ def test_rows_whose_sum_of_squares_is_past_fp32(dtype, D):
     n = np.abs(f64(x)) * rstd[:, None]
     size = rstd[:, None] * (np.abs(f64(dy)) + n * (np.abs(f64(dy)) * n).mean(1, keepdims=True))
     within(g["dx"], dx, size)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("s, w", [(1e18, 1e21), (1e18, 1e36), (1e-18, 1e-25), (2e19, 1e25)])
+@pytest.mark.parametrize("D", [64, 333])
+def test_large_and_small_weights(dtype, s, w, D):
+    """The product with the weight passes fp32's range where y does, not where s (weight) alone would. With
+    s = 2e19 the mean of squares is past fp32: rstd is zero, and so is y."""
+    print(dtype, s, w, D, file=sys.stderr, flush=True)
+    x, weight = (make(4, D, dtype, 6) * s).to(dtype), (make(1, D, dtype, 7)[0] * w).to(dtype)
+    past = s > 1e19
+    y, _ = Y.rmsnorm(f64(x), f64(weight), 0.0)
+    for quant, group in (("row", 0), (128, 128)):
+        out = gdn.rmsnorm_fwd(x, weight, quant=quant, want_y=True, eps=0.0)
+        if past:
+            assert not out["y"].any() and not out["y8"].float().any()
+            continue
+        within(out["y"], y)
+        sc = Y.scales(y, group)
+        within(out["scales"], sc)
+        v = y / (np.repeat(sc, 128, 1)[:, :D] if group else sc[:, None])
+        err = np.abs(f64(out["y8"].float()) - v)
+        assert (err <= np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10) * (1 + 2.0 ** -12)).all()
