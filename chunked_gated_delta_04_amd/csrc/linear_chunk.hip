@@ -510,6 +510,10 @@ __device__ __forceinline__ void lin_pass(const LinCut& cut, int hv, const Segmen
       float w[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) w[r] = pw[n][r] != 0.f ? pt[n][r] * pw[n][r] : 0.f;
+      if (kBack && len < kChunk) {  // no tokens past the chunk's end: zeros, whose decays may be past fp32's range
+#pragma unroll
+        for (int r = 0; r < 4; ++r) w[r] = 16 * x.j + 4 * q4 + r < len ? w[r] : 0.f;
+      }
       *reinterpret_cast<uint2*>(Ps + (16 * x.i + l16) * kPPitch + 16 * x.j + 4 * q4) = pack4_bf16(w[0], w[1], w[2], w[3]);
     };
 

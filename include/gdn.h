@@ -427,7 +427,8 @@ int gdn_conv_update(int32_t N, int32_t C, int32_t W, int32_t activation, const u
  *                 such as the short convolution's output: a multiple of 8, at
  *                 least H * K (HV * V) and below 2^23, or 0 for dense rows.
  * log_decay is fp32 [HV] on the device. -inf is decay zero (every value from
- * -128 down counts as that); values above 0 are growth.
+ * -128 down counts as that); values above 0 are growth, for sequences whose
+ * e^(log_decay * tokens) fp32 holds.
  * A NaN or infinity in a token's q, k or v can spoil the outputs of the 64
  * tokens of its chunk (counted from the sequence's start), earlier ones too,
  * besides the later tokens of its sequence; no other sequence is touched. */
