@@ -669,9 +669,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on_stream(dev, stream, call):
+def _on_stream(dev, stream, call, *tensors):
     """call(stream handle) with the tensors' device current, on `stream` (a torch stream or a raw
-    handle), which is then current too, or by default on the device's current stream."""
+    handle, of a stream that outlives the tensors), which is then current too, or by default on the
+    device's current stream. The call's tensors are recorded on a given stream: the memory of one
+    that is freed before the stream is through is not handed out until then. Waiting for what
+    other streams write into them is the caller's."""
     if stream is None:
         if dev.index == torch.cuda.current_device():
             return call(_raw_stream(dev.index))
@@ -682,6 +685,9 @@ def _on_stream(dev, stream, call):
     if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
     with torch.cuda.stream(stream):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
         return call(stream.cuda_stream)
 
 
@@ -777,7 +783,7 @@ def linear_fwd(q, k, v, log_decay, cu_seqlens, h0=None, scale=0.0, cu_seqlens_ho
                                    _at(ws), _bytes(ws), s), "gdn_linear_fwd")
         return o, hT, saved
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, q, k, v, log_decay, cu_seqlens, h0)
 
 
 def linear_fwd_paged(q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indices,
@@ -803,7 +809,8 @@ def linear_fwd_paged(q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indic
                                          _at(ws), _bytes(ws), s), "gdn_linear_fwd_paged")
         return o, saved
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, q, k, v, log_decay, cu_seqlens, state_pool, ssm_state_indices,
+                      has_initial_state)
 
 
 def linear_bwd(q, k, v, log_decay, cu_seqlens, saved, dO, dhT=None, scale=0.0,
@@ -828,7 +835,7 @@ def linear_bwd(q, k, v, log_decay, cu_seqlens, saved, dO, dhT=None, scale=0.0,
                "gdn_linear_bwd")
         return dict(dq=dq, dk=dk, dv=dv, dh0=dh0)
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, q, k, v, log_decay, cu_seqlens, saved, dO, dhT)
 
 
 def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=None, scale=0.0,
@@ -850,7 +857,7 @@ def linear_step(q, k, v, log_decay, state_pool, ssm_state_indices, indices_host=
                "gdn_linear_step")
         return o
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, q, k, v, log_decay, state_pool, ssm_state_indices)
 
 
 # ---------------------------------------------------------------- rotary positions and the norm
@@ -921,7 +928,7 @@ def _rotary(call, q, k, inv_freq, positions, cu_seqlens, offsets, cu_seqlens_hos
         _check(call(ctypes.byref(p), freq, qp, kp, qo, ko, s), "gdn_rotary_bwd" if back else "gdn_rotary")
         return qr, kr
 
-    return _on_stream(dev, stream, launch)
+    return _on_stream(dev, stream, launch, q, k, inv_freq, positions, cu_seqlens, offsets, q_out, k_out)
 
 
 def rotary(q, k, inv_freq, positions=None, cu_seqlens=None, offsets=None, cu_seqlens_host=None,
@@ -1004,7 +1011,7 @@ def rmsnorm_fwd(x, weight=None, residual=None, eps=1e-6, unit_offset=False, quan
                "gdn_rmsnorm_fwd")
         return out
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, x, weight, residual, residual_out)
 
 
 def gdn_rmsnorm_bwd_workspace_size(problem):
@@ -1032,4 +1039,4 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual_out=None, unit_offset=False, want
                                     _at(ws), _bytes(ws), stream_), "gdn_rmsnorm_bwd")
         return dict(dx=dx, dweight=dw)
 
-    return _on_stream(dev, stream, call)
+    return _on_stream(dev, stream, call, dy, s, weight, rstd, dresidual_out)
