@@ -2,13 +2,17 @@
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of the library. Functions named gdn_* mirror the C entry points one
-for one and take torch tensors (or None for a NULL pointer); the lower-case
-helpers at the end allocate outputs and workspaces with torch and call them.
+for one and take torch tensors (or None for a NULL pointer), which the caller
+keeps until the stream has done with them; the lower-case helpers at the end
+allocate outputs and workspaces with torch, on the stream that they run on, and
+call them.
 
 The library is loaded from this package directory. If it is missing, importing
 this module raises ImportError: there is no fallback of any kind.
 """
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -390,10 +394,29 @@ def gdn_recurrent_step(N, H, HV, K, V, scale, q, k, v, a, b, A_log, dt_bias, sta
 
 
 # ---------------------------------------------------------------- allocating helpers
+def _for_stream(f):
+    """f(..., stream=None) run with a given stream current, so that its outputs and workspace are that
+    stream's memory, and its tensors recorded on it (see _on_stream)."""
+    place = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def on_given(*args, **kw):
+        stream = args[place] if len(args) > place else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        tensors = [t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor) and t.is_cuda]
+        if not tensors:
+            return f(*args, **kw)
+        return _on_stream(tensors[0].device, stream, lambda _: f(*args, **kw), *tensors)
+
+    return on_given
+
+
 def _ws(nbytes, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
 
+@_for_stream
 def chunk_fwd(q, k, v, g, beta, cu_seqlens, h0=None, scale=0.0, cu_seqlens_host=None,
               save_for_backward=False, output_final_state=True, stream=None):
     """Allocate outputs and workspace and run gdn_chunk_fwd.
@@ -414,6 +437,7 @@ def chunk_fwd(q, k, v, g, beta, cu_seqlens, h0=None, scale=0.0, cu_seqlens_host=
     return o, hT, saved
 
 
+@_for_stream
 def chunk_fwd_paged(q, k, v, g, beta, cu_seqlens, state_pool, ssm_state_indices,
                     has_initial_state=None, indices_host=None, scale=0.0, cu_seqlens_host=None,
                     save_for_backward=False, stream=None):
@@ -432,6 +456,7 @@ def chunk_fwd_paged(q, k, v, g, beta, cu_seqlens, state_pool, ssm_state_indices,
     return o, saved
 
 
+@_for_stream
 def chunk_bwd(q, k, v, g, beta, cu_seqlens, saved, dO, dhT=None, scale=0.0,
               cu_seqlens_host=None, want_dh0=True, stream=None):
     """Allocate gradients and workspace and run gdn_chunk_bwd.
@@ -455,6 +480,7 @@ def chunk_bwd(q, k, v, g, beta, cu_seqlens, saved, dO, dhT=None, scale=0.0,
     return out
 
 
+@_for_stream
 def chunk_bwd_recompute(q, k, v, g, beta, cu_seqlens, dO, h0=None, dhT=None, scale=0.0,
                         cu_seqlens_host=None, want_dh0=True, stream=None):
     """Allocate gradients and workspace and run gdn_chunk_bwd_recompute (no saved
@@ -476,6 +502,7 @@ def chunk_bwd_recompute(q, k, v, g, beta, cu_seqlens, dO, h0=None, dhT=None, sca
     return out
 
 
+@_for_stream
 def chunk_transition(q, k, v, g, beta, cu_seqlens, scale=0.0, cu_seqlens_host=None,
                      stream=None):
     """Allocate M [N, HV, 128, 128] and s [N, HV, 128, 128] (fp32) and run
@@ -492,6 +519,7 @@ def chunk_transition(q, k, v, g, beta, cu_seqlens, scale=0.0, cu_seqlens_host=No
     return M, s
 
 
+@_for_stream
 def recurrent_step(q, k, v, a, b, A_log, dt_bias, state_pool, ssm_state_indices,
                    indices_host=None, scale=0.0, stream=None):
     """Allocate o and run gdn_recurrent_step (the pool is updated in place)."""
@@ -566,6 +594,7 @@ def gdn_conv_update(N, C, W, activation, x, weight, bias, state_pool, slots, ind
     _check(st, "gdn_conv_update")
 
 
+@_for_stream
 def conv_fwd(x, weight, bias, cu_seqlens, state_in=None, activation="silu",
              cu_seqlens_host=None, want_state=True, stream=None):
     """x [T, C] bf16, weight [C, W] bf16, bias [C] bf16 or None (device).
@@ -580,6 +609,7 @@ def conv_fwd(x, weight, bias, cu_seqlens, state_in=None, activation="silu",
     return y, so
 
 
+@_for_stream
 def conv_fwd_paged(x, weight, bias, cu_seqlens, state_pool, indices, has_initial_state=None,
                    indices_host=None, activation="silu", cu_seqlens_host=None, stream=None):
     """Paged forward: state_pool [slots, C, W-1] bf16 is read and updated in place."""
@@ -593,6 +623,7 @@ def conv_fwd_paged(x, weight, bias, cu_seqlens, state_pool, indices, has_initial
     return y
 
 
+@_for_stream
 def conv_bwd(x, weight, bias, cu_seqlens, dy, state_in=None, activation="silu",
              cu_seqlens_host=None, want_dstate=True, stream=None):
     """Returns dict dx [T, C] bf16, dweight [C, W] fp32, dbias [C] fp32 (None
@@ -613,6 +644,7 @@ def conv_bwd(x, weight, bias, cu_seqlens, dy, state_in=None, activation="silu",
     return out
 
 
+@_for_stream
 def conv_update(x, weight, bias, state_pool, indices, indices_host=None, activation="silu",
                 stream=None):
     """One decode token per row; state_pool [slots, C, W-1] bf16 updated in place."""
