@@ -169,3 +169,25 @@ def test_outputs_and_workspaces_are_the_streams_memory(operator):
     got = flat(f(**again, stream=torch.cuda.default_stream().cuda_stream))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(fresh) == len(sizes)
+
+
+@pytest.mark.parametrize("operator", [linear_fwd, linear_bwd, rotary, rmsnorm_bwd, chunk_fwd, conv_bwd])
+def test_a_given_stream_that_is_being_captured(operator):
+    """The capturing stream handed on by name, a tensor of the call let go of meanwhile; replays beside eager calls."""
+    f, x = operator()
+    want = flat(f(**{n: t.clone() for n, t in x.items()}))
+    g, kept = torch.cuda.CUDAGraph(), {n: t.clone() for n, t in x.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        got = flat(f(**kept, stream=torch.cuda.current_stream()))
+        other = {n: t.clone() for n, t in kept.items()}  # the graph's own memory
+        f(**other, stream=torch.cuda.current_stream())
+        del other
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        f(**{n: t.clone() for n, t in x.items()})
+        torch.cuda.synchronize()
