@@ -45,13 +45,17 @@ bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 //       2048     44    51    69
 //      10000    120   100   106   128
 //      24576          228   201   224   257
-//   Chains enough to fill half the chip, and short: no cut in sequences of the mean
+//   From 128 chains on (half the CUs), and short: no cut in sequences of the mean
 // length, where that takes less time by fits of these measurements (us, forward):
 //                     D = 128, uncut   cut   D = 64, uncut   cut
 //     16 x 1024,  8 heads         60    73              40    33
 //      4 x 2048, 32 heads        108   106              64    52
 //      8 x 2048, 32 heads        155   195              78    98
 //     16 x 2048, 32 heads        277   419             147   201
+// Fewer chains are cut by their work alone. Sequences of 1024 tokens, D = 128, us
+// forward, the best cut and none: 48 chains 38 and 53, 64 chains 51 and 52, 96 chains
+// 58 (72 by this rule) and 55, 128 chains 67 and 55; D = 64: 96 chains 30 and 35, 128
+// chains 34 and 36, 192 chains 43 and 36.
 // Uncut, a step of 64 tokens takes 3.0 us (1.9 with D = 64) while every chain has a
 // CU (half a CU) to itself, and 4.5 (2.15) with 256 chains and in proportion; cut, 15
 // us and 7 passes over rows at 5 TB/s. Means over 2048 are left out: where the

@@ -391,9 +391,9 @@ struct PassLds {
 // vector unit for 1750 (31 %) and the CU's LDS for 2250 (40 %): the bound is how well
 // two waves a SIMD fill each other's waits, and beside it HBM: o of 2 x 8192 tokens,
 // 32 heads, takes 112 us (570 MB, 5.1 TB/s), the three gradients 267 us (1.4 GB, 5.2
-// TB/s). A third workgroup does not fit (244 VGPRs). Waves of 16 columns, four to a
-// SIMD, read b^T and a twice as often: no faster (a step alone 7700 clocks, these
-// gradients 297 us for 286).
+// TB/s; the least of sixty calls, their medians 118 and 293). A third workgroup does
+// not fit (244 VGPRs). Waves of 16 columns, four to a SIMD, read b^T and a twice as
+// often: no faster (a step alone 7700 clocks, these gradients 297 us for 286).
 // kEnds: the segment is a whole sequence whose end state goes to p.io: it is
 // gathered to fp32's precision. Otherwise the carried state only meets a, rounded
 // to bf16, and 16 bits of what it gathers are enough (a third less matrix work);
