@@ -1,0 +1,450 @@
+// Gradients of the causal softmax attention over packed sequences. With the
+// forward's lse, P = e^(scale s - lse), delta = dO . o for each row, and
+//   dS = scale P (dO V^T - delta):   dq = dS K,   dk = dS^T q,   dv = P^T dO,
+// the rows of all query heads of a key head summed in dk and dv.
+//
+// Two kernels, without atomics: one goes over the keys for 128 rows (dq, and
+// delta on the way), the other over the rows for 128 keys (dk, dv). Both form
+// the scores and dO V^T again: seven products instead of the five that one
+// kernel with atomic sums of dq would take. As in the forward, each operand
+// that follows from scores is used where it stands in the accumulator.
+//
+// P and dS are rounded once to the inputs' type, where they are multiplied; all
+// sums are fp32.
+#include <algorithm>
+
+#include "attn_tile.h"
+
+namespace gdn {
+
+namespace {
+
+template <int D>
+constexpr int kGradKeys = D == 64 ? 64 : 32;  // keys a step of dq's kernel
+constexpr int kGradRows = 32;                 // rows a step of dk's and dv's kernel
+
+template <typename T>
+__device__ __forceinline__ uint4 operand(const f32x16& x, int h) {
+  return make_uint4(pack2<T>(x[8 * h], x[8 * h + 1]), pack2<T>(x[8 * h + 2], x[8 * h + 3]),
+                    pack2<T>(x[8 * h + 4], x[8 * h + 5]), pack2<T>(x[8 * h + 6], x[8 * h + 7]));
+}
+template <typename T>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+  T x[8], y[8];
+  __builtin_memcpy(x, &a, 16);
+  __builtin_memcpy(y, &b, 16);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s = fmaf(to_f32(x[i]), to_f32(y[i]), s);
+  return s;
+}
+__device__ __forceinline__ void zero16(f32x16& x) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x[r] = 0.f;
+}
+
+}  // namespace
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
+  constexpr int kT = kGradKeys<D>, KB = kT / 32, DB = D / 32;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kT * D];  // [buffer][k, v]
+  const AttnPack& pk = a.pack;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int hk = blockIdx.x % pk.HK;
+  const int G = pk.G.by, per = kAttnRows / G;
+  const RowTile rt = find_tile(pk.cu, pk.N, pk.T, per, a.slots - 1 - blockIdx.x / pk.HK);
+  if (rt.tokens <= 0) return;
+  const int t0 = rt.first;
+  const KeyTiles kt = key_tiles<kT>(t0, t0 + rt.tokens - 1, rt.len, pk.window, pk.sinks);
+
+  const int row = wave * 32 + l32;
+  const int token = divide(row, pk.G), head = hk * G + row - token * G;
+  const bool live = token < rt.tokens;
+  const int t = t0 + token;
+  const int wlo = t0 + divide(wave * 32, pk.G);
+  const int whi = t0 + min(divide(wave * 32 + 31, pk.G), rt.tokens - 1);
+  const int64_t out = (int64_t)(rt.bos + t0 + token) * pk.HQ + head;
+
+  uint4 q[D / 16], g[D / 16];
+  float delta = 0.f, lse = INFINITY;  // weights of rows that see nothing are zeros
+  {
+    const uint16_t* pq = static_cast<const uint16_t*>(a.q) + (int64_t)(rt.bos + t0 + token) * a.q_stride + head * D + 8 * hi;
+    const uint16_t* pg = static_cast<const uint16_t*>(a.dO) + out * D + 8 * hi;
+    const uint16_t* po = static_cast<const uint16_t*>(a.o) + out * D + 8 * hi;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      q[s] = g[s] = make_uint4(0, 0, 0, 0);
+      if (live) {
+        q[s] = *reinterpret_cast<const uint4*>(pq + 16 * s);
+        g[s] = *reinterpret_cast<const uint4*>(pg + 16 * s);
+        delta += dot8<T>(*reinterpret_cast<const uint4*>(po + 16 * s), g[s]);
+      }
+    }
+    delta += other_half(delta);
+    if (live) {
+      lse = a.lse[out] * kLog2e;
+      if (lse == kMinusInf) lse = INFINITY;
+      if (hi == 0) a.delta[out] = delta;
+    }
+  }
+
+  const uint16_t* kbase = static_cast<const uint16_t*>(a.k) + rt.bos * a.k_stride + hk * D;
+  const uint16_t* vbase = static_cast<const uint16_t*>(a.v) + rt.bos * a.v_stride + hk * D;
+  Staged<D, kT, 256> ks, vs;
+  auto load = [&](int i) {
+    const int j0 = kt.at(i) * kT, len = min(kT, rt.len - j0);
+    ks.load(kbase + j0 * a.k_stride, (int)a.k_stride, len, tid);
+    vs.load(vbase + j0 * a.v_stride, (int)a.v_stride, len, tid);
+  };
+
+  f32x16 dq[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i) zero16(dq[i]);
+  const float c = pk.scale * kLog2e;
+  const int ka = at<D>(l32, 8 * hi);
+  const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
+  const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+
+  if (kt.count > 0) {
+    load(0);
+    ks.store(lds[0][0], tid);
+    vs.store(lds[0][1], tid);
+  }
+  __syncthreads();
+  for (int i = 0, buf = 0; i < kt.count; ++i, buf ^= 1) {
+    const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
+    if (i + 1 < kt.count) load(i + 1);
+    bool some = wlo <= whi && j0 <= whi;
+    if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
+    if (some) {
+      const uint16_t *K = lds[buf][0], *V = lds[buf][1];
+      bool mask = j1 > wlo;
+      if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
+      const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        f32x16 s, dp;
+        zero16(s);
+        zero16(dp);
+        const int kf = fresh(ka);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          s = mfma32_of<T>(*reinterpret_cast<const uint4*>(K + (kf ^ (16 * d)) + 32 * kb * D), q[d], s);
+          dp = mfma32_of<T>(*reinterpret_cast<const uint4*>(V + (kf ^ (16 * d)) + 32 * kb * D), g[d], dp);
+        }
+        if (mask) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int j = j0 + 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3);
+            const bool ok = j <= t && (j > from || j < pk.sinks);
+            dp[r] = ok ? exp2_fast(fmaf(s[r], c, -lse)) * (dp[r] - delta) * pk.scale : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) dp[r] = exp2_fast(fmaf(s[r], c, -lse)) * (dp[r] - delta) * pk.scale;
+        }
+        const int k0 = fresh(va), k1 = fresh(vb);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 ds = operand<T>(dp, h);
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            dq[d] = mfma32_of<T>(column8(K + (32 * kb + 16 * h) * D, k0 ^ (32 * d), k1 ^ (32 * d)), ds, dq[d]);
+        }
+      }
+    }
+    if (i + 1 < kt.count) {
+      ks.store(lds[buf ^ 1][0], tid);
+      vs.store(lds[buf ^ 1][1], tid);
+    }
+    __syncthreads();
+  }
+  if (!live) return;
+  uint16_t* p = static_cast<uint16_t*>(a.dq) + out * D;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      *reinterpret_cast<uint4*>(p + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dq[d], u, 1.f);
+}
+
+// The rows of a sequence that see some of its keys j0 .. j0 + kAttnKeys - 1: in the window, or behind it
+// (far, sinks only). In rows of the G query heads, r = token G + head.
+struct RowRange {
+  int from, to;
+};
+__device__ __forceinline__ RowRange rows_of(const AttnPack& pk, int len, int j0, bool far) {
+  const int W = pk.window, G = pk.G.by;
+  if (far) return {min(j0 + W, len) * G, len * G};
+  return {j0 * G, (W ? min(j0 + kAttnKeys - 1 + W, len) : len) * G};
+}
+
+// Where a part of the gradients of key tokens goes: [parts][tokens][HK][dk, dv][D] fp32. The parts of
+// sinks hold the first `far_tiles` tiles of every sequence, side by side, or where that is more than the
+// pack's tokens, by token.
+__device__ __forceinline__ int64_t far_rows(const AttnGradArgs& a) {
+  return min((int64_t)a.pack.N * a.far_tiles * kAttnKeys, (int64_t)a.pack.T);
+}
+__device__ __forceinline__ float* far_at(const AttnGradArgs& a, int part, const RowTile& kt, int token, int hk, int D) {
+  const int64_t rows = far_rows(a), dense = (int64_t)a.far_tiles * kAttnKeys;
+  const int64_t r = rows < a.pack.N * dense ? kt.bos + token : kt.seq * dense + token;
+  return a.far + (((part * rows + r) * a.pack.HK + hk) * 2) * D;
+}
+__device__ __forceinline__ float* part_at(const AttnGradArgs& a, int part, const RowTile& kt, int token, int hk, int D) {
+  return a.part + ((((int64_t)part * a.pack.T + kt.bos + token) * a.pack.HK + hk) * 2) * D;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(AttnGradArgs a) {
+  constexpr int kR = kGradRows, DB = D / 32;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kR * D];  // [buffer][q, dO]
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kR];       // [buffer][lse, delta]
+  const AttnPack& pk = a.pack;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int G = pk.G.by;
+  int b = blockIdx.x;
+  const int hk = b % pk.HK;
+  b /= pk.HK;
+  // first the rows behind the windows of the sinks' tiles, then all tiles' rows
+  const int far_items = a.far_pieces * a.far_tiles * pk.N;
+  const bool far = b < far_items;
+  int piece, pieces;
+  RowTile kt;
+  if (far) {
+    pieces = a.far_pieces;
+    piece = b % pieces;
+    b /= pieces;
+    kt.seq = b / a.far_tiles;
+    kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
+    kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
+    kt.first = b % a.far_tiles * kAttnKeys;
+    kt.tokens = min(kAttnKeys, kt.len - kt.first);
+  } else {
+    b -= far_items;
+    pieces = a.pieces;
+    piece = b % pieces;
+    kt = find_tile(pk.cu, pk.N, pk.T, kAttnKeys, b / pieces);
+  }
+  if (kt.tokens <= 0) return;
+  const RowRange all = rows_of(pk, kt.len, kt.first, far);
+  const int steps = (all.to - all.from + kR - 1) / kR, share = (steps + pieces - 1) / pieces;
+  const int from = all.from + min(piece * share, steps) * kR, to = min(all.to, from + share * kR);
+
+  const int key = wave * 32 + l32, j = kt.first + key;
+  const bool live = key < kt.tokens;
+  uint4 k[D / 16], v[D / 16];
+  {
+    const uint16_t* pkk = static_cast<const uint16_t*>(a.k) + (int64_t)(kt.bos + j) * a.k_stride + hk * D + 8 * hi;
+    const uint16_t* pv = static_cast<const uint16_t*>(a.v) + (int64_t)(kt.bos + j) * a.v_stride + hk * D + 8 * hi;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      k[s] = v[s] = make_uint4(0, 0, 0, 0);
+      if (live) {
+        k[s] = *reinterpret_cast<const uint4*>(pkk + 16 * s);
+        v[s] = *reinterpret_cast<const uint4*>(pv + 16 * s);
+      }
+    }
+  }
+  // rows that see this lane's key, and the wave's keys
+  const int W = pk.window, wlo = kt.first + wave * 32, whi = wlo + 31;
+  const int64_t none = (int64_t)1 << 40, lim = (int64_t)kt.len * G;
+  int64_t seen_from = (int64_t)j * G, seen_to = W ? min(((int64_t)j + W) * G, lim) : lim;
+  if (far) {
+    seen_from = j < pk.sinks ? ((int64_t)j + W) * G : none;
+    seen_to = lim;
+  }
+  const int lo = (int)min(seen_from, lim), up = (int)seen_to;  // lim < 2^31
+
+  const uint16_t* qbase = static_cast<const uint16_t*>(a.q) + kt.bos * a.q_stride + hk * G * D;
+  const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
+  const float* lses = a.lse + (int64_t)kt.bos * pk.HQ + hk * G;
+  const float* deltas = a.delta + (int64_t)kt.bos * pk.HQ + hk * G;
+  Staged<D, kR, 256> qs, gs;
+  float lse = INFINITY, delta = 0.f;
+  auto load = [&](int r0) {
+    // offsets from the step's first token: its rows are of at most kR + 1 tokens
+    const int first = divide(r0, pk.G);
+    const __amdgpu_buffer_rsrc_t rq =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(qbase) + first * a.q_stride, 0, 0x7ffffff0, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(gbase) + (int64_t)first * pk.HQ * D, 0, 0x7ffffff0, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < qs.kPieces; ++i) {
+      const int r = r0 + qs.row(i, tid), token = divide(r, pk.G), h = r - token * G;
+      const int col = h * D + qs.column(tid);
+      const bool ok = r < to;  // others are past the resource: zeros
+      qs.x[i] = load_b128(rq, ok ? ((token - first) * (int)a.q_stride + col) * 2 : -1);
+      gs.x[i] = load_b128(rg, ok ? ((token - first) * pk.HQ * D + col) * 2 : -1);
+    }
+    if (tid < kR) {
+      const int r = r0 + tid, token = divide(r, pk.G), h = r - token * G;
+      lse = INFINITY;
+      delta = 0.f;
+      if (r < to) {
+        lse = lses[(int64_t)token * pk.HQ + h] * kLog2e;
+        if (lse == kMinusInf) lse = INFINITY;
+        delta = deltas[(int64_t)token * pk.HQ + h];
+      }
+    }
+  };
+  auto store = [&](int buf) {
+    qs.store(lds[buf][0], tid);
+    gs.store(lds[buf][1], tid);
+    if (tid < kR) {
+      stats[buf][0][tid] = lse;
+      stats[buf][1][tid] = delta;
+    }
+  };
+
+  f32x16 dk[DB], dv[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i) {
+    zero16(dk[i]);
+    zero16(dv[i]);
+  }
+  const float c = pk.scale * kLog2e;
+  const int ka = at<D>(l32, 8 * hi);
+  const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
+  const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  // rows that see any and all of the wave's keys
+  const int64_t any_from = far ? (int64_t)(wlo + W) * G : (int64_t)wlo * G;
+  const int64_t any_to = far ? (wlo < pk.sinks ? lim : 0) : W ? ((int64_t)whi + W) * G : lim;
+  const int64_t all_from = far ? (whi < pk.sinks ? (int64_t)(whi + W) * G : none) : (int64_t)whi * G;
+  const int64_t all_to = !far && W ? ((int64_t)wlo + W) * G : lim;
+
+  if (from < to) {
+    load(from);
+    store(0);
+  }
+  __syncthreads();
+  for (int r0 = from, buf = 0; r0 < to; r0 += kR, buf ^= 1) {
+    if (r0 + kR < to) load(r0 + kR);
+    if (r0 + kR > any_from && r0 < any_to && wlo < kt.len) {
+      const uint16_t *Q = lds[buf][0], *O = lds[buf][1];
+      f32x16 s, dp;
+      zero16(s);
+      zero16(dp);
+      const int kf = fresh(ka);
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        s = mfma32_of<T>(*reinterpret_cast<const uint4*>(Q + (kf ^ (16 * d))), k[d], s);
+        dp = mfma32_of<T>(*reinterpret_cast<const uint4*>(O + (kf ^ (16 * d))), v[d], dp);
+      }
+      const bool mask = r0 < all_from || r0 + kR > all_to;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const f32x4 ls = *reinterpret_cast<const f32x4*>(stats[buf][0] + 8 * n + 4 * hi);
+        const f32x4 de = *reinterpret_cast<const f32x4*>(stats[buf][1] + 8 * n + 4 * hi);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * n + e;
+          float p = exp2_fast(fmaf(s[r], c, -ls[e])), x = p * (dp[r] - de[e]) * pk.scale;
+          if (mask) {
+            const int rr = r0 + 8 * n + 4 * hi + e;
+            const bool ok = rr >= lo && rr < up;
+            p = ok ? p : 0.f;
+            x = ok ? x : 0.f;
+          }
+          s[r] = p;
+          dp[r] = x;
+        }
+      }
+      const int c0 = fresh(va), c1 = fresh(vb);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 p = operand<T>(s, h), ds = operand<T>(dp, h);
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          dv[d] = mfma32_of<T>(column8(O + 16 * h * D, c0 ^ (32 * d), c1 ^ (32 * d)), p, dv[d]);
+          dk[d] = mfma32_of<T>(column8(Q + 16 * h * D, c0 ^ (32 * d), c1 ^ (32 * d)), ds, dk[d]);
+        }
+      }
+    }
+    if (r0 + kR < to) store(buf ^ 1);
+    __syncthreads();
+  }
+  if (!live) return;
+  const bool sunk = j / kAttnKeys < a.far_tiles;
+  if (far || a.pieces > 1 || sunk) {
+    float* p = far ? far_at(a, piece, kt, j, hk, D)
+                   : a.pieces > 1 ? part_at(a, piece, kt, j, hk, D) : far_at(a, a.far_pieces, kt, j, hk, D);
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int col = 32 * d + 8 * n + 4 * hi;
+        *reinterpret_cast<f32x4*>(p + col) = f32x4{dk[d][4 * n], dk[d][4 * n + 1], dk[d][4 * n + 2], dk[d][4 * n + 3]};
+        *reinterpret_cast<f32x4*>(p + D + col) = f32x4{dv[d][4 * n], dv[d][4 * n + 1], dv[d][4 * n + 2], dv[d][4 * n + 3]};
+      }
+  } else {
+    const int64_t at = ((int64_t)(kt.bos + j) * pk.HK + hk) * D;
+    uint16_t *pd = static_cast<uint16_t*>(a.dk) + at, *pv = static_cast<uint16_t*>(a.dv) + at;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        *reinterpret_cast<uint4*>(pd + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dk[d], u, 1.f);
+        *reinterpret_cast<uint4*>(pv + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dv[d], u, 1.f);
+      }
+  }
+}
+
+// The parts of dk and dv, in order: first those in the window, then those of the rows behind it. A
+// workgroup takes eight keys of a tile; without parts of the windows, of the sinks' tiles alone.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a) {
+  const AttnPack& pk = a.pack;
+  int b = blockIdx.x;
+  const int some = b % (kAttnKeys / 8) * 8;
+  b /= kAttnKeys / 8;
+  RowTile kt;
+  if (a.pieces > 1) {
+    kt = find_tile(pk.cu, pk.N, pk.T, kAttnKeys, b);
+  } else {
+    kt.seq = b / a.far_tiles;
+    kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
+    kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
+    kt.first = b % a.far_tiles * kAttnKeys;
+    kt.tokens = min(kAttnKeys, kt.len - kt.first);
+  }
+  const int keys = min(8, kt.tokens - some), unit = 2 * pk.HK * D / 4;
+  const bool sunk = kt.first / kAttnKeys < a.far_tiles;
+  const int from_part = a.pieces > 1 ? a.pieces : 0;
+  const int from_far = sunk ? a.far_pieces + (a.pieces > 1 ? 0 : 1) : 0;
+  for (int i = threadIdx.x; i < keys * unit; i += 256) {
+    const int j = kt.first + some + i / unit, at = i % unit * 4, hk = at / (2 * D), col = at % (2 * D);
+    f32x4 x = zero4();
+    for (int n = 0; n < from_part; ++n) x += *reinterpret_cast<const f32x4*>(part_at(a, n, kt, j, hk, D) + col);
+    for (int n = 0; n < from_far; ++n) x += *reinterpret_cast<const f32x4*>(far_at(a, n, kt, j, hk, D) + col);
+    uint16_t* to = static_cast<uint16_t*>(col < D ? a.dk : a.dv) + ((int64_t)(kt.bos + j) * pk.HK + hk) * D + col % D;
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+  }
+}
+
+namespace {
+
+template <typename T, int D>
+hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
+  const AttnPack& pk = a.pack;
+  const dim3 block(256);
+  hipLaunchKernelGGL((attn_grad_q_kernel<T, D>), dim3(a.slots * pk.HK), block, 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int items = a.far_pieces * a.far_tiles * pk.N + a.pieces * a.key_slots;
+  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), block, 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int tiles = a.pieces > 1 ? a.key_slots : a.far_tiles * pk.N;
+  if (tiles > 0) hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(tiles * (kAttnKeys / 8)), block, 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_bwd(Elem type, int D, const AttnGradArgs& a, hipStream_t s) {
+  if (type == Elem::kBf16) return D == 64 ? bwd_of<Bf16, 64>(a, s) : D == 128 ? bwd_of<Bf16, 128>(a, s) : bwd_of<Bf16, 256>(a, s);
+  return D == 64 ? bwd_of<Fp16, 64>(a, s) : D == 128 ? bwd_of<Fp16, 128>(a, s) : bwd_of<Fp16, 256>(a, s);
+}
+
+}  // namespace gdn

@@ -19,13 +19,12 @@
 // pieces that hold all 24 bits, against b's exact bf16 rows.
 #include <type_traits>
 
+#include "lds_tile.h"
 #include "linear.h"
 
 namespace gdn {
 
 namespace {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ f32x16 mfma32(const bf16x8& a, const bf16x8& b, const f32x16& c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -108,21 +107,6 @@ __device__ __forceinline__ StateAt state_at(const StateRef& io, int seq, int hv,
   return {from ? from + base : nullptr, to ? to + base : nullptr};
 }
 
-// 64 rows of D bf16 in LDS, 16-byte pieces of a row permuted by the row's number
-// (xor): the 16 rows of a row-wise operand read, and the 4 rows x 2 pieces that a
-// lane group's transposing read takes, then all lie in different banks (with rows
-// padded by 16 bytes instead, nearly half of the LDS cycles were conflicts). The
-// permutation has a period of 16 rows, so it is a constant of the lane.
-template <int D>
-__device__ __forceinline__ int piece_of(int row) {
-  const int x = D == 128 ? row & 15 : (row >> 1) & 7;
-  return ((x & 3) << 1) | ((x >> 2) & 1) | (x & 8);
-}
-// element offset of column c (a multiple of 4) of a row
-template <int D>
-__device__ __forceinline__ int at(int row, int c) {
-  return row * D + (((c >> 3) ^ piece_of<D>(row)) << 3) + (c & 4);
-}
 constexpr int kPPitch = kChunk + 8;
 
 // 64 rows of one operand, 16 bytes a piece, held by the NT threads.
@@ -157,12 +141,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rows(const uint16_t* p, 
                                            len > 0 ? ((len - 1) * stride + D) * 2 : 0, kBufferWord3);
 }
 
-// A value that the compiler must not keep computed things of across the loop:
-// the LDS offsets that follow from it by one xor cost a register each otherwise.
-__device__ __forceinline__ int fresh(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
 // Offsets of a wave's operand reads: one lane-dependent part each, to which a
 // read's pieces add by xor (they are bits below the row's) and its 16-row tiles
 // by plus.
@@ -174,7 +152,7 @@ struct Lane {
     row32 = at<D>(l32, 8 * hi);
     row16 = at<D>(l16, 8 * q4);
     const int r = 8 * hi + (j >> 2), c = 16 * (q4 & 1);
-    const int swapped = ((j & 1) << 1) | ((j >> 1) & 1);  // see column8
+    const int swapped = ((j & 1) << 1) | ((j >> 1) & 1);  // see State
     ka = at<D>(r, c + 4 * swapped);
     kb = at<D>(r + 4, c + 4 * swapped);
     va = at<D>(r, 32 * wave + c + 4 * (j & 3));
@@ -186,7 +164,8 @@ struct Lane {
 // 8 m + e of tile kb is k = 32 kb + 16 m + 8 (lane / 32) + e: the accumulator's
 // rows, taken in an order that makes 8 consecutive k one MFMA operand, so that
 // the state is multiplied from the registers that it is gathered in. (The
-// operand gathered from, b^T, is read in that order: see column8.)
+// operand gathered from, b^T, is read in that order, with the 16 columns' middle groups of
+// four exchanged.)
 template <int D>
 struct State {
   static constexpr int KB = D / 32;
@@ -247,14 +226,6 @@ struct State {
                                                  pk2(s[8 * m + 4], s[8 * m + 5]), pk2(s[8 * m + 6], s[8 * m + 7])));
   }
 };
-
-// A lane's column (lane % 16 of its group's 16) of 8 rows by two transposing reads
-// of 4 rows (see lds_tr16). b's are read with the 16 columns' middle groups of four
-// exchanged, which is the order of State's rows.
-__device__ __forceinline__ uint4 column8(const uint16_t* tile, int a, int b) {
-  const uint2 x = lds_tr16(tile + a), y = lds_tr16(tile + b);
-  return make_uint4(x.x, x.y, y.x, y.y);
-}
 
 // c's columns of one 16-token step times the tokens' weights, as kPieces bf16
 // operands: three hold the fp32 products' 24 bits, two their first 16.

@@ -45,6 +45,9 @@ EXPORTED = (
     "gdn_linear_fwd", "gdn_linear_fwd_paged", "gdn_linear_bwd", "gdn_linear_step",
     "gdn_rotary", "gdn_rotary_bwd", "gdn_rotary_inv_freq",
     "gdn_rmsnorm_fwd", "gdn_rmsnorm_bwd", "gdn_rmsnorm_bwd_workspace_size",
+    "gdn_kv_append", "gdn_attn_fwd", "gdn_attn_fwd_paged", "gdn_attn_step", "gdn_attn_bwd",
+    "gdn_attn_fwd_workspace_size", "gdn_attn_fwd_paged_workspace_size",
+    "gdn_attn_step_workspace_size", "gdn_attn_bwd_workspace_size",
 )
 GDN_MAX_STAGES = 8
 
@@ -88,6 +91,27 @@ class GdnRmsnormProblem(ctypes.Structure):
     _fields_ = [(_n, ctypes.c_int32) for _n in ("rows", "D", "dtype", "unit_offset", "group")] + [
         ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
     ]
+
+
+class GdnAttnProblem(ctypes.Structure):
+    _fields_ = [(_n, ctypes.c_int32) for _n in ("N", "T", "HQ", "HK", "D", "dtype", "window", "sinks")] + [
+        ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_host", ctypes.c_void_p),
+    ] + [(_n, ctypes.c_int64) for _n in ("q_stride", "k_stride", "v_stride")]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (_n, ctypes.c_int32) for _n in ("pages", "page_size", "columns")] + [
+        (_n, ctypes.c_int64) for _n in ("table_stride", "page_stride", "token_stride", "head_stride")
+    ] + [("page_table", ctypes.c_void_p), ("offsets", ctypes.c_void_p)]
+
+
+class GdnKvAppendProblem(ctypes.Structure):
+    _fields_ = [(_n, ctypes.c_int32) for _n in ("N", "T", "HQ", "HK", "D", "R", "interleaved", "dtype")] + [
+        ("mscale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p),
+        ("cu_seqlens_host", ctypes.c_void_p),
+    ] + [(_n, ctypes.c_int64) for _n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
 
 
 class GdnError(RuntimeError):
@@ -175,6 +199,19 @@ _lib.gdn_rmsnorm_bwd.restype = ctypes.c_int
 _lib.gdn_rmsnorm_bwd.argtypes = [_NP] + [_vp] * 8 + [_sz, _vp]
 _lib.gdn_rmsnorm_bwd_workspace_size.restype = _sz
 _lib.gdn_rmsnorm_bwd_workspace_size.argtypes = [_NP]
+
+_AP, _KP = ctypes.POINTER(GdnAttnProblem), ctypes.POINTER(GdnKvCache)
+for _n, _args in (("gdn_attn_fwd", [_AP]), ("gdn_attn_fwd_paged", [_AP, _KP]),
+                  ("gdn_attn_step", [_AP, _KP]), ("gdn_attn_bwd", [_AP])):
+    getattr(_lib, _n + "_workspace_size").restype = _sz
+    getattr(_lib, _n + "_workspace_size").argtypes = _args
+    getattr(_lib, _n).restype = ctypes.c_int
+_lib.gdn_attn_fwd.argtypes = [_AP] + [_vp] * 6 + [_sz, _vp]
+_lib.gdn_attn_fwd_paged.argtypes = [_AP, _KP] + [_vp] * 4 + [_sz, _vp]
+_lib.gdn_attn_step.argtypes = [_AP, _KP] + [_vp] * 4 + [_sz, _vp]
+_lib.gdn_attn_bwd.argtypes = [_AP] + [_vp] * 10 + [_sz, _vp]
+_lib.gdn_kv_append.restype = ctypes.c_int
+_lib.gdn_kv_append.argtypes = [ctypes.POINTER(GdnKvAppendProblem), _KP] + [_vp] * 6
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -1072,3 +1109,188 @@ def rmsnorm_bwd(dy, s, weight, rstd, dresidual_out=None, unit_offset=False, want
         return dict(dx=dx, dweight=dw)
 
     return _on_stream(dev, stream, call, dy, s, weight, rstd, dresidual_out)
+
+
+# ---------------------------------------------------------------- softmax attention and its cache
+_HALF = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _half(t, name):
+    if t.dtype not in _HALF:
+        raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    return _HALF[t.dtype]
+
+
+def _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev):
+    """The gdn_kv_cache of tensors [pages, page_size, HK, D] in any order of memory."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+        if t.dim() != 4 or t.shape[2] != HK or t.shape[3] != D or t.shape != k_cache.shape:
+            raise ValueError(f"{name} must be [pages, page_size, {HK}, {D}], got {tuple(t.shape)}")
+        if t.stride() != k_cache.stride() or (t.stride(3) != 1 and D > 1):
+            raise ValueError("k_cache and v_cache must have the same strides and dense columns")
+    pages, size = k_cache.shape[:2]
+    # an extent of 1 has no stride of its own
+    strides = [max(s, D) if n == 1 else s for n, s in zip(k_cache.shape[:3], k_cache.stride()[:3])]
+    if page_table.dtype is not torch.int32 or page_table.device != dev:
+        raise ValueError(f"page_table must be int32 on {dev}")
+    if page_table.dim() != 2 or page_table.shape[0] != N:
+        raise ValueError(f"page_table must be [{N}, columns], got {tuple(page_table.shape)}")
+    columns = page_table.shape[1]
+    if (page_table.stride(1) != 1 and columns > 1) or (page_table.stride(0) < columns and N > 1):
+        raise ValueError(f"page_table must have dense rows apart, got strides {page_table.stride()}")
+    return GdnKvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, columns,
+                      page_table.stride(0) if N > 1 else 0, *strides, page_table.data_ptr(),
+                      _dev(offsets, (N,), torch.int32, "offsets", dev))
+
+
+def _bounds(cu_seqlens, cu_seqlens_host, dev):
+    """(N, device pointer, host pointer) of a pack's boundaries."""
+    N = cu_seqlens.numel() - 1
+    if cu_seqlens_host is not None and cu_seqlens_host.numel() != N + 1:
+        raise ValueError(f"cu_seqlens_host must hold {N + 1} boundaries")
+    return (N, _dev(cu_seqlens, (N + 1,), torch.int32, "cu_seqlens", dev),
+            _host_ptr(cu_seqlens_host, "cu_seqlens_host"))
+
+
+def _attn_rows(q, k, v, dev):
+    """(HK, pointers, strides) of q [T, HQ, D] and k, v [T, HK, D]."""
+    T, _, D = q.shape
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D or t.shape != k.shape:
+            raise ValueError(f"{name} must be [{T}, HK, {D}], got {tuple(t.shape)}")
+    rows = [_rows(t, q.dtype, n, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    return k.shape[1], [r[0] for r in rows], [r[1] for r in rows]
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, offsets, cu_seqlens=None, q=None, inv_freq=None,
+              interleaved=False, mscale=1.0, cu_seqlens_host=None, q_out=None, stream=None):
+    """New tokens' k, v [T, HK, D] into a paged cache (gdn_kv_append), k turned by rotary positions on
+    the way and q [T, HQ, D] beside it; bf16 or fp16, dense or slices of a wider buffer's rows.
+
+    k_cache, v_cache [pages, page_size, HK, D], in any order of memory, are updated in place; page_table
+    [N, columns] and offsets [N] (tokens that each sequence had before) int32. cu_seqlens [N+1] int32, or
+    None for one token of each sequence. inv_freq [R / 2] fp32, or None: nothing turns. q_out: where q's
+    result goes (q itself: in place), by default a new tensor. Returns q_out, or None without q."""
+    dev = _on_device(k, "k")
+    dtype = _half(k, "k")
+    T, HK, D = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
+    HQ = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"q must be [{T}, HQ, {D}], got {tuple(q.shape)}")
+        HQ = q.shape[1]
+    N, cu, host = T, None, None
+    if cu_seqlens is not None:
+        N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
+    kp, ks = _rows(k, k.dtype, "k", dev)
+    vp, vs = _rows(v, k.dtype, "v", dev)
+    qp, qs = _rows(q, k.dtype, "q", dev) if HQ else (None, 0)
+    R = 2 * inv_freq.numel() if inv_freq is not None else 0
+    p = GdnKvAppendProblem(N, T, HQ, HK, D, R, bool(interleaved), dtype, mscale, cu, host, qs, ks, vs, 0)
+    freq = _dev(inv_freq, (R // 2,), _f32, "inv_freq", dev)
+    cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, k.dtype, dev)
+
+    def call(s):
+        out, op = q_out, None
+        if HQ:
+            if out is None:
+                out = torch.empty(T, HQ, D, dtype=k.dtype, device=dev)
+            elif out.shape != q.shape:
+                raise ValueError(f"q_out must have the shape {tuple(q.shape)}, got {tuple(out.shape)}")
+            op, p.q_out_stride = _rows(out, k.dtype, "q_out", dev)
+        _check(_lib.gdn_kv_append(ctypes.byref(p), ctypes.byref(cache), freq, qp, kp, vp, op, s),
+               "gdn_kv_append")
+        return out if HQ else None
+
+    return _on_stream(dev, stream, call, q, k, v, inv_freq, cu_seqlens, k_cache, v_cache, page_table,
+                      offsets, q_out)
+
+
+def _attn_call(name, p, cache, q, want_lse, ptrs):
+    """call(stream) of one forward: allocates o, lse and the workspace."""
+    T, HQ, D = q.shape
+    args = [ctypes.byref(p)] + ([ctypes.byref(cache)] if cache is not None else [])
+
+    def call(s):
+        o = torch.empty(T, HQ, D, dtype=q.dtype, device=q.device)
+        lse = torch.empty(T, HQ, dtype=_f32, device=q.device) if want_lse else None
+        ws = _alloc_bytes(getattr(_lib, name + "_workspace_size")(*args), q.device)
+        _check(getattr(_lib, name)(*args, *ptrs, o.data_ptr(), _at(lse), _at(ws), _bytes(ws), s), name)
+        return o, lse
+
+    return call
+
+
+def attn_fwd(q, k, v, cu_seqlens, window=0, sinks=0, scale=0.0, cu_seqlens_host=None, want_lse=False,
+             stream=None):
+    """Causal softmax attention over a pack (gdn_attn_fwd).
+
+    q [T, HQ, D], k, v [T, HK, D], bf16 or fp16, D = 64, 128 or 256, dense or slices of a wider buffer's
+    rows; cu_seqlens [N+1] int32. window: the last positions that a token sees (0: all), sinks: the
+    first positions that it sees besides. Returns (o [T, HQ, D], lse [T, HQ] fp32 or None)."""
+    dev = _on_device(q, "q")
+    T, HQ, D = q.shape
+    HK, ptrs, strides = _attn_rows(q, k, v, dev)
+    N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
+    p = GdnAttnProblem(N, T, HQ, HK, D, _half(q, "q"), window, sinks, scale, cu, host, *strides)
+    return _on_stream(dev, stream, _attn_call("gdn_attn_fwd", p, None, q, want_lse, ptrs), q, k, v,
+                      cu_seqlens)
+
+
+def attn_bwd(q, k, v, cu_seqlens, o, lse, dO, window=0, sinks=0, scale=0.0, cu_seqlens_host=None,
+             stream=None):
+    """Gradients of attn_fwd (gdn_attn_bwd), o and lse as it gave them: dict dq [T, HQ, D] and
+    dk, dv [T, HK, D]."""
+    dev = _on_device(q, "q")
+    T, HQ, D = q.shape
+    HK, ptrs, strides = _attn_rows(q, k, v, dev)
+    N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
+    p = GdnAttnProblem(N, T, HQ, HK, D, _half(q, "q"), window, sinks, scale, cu, host, *strides)
+    more = (_dev(o, (T, HQ, D), q.dtype, "o", dev), _dev(lse, (T, HQ), _f32, "lse", dev),
+            _dev(dO, (T, HQ, D), q.dtype, "dO", dev))
+
+    def call(s):
+        dq = torch.empty(T, HQ, D, dtype=q.dtype, device=dev)
+        dk, dv = (torch.empty(T, HK, D, dtype=q.dtype, device=dev) for _ in range(2))
+        ws = _alloc_bytes(_lib.gdn_attn_bwd_workspace_size(ctypes.byref(p)), dev)
+        _check(_lib.gdn_attn_bwd(ctypes.byref(p), *ptrs, *more, dq.data_ptr(), dk.data_ptr(),
+                                 dv.data_ptr(), _at(ws), _bytes(ws), s), "gdn_attn_bwd")
+        return dict(dq=dq, dk=dk, dv=dv)
+
+    return _on_stream(dev, stream, call, q, k, v, cu_seqlens, o, lse, dO)
+
+
+def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, offsets, window=0, sinks=0, scale=0.0,
+                   cu_seqlens_host=None, want_lse=False, stream=None):
+    """attn_fwd over a paged cache that holds the tokens' keys and values already (gdn_attn_fwd_paged):
+    token i of sequence n is at position offsets[n] + i. The cache as in kv_append."""
+    dev = _on_device(q, "q")
+    T, HQ, D = q.shape
+    qp, qs = _rows(q, q.dtype, "q", dev)
+    N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
+    HK = k_cache.shape[2]
+    p = GdnAttnProblem(N, T, HQ, HK, D, _half(q, "q"), window, sinks, scale, cu, host, qs, 0, 0)
+    cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, q.dtype, dev)
+    return _on_stream(dev, stream, _attn_call("gdn_attn_fwd_paged", p, cache, q, want_lse, (qp,)), q,
+                      k_cache, v_cache, page_table, cu_seqlens, offsets)
+
+
+def attn_step(q, k_cache, v_cache, page_table, offsets, window=0, sinks=0, scale=0.0, want_lse=False,
+              stream=None):
+    """Attention of one new token a row over a paged cache that holds it already (gdn_attn_step): q
+    [N, HQ, D], the token of row n at position offsets[n] (negative: an idle row, o = 0). The cache as
+    in kv_append. Returns (o [N, HQ, D], lse [N, HQ] fp32 or None)."""
+    dev = _on_device(q, "q")
+    N, HQ, D = q.shape
+    qp, qs = _rows(q, q.dtype, "q", dev)
+    HK = k_cache.shape[2]
+    p = GdnAttnProblem(N, N, HQ, HK, D, _half(q, "q"), window, sinks, scale, None, None, qs, 0, 0)
+    cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, q.dtype, dev)
+    return _on_stream(dev, stream, _attn_call("gdn_attn_step", p, cache, q, want_lse, (qp,)), q, k_cache,
+                      v_cache, page_table, offsets)

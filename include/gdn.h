@@ -632,6 +632,140 @@ int gdn_rmsnorm_bwd(const gdn_rmsnorm_problem* p, const void* s, const void* wei
                     const float* rstd, const void* dy, const void* ds, void* dx, float* dweight,
                     void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Softmax attention, for the attention layers between the recurrent ones, and
+ * the paged cache of its keys and values. bf16 or fp16 tensors, fp32 inside.
+ *
+ * The query of a token at position t of its sequence sees the keys at the
+ * positions j <= t, with window > 0 those of them with j > t - window or
+ * j < sinks. Query head h reads key head h / (HQ / HK). Over the keys that are
+ * seen, with s_j = scale (q . k_j),
+ *   lse = ln sum e^s_j,   o = sum e^(s_j - lse) v_j;
+ * a query that sees no key has o = 0 and lse = -inf.
+ *
+ *   N, T        sequences and query tokens of the call (T <= 2^30, T HQ < 2^31)
+ *   HQ, HK      query and key heads: HK divides HQ, HQ / HK <= 128
+ *   D           columns of a head: 64, 128 or 256
+ *   dtype       GDN_BF16 or GDN_FP16: of q, k, v, o, the cache and the gradients
+ *   window      last positions that are seen, 0: all (<= 2^30)
+ *   sinks       first positions that stay seen behind the window (<= 2^30; not
+ *               read without a window)
+ *   scale       <= 0 selects D^-1/2
+ *   cu_seqlens, cu_seqlens_host   as in gdn_problem
+ *   strides     elements from one token of q, k, v to the next (its heads are
+ *               dense), for rows inside a wider buffer: a multiple of 8, at least
+ *               the heads' columns and below 2^23, or 0 for dense rows
+ * Rows of the outputs at or past cu_seqlens[N] are left as they were. No output
+ * overlaps an input. A NaN or infinity in a token's k or v can spoil the outputs
+ * of its sequence's tokens that share a tile of rows (128 / (HQ / HK) tokens)
+ * or keys (64) with one that sees it; its q or dO, the gradients of k and v of
+ * the keys that share a tile (128) with one that it sees. */
+typedef struct {
+  int32_t N, T, HQ, HK, D, dtype;
+  int32_t window, sinks;
+  float scale;
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+  int64_t q_stride, k_stride, v_stride;
+} gdn_attn_problem;
+
+/* A paged cache. The token at position j of sequence n is row j % page_size of
+ * page page_table[n * table_stride + j / page_size]; row r, head h of page i is
+ * at k + i * page_stride + r * token_stride + h * head_stride, v likewise.
+ *   k, v        device memory of `pages` pages
+ *   pages       index 0 is the null page, as in the state pools: an index
+ *               outside 1 .. pages - 1, or a position past the table's columns,
+ *               has no page: its token is not written, and not seen
+ *   page_size   rows of a page, any number
+ *   columns     of the page table
+ *   table_stride  elements between its rows, 0: columns (not checked further:
+ *               the caller's table has N such rows)
+ *   page_stride, token_stride, head_stride  elements, at least D: any order of
+ *               page, token and head. For the attention multiples of 8.
+ *   page_table  device int32 [N][table_stride]
+ *   offsets     device int32 [N]: tokens that the sequence had before the call,
+ *               so its new token i is at position offsets[n] + i; all positions
+ *               below 2^31 - 256. A negative position (an idle row of a padded
+ *               batch) is not written and sees nothing.
+ * Rows of the cache that no token of a call sees are never read into its results,
+ * whatever they hold. */
+typedef struct {
+  void *k, *v;
+  int32_t pages, page_size, columns;
+  int64_t table_stride, page_stride, token_stride, head_stride;
+  const int32_t* page_table;
+  const int32_t* offsets;
+} gdn_kv_cache;
+
+/* New tokens' k and v into the cache, k turned by rotary positions on the way,
+ * and q turned beside it: what gdn_rotary does with the tokens' positions in
+ * the cache, then the rows' copy, in one launch.
+ *   N, T        sequences and new tokens
+ *   HQ, HK, D   heads of q (0: no q) and of k and v, their columns (at most 1024)
+ *   R, interleaved, mscale, inv_freq   as in gdn_rotary_problem; R = 0: nothing
+ *               turns
+ *   dtype       GDN_BF16 or GDN_FP16
+ *   cu_seqlens  device int32 [N + 1], or NULL for one token of each sequence
+ *               (T = N)
+ *   strides     elements from one token of q, k, v, q_out to the next, 0: dense;
+ *               below 2^31
+ *   q, q_out    [T, HQ, D], q_out may be q with the same stride
+ *   k, v        [T, HK, D]
+ * Two tokens with one place in the cache leave either's row there. Rows of q_out
+ * that no sequence holds are left as they were; a token without a place in the
+ * cache still has its q turned. Fastest with rows of 16-byte aligned pieces.
+ * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS,
+ * GDN_ERR_ALIGN (a pointer not aligned to its elements), GDN_ERR_HIP. */
+typedef struct {
+  int32_t N, T, HQ, HK, D, R, interleaved, dtype;
+  float mscale;
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+} gdn_kv_append_problem;
+int gdn_kv_append(const gdn_kv_append_problem* p, const gdn_kv_cache* cache, const float* inv_freq,
+                  const void* q, const void* k, const void* v, void* q_out, void* stream);
+
+/* Workspace bytes of the calls (0 on a bad problem, and for problems that need
+ * none; workspace may then be NULL): from the extents, windows and, where the
+ * cache is read, its page size and columns only. Workspaces are 16-byte aligned
+ * device memory, used only during the call, and need not be zeroed. */
+size_t gdn_attn_fwd_workspace_size(const gdn_attn_problem* p);
+size_t gdn_attn_fwd_paged_workspace_size(const gdn_attn_problem* p, const gdn_kv_cache* cache);
+size_t gdn_attn_step_workspace_size(const gdn_attn_problem* p, const gdn_kv_cache* cache);
+size_t gdn_attn_bwd_workspace_size(const gdn_attn_problem* p);
+
+/* q [T, HQ, D], k and v [T, HK, D] -> o [T, HQ, D] (dense) and lse fp32 [T, HQ]
+ * (NULL to skip; the backward reads it). Every sequence begins at position 0.
+ * Errors: GDN_ERR_NULL (p; q, k, v, o, cu_seqlens when T > 0), GDN_ERR_SHAPE,
+ * GDN_ERR_UNSUPPORTED (D, heads, dtype), GDN_ERR_SEQLENS, GDN_ERR_ALIGN,
+ * GDN_ERR_WORKSPACE, GDN_ERR_HIP. */
+int gdn_attn_fwd(const gdn_attn_problem* p, const void* q, const void* k, const void* v, void* o,
+                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same with the keys and values of a cache, which holds the call's tokens
+ * already (gdn_kv_append): token i of sequence n is at position offsets[n] + i.
+ * p's k_stride and v_stride are not read. Errors: as gdn_attn_fwd, and
+ * GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_ALIGN for the cache. */
+int gdn_attn_fwd_paged(const gdn_attn_problem* p, const gdn_kv_cache* cache, const void* q, void* o,
+                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token a sequence: T = N rows of q, cu_seqlens not read, the token of row n
+ * at position offsets[n] and in the cache already. Errors: as gdn_attn_fwd_paged. */
+int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* cache, const void* q, void* o,
+                  float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of gdn_attn_fwd (same p, q, k, v), o and lse as it gave them:
+ *   dO          [T, HQ, D] cotangent of o (dense)
+ *   dq          [T, HQ, D], dk, dv [T, HK, D] (dense)
+ * The query heads of a key head are summed into dk and dv in fp32 in a fixed
+ * order; no atomics. With fp16 the gradients of the scores are fp16 where they
+ * are multiplied, so a cotangent as large as its range can pass it. Errors: as
+ * gdn_attn_fwd, GDN_ERR_NULL for o, lse, dO, dq, dk, dv. */
+int gdn_attn_bwd(const gdn_attn_problem* p, const void* q, const void* k, const void* v,
+                 const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
