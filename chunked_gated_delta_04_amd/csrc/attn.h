@@ -73,7 +73,8 @@ struct AttnGradArgs {
   float *part, *far;         // partial dk and dv
 };
 
-constexpr int kAttnRows = 128;  // rows of a workgroup's tile
+// rows of a workgroup's tile, 32 to a wave; with 256 columns a wave has a SIMD's registers to itself
+constexpr int attn_rows(int D) { return D == 256 ? 128 : 256; }
 constexpr int kAttnKeys = 128;  // keys of a workgroup's tile in the backward
 constexpr int kAttnGroup = 128; // most query heads to a key head
 

@@ -38,7 +38,7 @@ gdn_status check_bounds(int N, int T, const int32_t* cu) {
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int group(const gdn_attn_problem* p) { return p->HQ / p->HK; }
-int64_t row_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / (kAttnRows / group(p)) + p->N; }
+int64_t row_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / (attn_rows(p->D) / group(p)) + p->N; }
 int64_t key_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / kAttnKeys + p->N; }
 
 gdn_status check_attn(const gdn_attn_problem* p) {
@@ -120,7 +120,7 @@ int splits_of(int64_t items, int64_t keys, int fill, int least) {
 }
 int fwd_splits(const gdn_attn_problem* p, const gdn_kv_cache* c) {
   const int64_t keys = c ? (int64_t)c->columns * c->page_size : p->T;
-  return splits_of(row_tiles(p) * p->HK, most_keys(p, keys, kAttnRows / group(p)), 2 * kCUs, 512);
+  return splits_of(row_tiles(p) * p->HK, most_keys(p, keys, attn_rows(p->D) / group(p)), 2 * kCUs, 512);
 }
 int64_t step_items(const gdn_attn_problem* p) { return (int64_t)p->N * p->HK * div_up(group(p), 16); }
 int step_splits(const gdn_attn_problem* p, const gdn_kv_cache* c) {

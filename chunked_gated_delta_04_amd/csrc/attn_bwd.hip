@@ -19,15 +19,14 @@ namespace gdn {
 
 namespace {
 
+constexpr int kGradKeys = 64;  // keys a step of dq's kernel
+// rows a step of dk's and dv's kernel, in parts of 32
 template <int D>
-constexpr int kGradKeys = D == 64 ? 64 : 32;  // keys a step of dq's kernel
-constexpr int kGradRows = 32;                 // rows a step of dk's and dv's kernel
+constexpr int kGradRows = D == 256 ? 32 : 64;
+// workgroups that share a key tile's columns of dk and dv, with the scores formed in each
+template <int D>
+constexpr int kGradHalves = D == 256 ? 2 : 1;
 
-template <typename T>
-__device__ __forceinline__ uint4 operand(const f32x16& x, int h) {
-  return make_uint4(pack2<T>(x[8 * h], x[8 * h + 1]), pack2<T>(x[8 * h + 2], x[8 * h + 3]),
-                    pack2<T>(x[8 * h + 4], x[8 * h + 5]), pack2<T>(x[8 * h + 6], x[8 * h + 7]));
-}
 template <typename T>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   T x[8], y[8];
@@ -38,21 +37,18 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   for (int i = 0; i < 8; ++i) s = fmaf(to_f32(x[i]), to_f32(y[i]), s);
   return s;
 }
-__device__ __forceinline__ void zero16(f32x16& x) {
-#pragma unroll
-  for (int r = 0; r < 16; ++r) x[r] = 0.f;
-}
 
 }  // namespace
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
-  constexpr int kT = kGradKeys<D>, KB = kT / 32, DB = D / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kT * D];  // [buffer][k, v]
+__global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
+  constexpr int kT = kGradKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
+  typedef Tile<D, kT, kThreads> KTile;
+  __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int hk = blockIdx.x % pk.HK;
-  const int G = pk.G.by, per = kAttnRows / G;
+  const int G = pk.G.by, per = attn_rows(D) / G;
   const RowTile rt = find_tile(pk.cu, pk.N, pk.T, per, a.slots - 1 - blockIdx.x / pk.HK);
   if (rt.tokens <= 0) return;
   const int t0 = rt.first;
@@ -66,14 +62,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_q_kernel(Attn
   const int whi = t0 + min(divide(wave * 32 + 31, pk.G), rt.tokens - 1);
   const int64_t out = (int64_t)(rt.bos + t0 + token) * pk.HQ + head;
 
-  uint4 q[D / 16], g[D / 16];
+  uint4 q[N], g[N];
   float delta = 0.f, lse = INFINITY;  // weights of rows that see nothing are zeros
   {
     const uint16_t* pq = static_cast<const uint16_t*>(a.q) + (int64_t)(rt.bos + t0 + token) * a.q_stride + head * D + 8 * hi;
     const uint16_t* pg = static_cast<const uint16_t*>(a.dO) + out * D + 8 * hi;
     const uint16_t* po = static_cast<const uint16_t*>(a.o) + out * D + 8 * hi;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
+    for (int s = 0; s < N; ++s) {
       q[s] = g[s] = make_uint4(0, 0, 0, 0);
       if (live) {
         q[s] = *reinterpret_cast<const uint4*>(pq + 16 * s);
@@ -81,7 +77,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_q_kernel(Attn
         delta += dot8<T>(*reinterpret_cast<const uint4*>(po + 16 * s), g[s]);
       }
     }
-    delta += other_half(delta);
+    delta = sum_halves(delta);
     if (live) {
       lse = a.lse[out] * kLog2e;
       if (lse == kMinusInf) lse = INFINITY;
@@ -91,74 +87,98 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_q_kernel(Attn
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k) + rt.bos * a.k_stride + hk * D;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v) + rt.bos * a.v_stride + hk * D;
-  Staged<D, kT, 256> ks, vs;
-  auto load = [&](int i) {
+  auto load = [&](auto& k, auto& v, int i) {
     const int j0 = kt.at(i) * kT, len = min(kT, rt.len - j0);
-    ks.load(kbase + j0 * a.k_stride, (int)a.k_stride, len, tid);
-    vs.load(vbase + j0 * a.v_stride, (int)a.v_stride, len, tid);
+    KTile::load(k, kbase + j0 * a.k_stride, (int)a.k_stride, len, tid);
+    KTile::load(v, vbase + j0 * a.v_stride, (int)a.v_stride, len, tid);
   };
 
   f32x16 dq[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) zero16(dq[i]);
-  const float c = pk.scale * kLog2e;
+  const float c = pk.scale * kLog2e, scale = pk.scale;
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
 
-  if (kt.count > 0) {
-    load(0);
-    ks.store(lds[0][0], tid);
-    vs.store(lds[0][1], tid);
-  }
-  __syncthreads();
-  for (int i = 0, buf = 0; i < kt.count; ++i, buf ^= 1) {
-    const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
-    if (i + 1 < kt.count) load(i + 1);
-    bool some = wlo <= whi && j0 <= whi;
-    if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
-    if (some) {
-      const uint16_t *K = lds[buf][0], *V = lds[buf][1];
-      bool mask = j1 > wlo;
-      if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
-      const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        f32x16 s, dp;
-        zero16(s);
-        zero16(dp);
-        const int kf = fresh(ka);
-#pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          s = mfma32_of<T>(*reinterpret_cast<const uint4*>(K + (kf ^ (16 * d)) + 32 * kb * D), q[d], s);
-          dp = mfma32_of<T>(*reinterpret_cast<const uint4*>(V + (kf ^ (16 * d)) + 32 * kb * D), g[d], dp);
-        }
-        if (mask) {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = j0 + 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3);
-            const bool ok = j <= t && (j > from || j < pk.sinks);
-            dp[r] = ok ? exp2_fast(fmaf(s[r], c, -lse)) * (dp[r] - delta) * pk.scale : 0.f;
+  // 64 keys from j0 in LDS, in two halves. The matrix instructions go in the order S0, dO V0^T, S1, dO V1^T, dq of
+  // the first half, of the second, each with its LDS operand requested kAhead before; the vector unit
+  // forms the weights and the scores' gradients of a half during the products that follow it.
+  auto part = [&](auto masked, const uint16_t* K, const uint16_t* V, int j0) {
+    constexpr bool kMask = decltype(masked)::value;
+    constexpr int kAhead = 3;
+    f32x16 s[2], dp[2];
+    // positions relative to the lane's first key
+    const int first = j0 + 4 * hi, most = t - first, least = from - first, sunk = pk.sinks - first;
+    const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
+    uint4 op[kAhead], ds[4];
+    auto read = [&](auto slot) {
+      constexpr int n = slot, phase = n / N, d = n % N;
+      uint4& x = op[n % kAhead];
+      if constexpr (phase < 4)
+        x = *reinterpret_cast<const uint4*>((phase % 2 ? V : K) + (kf ^ (16 * d)) + 32 * (phase / 2) * D);
+      else
+        x = column8(K + (32 * (phase - 4) + 16 * (d / DB)) * D, c0 ^ (32 * (d % DB)), c1 ^ (32 * (d % DB)));
+    };
+    for_each<kAhead>(read);
+    for_each<6 * N>([&](auto slot) {
+      constexpr int n = slot, phase = n / N, d = n % N;
+      const uint4& x = op[n % kAhead];
+      if constexpr (phase >= 4) dq[d % DB] = mfma32_of<T>(x, ds[2 * (phase - 4) + d / DB], dq[d % DB]);
+      else if constexpr (phase % 2) dp[phase / 2] = mfma32_of<T>(x, g[d], d == 0 ? f32x16{} : dp[phase / 2]);
+      else s[phase / 2] = mfma32_of<T>(x, q[d], d == 0 ? f32x16{} : s[phase / 2]);
+      if constexpr (n + kAhead < 6 * N) read(std::integral_constant<int, n + kAhead>());
+      if constexpr (phase >= 1 && phase <= 4) {
+        constexpr int half = (phase - 1) / 2;
+        for_each<16>([&](auto element) {
+          constexpr int e = element;
+          if constexpr (e * N / 16 == d) {
+            if constexpr (phase % 2) {
+              constexpr int j = 32 * half + 8 * (e / 4) + e % 4;
+              const float w = exp2_fast(fmaf(s[half][e], c, -lse));
+              s[half][e] = !kMask || (j <= most && (j > least || j < sunk)) ? w : 0.f;
+            } else {
+              const float x2 = s[half][e] * (dp[half][e] - delta) * scale;
+              dp[half][e] = !kMask || s[half][e] != 0.f ? x2 : 0.f;  // a masked key's dO V^T may be anything
+            }
           }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 16; ++r) dp[r] = exp2_fast(fmaf(s[r], c, -lse)) * (dp[r] - delta) * pk.scale;
-        }
-        const int k0 = fresh(va), k1 = fresh(vb);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 ds = operand<T>(dp, h);
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-            dq[d] = mfma32_of<T>(column8(K + (32 * kb + 16 * h) * D, k0 ^ (32 * d), k1 ^ (32 * d)), ds, dq[d]);
+        });
+        if constexpr (phase % 2 == 0 && d == N - 1) {
+          ds[2 * half] = operand<T>(dp[half], 0);
+          ds[2 * half + 1] = operand<T>(dp[half], 1);
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  auto keep = [&] {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) keep_accumulated<D == 256>(dq[d]);
+  };
+
+  // one step: tile i in (k, v), the next one on its way to (nk, nv)
+  auto step = [&](int i, auto& k, auto& v, auto& nk, auto& nv) {
+    const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
+    if (i + 1 < kt.count) load(nk, nv, i + 1);
+    keep();
+    bool some = i < kt.count && wlo <= whi && j0 <= whi;
+    if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
+    if (some) {
+      bool mask = j1 > wlo;
+      if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
+      if (mask) part(std::true_type(), k, v, j0);
+      else part(std::false_type(), k, v, j0);
     }
-    if (i + 1 < kt.count) {
-      ks.store(lds[buf ^ 1][0], tid);
-      vs.store(lds[buf ^ 1][1], tid);
-    }
+    keep();
     __syncthreads();
+  };
+  if (kt.count > 0) load(k0, v0, 0);
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < kt.count; i += 2) {  // a step past the last tile does nothing
+    step(i, k0, v0, k1, v1);
+    step(i + 1, k1, v1, k0, v0);
   }
   if (!live) return;
   uint16_t* p = static_cast<uint16_t*>(a.dq) + out * D;
@@ -196,16 +216,19 @@ __device__ __forceinline__ float* part_at(const AttnGradArgs& a, int part, const
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(AttnGradArgs a) {
-  constexpr int kR = kGradRows, DB = D / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kR * D];  // [buffer][q, dO]
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kR];       // [buffer][lse, delta]
+__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(AttnGradArgs a) {
+  constexpr int kR = kGradRows<D>, kHalves = kGradHalves<D>, DB = D / 32 / kHalves;
+  typedef Tile<D, kR, 256> RTile;
+  __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
+  __shared__ __attribute__((aligned(16))) float stats[2][2][kR];               // [buffer][lse, delta]
   const AttnPack& pk = a.pack;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int G = pk.G.by;
   int b = blockIdx.x;
   const int hk = b % pk.HK;
   b /= pk.HK;
+  const int col0 = b % kHalves * (D / kHalves);
+  b /= kHalves;
   // first the rows behind the windows of the sinks' tiles, then all tiles' rows
   const int far_items = a.far_pieces * a.far_tiles * pk.N;
   const bool far = b < far_items;
@@ -260,9 +283,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(Att
   const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
   const float* lses = a.lse + (int64_t)kt.bos * pk.HQ + hk * G;
   const float* deltas = a.delta + (int64_t)kt.bos * pk.HQ + hk * G;
-  Staged<D, kR, 256> qs, gs;
   float lse = INFINITY, delta = 0.f;
-  auto load = [&](int r0) {
+  auto load = [&](auto& qs, auto& gs, int r0) {
     // offsets from the step's first token: its rows are of at most kR + 1 tokens
     const int first = divide(r0, pk.G);
     const __amdgpu_buffer_rsrc_t rq =
@@ -270,12 +292,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(Att
     const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint16_t*>(gbase) + (int64_t)first * pk.HQ * D, 0, 0x7ffffff0, kBufferWord3);
 #pragma unroll
-    for (int i = 0; i < qs.kPieces; ++i) {
-      const int r = r0 + qs.row(i, tid), token = divide(r, pk.G), h = r - token * G;
-      const int col = h * D + qs.column(tid);
+    for (int i = 0; i < RTile::kPieces; ++i) {
+      const int r = r0 + RTile::row(i, tid), token = divide(r, pk.G), h = r - token * G;
+      const int col = h * D + RTile::column(i, tid);
       const bool ok = r < to;  // others are past the resource: zeros
-      qs.x[i] = load_b128(rq, ok ? ((token - first) * (int)a.q_stride + col) * 2 : -1);
-      gs.x[i] = load_b128(rg, ok ? ((token - first) * pk.HQ * D + col) * 2 : -1);
+      RTile::request(qs, i, rq, ok ? ((token - first) * (int)a.q_stride + col) * 2 : -1, tid);
+      RTile::request(gs, i, rg, ok ? ((token - first) * pk.HQ * D + col) * 2 : -1, tid);
     }
     if (tid < kR) {
       const int r = r0 + tid, token = divide(r, pk.G), h = r - token * G;
@@ -288,9 +310,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(Att
       }
     }
   };
-  auto store = [&](int buf) {
-    qs.store(lds[buf][0], tid);
-    gs.store(lds[buf][1], tid);
+  auto store_stats = [&](int buf) {
     if (tid < kR) {
       stats[buf][0][tid] = lse;
       stats[buf][1][tid] = delta;
@@ -303,66 +323,114 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(Att
     zero16(dk[i]);
     zero16(dv[i]);
   }
-  const float c = pk.scale * kLog2e;
+  const float c = pk.scale * kLog2e, scale = pk.scale;
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
-  const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  const int va = at<D>(vr, col0 + vc), vb = at<D>(vr + 8, col0 + vc);
   // rows that see any and all of the wave's keys
   const int64_t any_from = far ? (int64_t)(wlo + W) * G : (int64_t)wlo * G;
   const int64_t any_to = far ? (wlo < pk.sinks ? lim : 0) : W ? ((int64_t)whi + W) * G : lim;
   const int64_t all_from = far ? (whi < pk.sinks ? (int64_t)(whi + W) * G : none) : (int64_t)whi * G;
   const int64_t all_to = !far && W ? ((int64_t)wlo + W) * G : lim;
 
+  // 32 rows at r0 with their q, dO and stats in LDS. The matrix instructions go in the order S, dO V^T, dv, dk, each
+  // with its LDS operand requested kAhead before, and what the vector unit does in between: the weights
+  // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.)
+  auto part = [&](auto masked, const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0) {
+    constexpr bool kMask = decltype(masked)::value;
+    constexpr int N = D / 16, M = 2 * DB, kSlots = 2 * N + 2 * M, kAhead = 3;
+    f32x16 s, dp;
+    const int least = lo - r0 - 4 * hi, most = up - r0 - 4 * hi;  // relative to the lane's first row
+    const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
+    uint4 op[kAhead], p[2], ds[2];
+    auto read = [&](auto slot) {
+      constexpr int n = slot;
+      uint4& x = op[n % kAhead];
+      if constexpr (n < 2 * N) {
+        x = *reinterpret_cast<const uint4*>((n < N ? Q : O) + (kf ^ (16 * (n % N))));
+      } else {
+        constexpr int d = (n - 2 * N) % M;
+        x = column8((n < 2 * N + M ? O : Q) + 16 * (d / DB) * D, c0 ^ (32 * (d % DB)), c1 ^ (32 * (d % DB)));
+      }
+    };
+    f32x4 stat;
+    for_each<kAhead>(read);
+    for_each<kSlots>([&](auto slot) {
+      constexpr int n = slot;
+      const uint4& x = op[n % kAhead];
+      if constexpr (n < N) {
+        s = mfma32_of<T>(x, k[n], n == 0 ? f32x16{} : s);
+      } else if constexpr (n < 2 * N) {
+        dp = mfma32_of<T>(x, v[n - N], n == N ? f32x16{} : dp);
+      } else if constexpr (n < 2 * N + M) {
+        constexpr int d = n - 2 * N;
+        dv[d % DB] = mfma32_of<T>(x, p[d / DB], dv[d % DB]);
+      } else {
+        constexpr int d = n - 2 * N - M;
+        dk[d % DB] = mfma32_of<T>(x, ds[d / DB], dk[d % DB]);
+      }
+      if constexpr (n + kAhead < kSlots) read(std::integral_constant<int, n + kAhead>());
+      // the weights of 16 rows, then their gradients
+      for_each<16>([&](auto element) {
+        constexpr int e = element;
+        if constexpr (n == N + e * N / 16) {
+          if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(ls + 2 * e + 4 * hi);
+          const float w = exp2_fast(fmaf(s[e], c, -stat[e % 4]));
+          constexpr int row = 8 * (e / 4) + e % 4;
+          s[e] = !kMask || (row >= least && row < most) ? w : 0.f;
+        }
+        if constexpr (n == 2 * N + e * M / 16) {
+          if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(de + 2 * e + 4 * hi);
+          const float g = s[e] * (dp[e] - stat[e % 4]) * scale;
+          dp[e] = !kMask || s[e] != 0.f ? g : 0.f;  // a masked row's dO V^T may be anything
+        }
+      });
+      if constexpr (n == 2 * N - 1) {
+        p[0] = operand<T>(s, 0);
+        p[1] = operand<T>(s, 1);
+      }
+      if constexpr (n == 2 * N + M - 1) {
+        ds[0] = operand<T>(dp, 0);
+        ds[1] = operand<T>(dp, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+
+  auto keep = [&] {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) {
+      keep_accumulated<(D >= 128)>(dk[d]);
+      keep_accumulated<(D >= 128)>(dv[d]);
+    }
+  };
+
+  // one step: rows from r0 in (q, g), the next ones on their way to (nq, ng)
+  auto step = [&](int r0, int buf, auto& q, auto& g, auto& nq, auto& ng) {
+    if (r0 + kR < to) load(nq, ng, r0 + kR);
+#pragma unroll 1
+    for (int i = 0; i < kR; i += 32) {
+      const int r = r0 + i;
+      keep();
+      if (r + 32 > any_from && r < any_to && r < to && wlo < kt.len) {
+        const float *ls = stats[buf][0] + i, *de = stats[buf][1] + i;
+        if (r < all_from || r + 32 > all_to) part(std::true_type(), q + i * D, g + i * D, ls, de, r);
+        else part(std::false_type(), q + i * D, g + i * D, ls, de, r);
+      }
+      keep();
+    }
+    if (r0 + kR < to) store_stats(buf ^ 1);
+    __syncthreads();
+  };
   if (from < to) {
-    load(from);
-    store(0);
+    load(q0, g0, from);
+    store_stats(0);
   }
   __syncthreads();
-  for (int r0 = from, buf = 0; r0 < to; r0 += kR, buf ^= 1) {
-    if (r0 + kR < to) load(r0 + kR);
-    if (r0 + kR > any_from && r0 < any_to && wlo < kt.len) {
-      const uint16_t *Q = lds[buf][0], *O = lds[buf][1];
-      f32x16 s, dp;
-      zero16(s);
-      zero16(dp);
-      const int kf = fresh(ka);
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        s = mfma32_of<T>(*reinterpret_cast<const uint4*>(Q + (kf ^ (16 * d))), k[d], s);
-        dp = mfma32_of<T>(*reinterpret_cast<const uint4*>(O + (kf ^ (16 * d))), v[d], dp);
-      }
-      const bool mask = r0 < all_from || r0 + kR > all_to;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const f32x4 ls = *reinterpret_cast<const f32x4*>(stats[buf][0] + 8 * n + 4 * hi);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(stats[buf][1] + 8 * n + 4 * hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * n + e;
-          float p = exp2_fast(fmaf(s[r], c, -ls[e])), x = p * (dp[r] - de[e]) * pk.scale;
-          if (mask) {
-            const int rr = r0 + 8 * n + 4 * hi + e;
-            const bool ok = rr >= lo && rr < up;
-            p = ok ? p : 0.f;
-            x = ok ? x : 0.f;
-          }
-          s[r] = p;
-          dp[r] = x;
-        }
-      }
-      const int c0 = fresh(va), c1 = fresh(vb);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 p = operand<T>(s, h), ds = operand<T>(dp, h);
-#pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          dv[d] = mfma32_of<T>(column8(O + 16 * h * D, c0 ^ (32 * d), c1 ^ (32 * d)), p, dv[d]);
-          dk[d] = mfma32_of<T>(column8(Q + 16 * h * D, c0 ^ (32 * d), c1 ^ (32 * d)), ds, dk[d]);
-        }
-      }
-    }
-    if (r0 + kR < to) store(buf ^ 1);
-    __syncthreads();
+#pragma unroll 1
+  for (int r0 = from; r0 < to; r0 += 2 * kR) {  // a step past the last row does nothing
+    step(r0, 0, q0, g0, q1, g1);
+    step(r0 + kR, 1, q1, g1, q0, g0);
   }
   if (!live) return;
   const bool sunk = j / kAttnKeys < a.far_tiles;
@@ -373,12 +441,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_grad_kv_kernel(Att
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const int col = 32 * d + 8 * n + 4 * hi;
+        const int col = col0 + 32 * d + 8 * n + 4 * hi;
         *reinterpret_cast<f32x4*>(p + col) = f32x4{dk[d][4 * n], dk[d][4 * n + 1], dk[d][4 * n + 2], dk[d][4 * n + 3]};
         *reinterpret_cast<f32x4*>(p + D + col) = f32x4{dv[d][4 * n], dv[d][4 * n + 1], dv[d][4 * n + 2], dv[d][4 * n + 3]};
       }
   } else {
-    const int64_t at = ((int64_t)(kt.bos + j) * pk.HK + hk) * D;
+    const int64_t at = ((int64_t)(kt.bos + j) * pk.HK + hk) * D + col0;
     uint16_t *pd = static_cast<uint16_t*>(a.dk) + at, *pv = static_cast<uint16_t*>(a.dv) + at;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -428,11 +496,11 @@ template <typename T, int D>
 hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
   const AttnPack& pk = a.pack;
   const dim3 block(256);
-  hipLaunchKernelGGL((attn_grad_q_kernel<T, D>), dim3(a.slots * pk.HK), block, 0, s, a);
+  hipLaunchKernelGGL((attn_grad_q_kernel<T, D>), dim3(a.slots * pk.HK), dim3(2 * attn_rows(D)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int items = a.far_pieces * a.far_tiles * pk.N + a.pieces * a.key_slots;
-  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), block, 0, s, a);
+  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK * kGradHalves<D>), block, 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tiles = a.pieces > 1 ? a.key_slots : a.far_tiles * pk.N;

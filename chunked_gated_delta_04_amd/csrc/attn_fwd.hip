@@ -23,24 +23,23 @@ namespace gdn {
 
 namespace {
 
-// keys a tile
-template <int D>
-constexpr int kFwdKeys = 64;
+constexpr int kFwdKeys = 64;  // keys a tile
 
 }  // namespace
 
 template <typename T, int D, bool kPaged>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArgs a) {
-  constexpr int kT = kFwdKeys<D>, KB = kT / 32, DB = D / 32;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2][2][kT * D];  // [buffer][k, v]
+__global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArgs a) {
+  constexpr int kT = kFwdKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
+  typedef Tile<D, kT, kThreads> KTile;
+  __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, l32 = lane & 31, hi = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   // the last rows of a sequence, which see the most keys, first
   int b = blockIdx.x;
   const int hk = b % pk.HK;
   b /= pk.HK;
   const int split = b % a.splits;
-  const int G = pk.G.by, per = kAttnRows / G;
+  const int G = pk.G.by, per = attn_rows(D) / G;
   const RowTile rt = find_tile(pk.cu, pk.N, pk.T, per, a.slots - 1 - b / a.splits);
   if (rt.tokens <= 0) return;
 
@@ -63,12 +62,25 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArg
   const int wlo = t0 + divide(wave * 32, pk.G);
   const int whi = t0 + min(divide(wave * 32 + 31, pk.G), rt.tokens - 1);
   const int64_t out = (int64_t)(rt.bos + rt.first + token) * pk.HQ + head;  // row of o
+  const int64_t all = (int64_t)pk.T * pk.HQ;
 
-  uint4 q[D / 16];
+  if (part.x >= part.y) {  // nothing to see, or nothing left for this split
+    if (!live || hi) return;
+    if (a.splits > 1) {  // the join reads no sums of weight 0
+      *reinterpret_cast<float2*>(a.part + all * a.splits * D + 2 * (all * split + out)) = make_float2(kMinusInf, 0.f);
+    } else {
+      uint4* po = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out * D);
+      for (int i = 0; i < D / 8; ++i) po[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse) a.lse[out] = kMinusInf;
+    }
+    return;
+  }
+
+  uint4 q[N];
   {
     const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(rt.bos + rt.first + token) * a.q_stride + head * D + 8 * hi;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
+    for (int s = 0; s < N; ++s) {
       q[s] = make_uint4(0, 0, 0, 0);
       if (live) q[s] = *reinterpret_cast<const uint4*>(p + 16 * s);
     }
@@ -83,132 +95,151 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArg
     kbase += rt.bos * a.k_stride + hk * D;
     vbase += rt.bos * a.v_stride + hk * D;
   }
-
-  Staged<D, kT, 256> ks, vs;
-  int id = 0;                 // page of row `lane` of the tile after the next
-  uint64_t seen_next = ~0ull; // which rows of the next tile have a page
-  auto look = [&](int i) {
-    if constexpr (kPaged) id = i < part.y ? page_of(a.pages, rt.seq, kt.at(i) * kT + lane, (int)keys) : 0;
+  // paged: where row `lane` of tiles i, i + 1 and i + 2 is
+  int64_t rows[3] = {-1, -1, -1};
+  auto look = [&](int i) -> int64_t {
+    return kPaged && i < part.y ? row_at(a.pages, rt.seq, kt.at(i) * kT + lane, keys) : -1;
   };
-  auto load = [&](int i) {
-    const int j0 = kt.at(i) * kT;
+  auto load = [&](auto& to, const uint16_t* base, int64_t stride, int i, int64_t at) {
     if constexpr (kPaged) {
-      seen_next = __ballot(id > 0);
-#pragma unroll
-      for (int n = 0; n < ks.kPieces; ++n) {
-        const int r = ks.row(n, tid), pid = __shfl(id, r);
-        ks.x[n] = vs.x[n] = make_uint4(0, 0, 0, 0);
-        if (pid > 0) {
-          const int64_t off = row_of(a.pages, pid, j0 + r) + ks.column(tid);
-          ks.x[n] = *reinterpret_cast<const uint4*>(kbase + off);
-          vs.x[n] = *reinterpret_cast<const uint4*>(vbase + off);
-        }
-      }
-      look(i + 1);
+      KTile::gather(to, base, at, tid);
     } else {
-      const int len = min(kT, rt.len - j0);
-      ks.load(kbase + j0 * a.k_stride, (int)a.k_stride, len, tid);
-      vs.load(vbase + j0 * a.v_stride, (int)a.v_stride, len, tid);
+      const int j0 = kt.at(i) * kT;
+      KTile::load(to, base + j0 * stride, (int)stride, min(kT, rt.len - j0), tid);
     }
   };
 
   f32x16 o[DB];
 #pragma unroll
-  for (int i = 0; i < DB; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) o[i][r] = 0.f;
+  for (int i = 0; i < DB; ++i) zero16(o[i]);
   float m = kMinusInf, l = 0.f;
   const float c = pk.scale * kLog2e;
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
 
-  if (part.x < part.y) {
-    look(part.x);
-    load(part.x);
-    ks.store(lds[0][0], tid);
-    vs.store(lds[0][1], tid);
-  }
-  __syncthreads();
-  for (int i = part.x, buf = 0; i < part.y; ++i, buf ^= 1) {
-    const uint64_t seen = seen_next;
-    const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
-    if (i + 1 < part.y) load(i + 1);
-    // rows of this wave that see a key of the tile
-    bool some = wlo <= whi && j0 <= whi;
-    if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
-    if (some) {
-      const uint16_t *K = lds[buf][0], *V = lds[buf][1];
-      f32x16 s[KB];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[kb][r] = 0.f;
-      const int kf = fresh(ka);
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          s[kb] = mfma32_of<T>(*reinterpret_cast<const uint4*>(K + (kf ^ (16 * d)) + 32 * kb * D), q[d], s[kb]);
-      bool mask = j1 > wlo;
-      if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
-      if constexpr (kPaged) mask = mask || ~seen != 0;
-      if (mask) {
-        const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int jr = 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3), j = j0 + jr;
-            bool ok = j <= t && (j > from || j < pk.sinks);
-            if constexpr (kPaged) ok = ok && (seen >> jr & 1);
-            s[kb][r] = ok ? s[kb][r] : kMinusInf;
+  // One step: the weights p of a tile from its scores s, while the matrix unit forms the next tile's scores `next` from K
+  // and adds the tile before's weights times V, `before`, to O. A slot has one matrix instruction of each and a share of
+  // the vector unit's work; the LDS operands are requested kAhead slots before.
+  auto step = [&](f32x16(&s)[2], f32x16(&next)[2], uint4(&p)[4], const uint4(&before)[4], const uint16_t* K,
+                  const uint16_t* V, int j0, uint64_t seen) {
+    constexpr int kSlots = 2 * N, kTop = kSlots / 4, kAhead = 2;
+    bool mask = j0 + kT - 1 > wlo;
+    if (pk.window) mask = mask || (j0 <= whi - pk.window && j0 + kT > pk.sinks);
+    if constexpr (kPaged) mask = mask || ~seen != 0;
+    if (mask) {
+      // against constants: positions and the pages' bits relative to the lane's first key
+      const int first = j0 + 4 * hi, most = t - first, least = from - first, far = pk.sinks - first;
+      const uint64_t has = seen >> (4 * hi);
+      for_each<32>([&](auto element) {
+        constexpr int e = element, r = e % 16, j = 32 * (e / 16) + 8 * (r / 4) + r % 4;
+        bool ok = j <= most && (j > least || j < far);
+        if constexpr (kPaged) ok = ok && (has >> j & 1);
+        s[e / 16][r] = ok ? s[e / 16][r] : kMinusInf;
+      });
+    }
+    const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
+    uint4 ko[kAhead], vo[kAhead];
+    auto read = [&](auto slot) {
+      constexpr int n = slot;
+      ko[n % kAhead] = *reinterpret_cast<const uint4*>(K + (kf ^ (16 * (n / 2))) + 32 * (n % 2) * D);
+      vo[n % kAhead] = column8(V + 16 * (n / DB) * D, c0 ^ (32 * (n % DB)), c1 ^ (32 * (n % DB)));
+    };
+    for_each<kAhead>(read);
+    float top = kMinusInf, base = 0.f, f = 1.f, sum[2] = {0.f, 0.f};
+    for_each<kSlots>([&](auto slot) {
+      constexpr int n = slot;
+      next[n % 2] = mfma32_of<T>(ko[n % kAhead], q[n / 2], n < 2 ? f32x16{} : next[n % 2]);
+      o[n % DB] = mfma32_of<T>(vo[n % kAhead], before[n / DB], o[n % DB]);
+      if constexpr (n + kAhead < kSlots) read(std::integral_constant<int, n + kAhead>());
+      for_each<32>([&](auto element) {
+        constexpr int e = element;
+        if constexpr (e * kTop / 32 == n) top = fmaxf(top, s[e / 16][e % 16]);
+      });
+      if constexpr (n == kTop - 1) {
+        const float2 tops = both_halves(top);
+        top = fmaxf(tops.x, tops.y) * c;
+        // The maximum that weights are relative to follows only where the row's has grown by a
+        // factor of 2^8: weights up to that are as exact.
+        const float now = top > m + 8.f ? top : m;
+        base = now == kMinusInf ? 0.f : now;  // a row that has seen nothing yet
+        f = exp2_fast(m - base);
+        m = now;
+      }
+      for_each<32>([&](auto element) {
+        constexpr int e = element;
+        if constexpr (kTop + e * (kSlots - kTop) / 32 == n) {
+          const float x = exp2_fast(fmaf(s[e / 16][e % 16], c, -base));
+          s[e / 16][e % 16] = x;
+          sum[e % 2] += x;
+          if constexpr (e % 8 == 7) {
+            p[e / 8] = operand<T>(s[e / 16], e / 8 % 2);
+            stay_here(p[e / 8]);
           }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kb][r]);
-      top = fmaxf(top, other_half(top)) * c;
-      const float now = fmaxf(m, top);
-      const float base = now == kMinusInf ? 0.f : now;  // a row that has seen nothing yet
-      if (__any(now > m)) {
-        const float f = exp2_fast(m - base);
-        l *= f;
-#pragma unroll
-        for (int i2 = 0; i2 < DB; ++i2)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[i2][r] *= f;
-      }
-      m = now;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          s[kb][r] = exp2_fast(fmaf(s[kb][r], c, -base));
-          l += s[kb][r];
         }
-      }
-      const int v0 = fresh(va), v1 = fresh(vb);
+      });
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    l = fmaf(l, f, sum[0] + sum[1]);
+    if (__any(f != 1.f)) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 p = make_uint4(pack2<T>(s[kb][8 * h], s[kb][8 * h + 1]), pack2<T>(s[kb][8 * h + 2], s[kb][8 * h + 3]),
-                                     pack2<T>(s[kb][8 * h + 4], s[kb][8 * h + 5]), pack2<T>(s[kb][8 * h + 6], s[kb][8 * h + 7]));
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-            o[d] = mfma32_of<T>(column8(V + (32 * kb + 16 * h) * D, v0 ^ (32 * d), v1 ^ (32 * d)), p, o[d]);
-        }
+      for (int d = 0; d < DB; ++d) o[d] *= f;
     }
-    if (i + 1 < part.y) {
-      ks.store(lds[buf ^ 1][0], tid);
-      vs.store(lds[buf ^ 1][1], tid);
-    }
+  };
+  auto keep = [&] {
+#pragma unroll
+    for (int d = 0; d < DB; ++d) keep_accumulated<D == 256>(o[d]);
+  };
+
+  // K of the first two tiles, scores of the first; the weights before it are zeros, and so is their V
+  f32x16 s0[2], s1[2];
+  uint4 p0[4], p1[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p1[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int n = 0; n < 3; ++n) rows[n] = look(part.x + n);
+  load(k0, kbase, a.k_stride, part.x, rows[0]);
+  if (part.x + 1 < part.y) load(k1, kbase, a.k_stride, part.x + 1, rows[1]);
+  for (int i = tid; i < kT * D / 8; i += kThreads) reinterpret_cast<uint4*>(v1)[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < N; ++d)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+      s0[kb] = mfma32_of<T>(*reinterpret_cast<const uint4*>(k0 + (ka ^ (16 * d)) + 32 * kb * D), q[d],
+                            d == 0 ? f32x16{} : s0[kb]);
+  __syncthreads();
+  // Step i has K of tile i + 1 and V of tile i - 1 in LDS; K of i + 2 and V of i come into the other buffers meanwhile.
+  auto turn = [&](int i, auto& nk, auto& nv, const uint16_t* K, const uint16_t* V, f32x16(&s)[2], f32x16(&next)[2],
+                  uint4(&p)[4], const uint4(&before)[4]) {
+    uint64_t seen = ~0ull;
+    if constexpr (kPaged) seen = __ballot(rows[0] >= 0);
+    if (i + 2 < part.y) load(nk, kbase, a.k_stride, i + 2, rows[2]);
+    if (i < part.y) load(nv, vbase, a.v_stride, i, rows[0]);
+    rows[0] = rows[1];
+    rows[1] = rows[2];
+    rows[2] = look(i + 3);
+    keep();
+    // past the last tile no row sees anything
+    step(s, next, p, before, K, V, i < part.y ? kt.at(i) * kT : whi + 64, seen);
+    keep();
     __syncthreads();
+  };
+#pragma unroll 1
+  for (int i = part.x; i < part.y; i += 2) {
+    turn(i, k0, v0, k1, v1, s0, s1, p0, p1);
+    turn(i + 1, k1, v1, k0, v0, s1, s0, p1, p0);
   }
-  l += other_half(l);
+  if ((part.y - part.x) % 2 == 0) {  // else the step past the last tile has added it
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        o[d] = mfma32_of<T>(column8(v1 + 16 * i * D, va ^ (32 * d), vb ^ (32 * d)), p1[i], o[d]);
+  }
+
+  l = sum_halves(l);
   if (!live) return;
   if (a.splits == 1) {
     const float f = l > 0.f || l != l ? 1.f / l : 0.f;  // a row that sees nothing is zeros
@@ -220,10 +251,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArg
         *reinterpret_cast<uint4*>(po + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(o[d], u, f);
     if (a.lse && hi == 0) a.lse[out] = (m + log2f(l)) * 0.6931471805599453f;
   } else {
-    const int64_t rows = (int64_t)pk.T * pk.HQ, at = rows * split + out;
-    float* ml = a.part + rows * a.splits * D + 2 * at;
-    if (hi == 0) *reinterpret_cast<float2*>(ml) = make_float2(m, l);
-    if (part.x >= part.y) return;  // the join reads no sums of weight 0
+    const int64_t at = all * split + out;
+    if (hi == 0) *reinterpret_cast<float2*>(a.part + all * a.splits * D + 2 * at) = make_float2(m, l);
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -281,7 +310,7 @@ namespace {
 
 template <typename T>
 hipError_t fwd_of(int D, bool paged, const AttnArgs& a, hipStream_t s) {
-  const dim3 grid(a.slots * a.pack.HK * a.splits), block(256);
+  const dim3 grid(a.slots * a.pack.HK * a.splits), block(2 * attn_rows(D));
 #define GDN_FWD(d)                                                                                \
   if (paged) hipLaunchKernelGGL((attn_fwd_kernel<T, d, true>), grid, block, 0, s, a);             \
   else hipLaunchKernelGGL((attn_fwd_kernel<T, d, false>), grid, block, 0, s, a)

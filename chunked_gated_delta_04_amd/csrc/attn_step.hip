@@ -18,6 +18,28 @@ namespace {
 
 constexpr int kStepKeys = 32;
 
+// kT rows of D elements of a cache on their way through a wave's registers into its LDS, 16 bytes a piece.
+template <int D, int kT>
+struct Staged {
+  static constexpr int kPieces = kT * D / 8 / 64, kRows = 64 / (D / 8);  // rows a piece of all lanes
+  uint4 x[kPieces];
+  static __device__ __forceinline__ int row(int i, int lane) { return lane / (D / 8) + i * kRows; }
+  static __device__ __forceinline__ int column(int lane) { return lane % (D / 8) * 8; }
+  // lane r has the offset of row r, or -1 for zeros
+  __device__ __forceinline__ void gather(const uint16_t* p, int64_t rows, int lane) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t off = from_lane(rows, row(i, lane));
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (off >= 0) x[i] = *reinterpret_cast<const uint4*>(p + off + column(lane));
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* tile, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(tile + at<D>(row(i, lane), column(lane))) = x[i];
+  }
+};
+
 }  // namespace
 
 template <typename T, int D>
@@ -55,29 +77,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   const uint16_t* vbase = static_cast<const uint16_t*>(a.pages.v) + hk * a.pages.head_stride;
   uint16_t *K = lds + wave * 2 * kT * D, *V = K + kT * D;
 
-  Staged<D, kT, 64> ks, vs;
-  int id = 0;             // page of row lane % 32 of the tile after the next, 0 where it is not seen
+  Staged<D, kT> ks, vs;
+  int64_t at_next = -1;   // where row lane % 32 of the tile after the next is, -1 where it is not seen
   uint32_t seen_next = 0; // the rows of the next tile that are seen
   auto look = [&](int i) {
-    id = 0;
+    at_next = -1;
     if (i < part.y) {
       const int j = kt.at(i) * kT + (lane & 31);
-      if (j > from || j < pk.sinks) id = page_of(a.pages, seq, j, (int)keys);
+      if (j > from || j < pk.sinks) at_next = row_at(a.pages, seq, j, keys);
     }
   };
   auto load = [&](int i) {
-    const int j0 = kt.at(i) * kT;
-    seen_next = (uint32_t)__ballot(id > 0);
-#pragma unroll
-    for (int n = 0; n < ks.kPieces; ++n) {
-      const int r = ks.row(n, lane), pid = __shfl(id, r);
-      ks.x[n] = vs.x[n] = make_uint4(0, 0, 0, 0);
-      if (pid > 0) {
-        const int64_t off = row_of(a.pages, pid, j0 + r) + ks.column(lane);
-        ks.x[n] = *reinterpret_cast<const uint4*>(kbase + off);
-        vs.x[n] = *reinterpret_cast<const uint4*>(vbase + off);
-      }
-    }
+    seen_next = (uint32_t)__ballot(at_next >= 0);
+    ks.gather(kbase, at_next, lane);
+    vs.gather(vbase, at_next, lane);
     look(i + 4);
   };
 

@@ -2,11 +2,24 @@
 // and a tile's way from memory into LDS.
 #pragma once
 
+#include <utility>
+
 #include "attn.h"
 
 namespace gdn {
 
 constexpr float kMinusInf = -INFINITY;
+
+// f(0), f(1), .. f(N - 1) with compile-time numbers: register arrays are then indexed by constants
+// however long the body is.
+template <int... I, class F>
+__device__ __forceinline__ void for_each_of(std::integer_sequence<int, I...>, const F& f) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void for_each(const F& f) {
+  for_each_of(std::make_integer_sequence<int, N>(), f);
+}
 
 // A tile of a pack's query rows: tokens first .. first + tokens - 1 of a sequence of `len` tokens that
 // begins at bos.
@@ -63,44 +76,63 @@ __device__ __forceinline__ int2 split_of(int count, int splits, int split, int l
   return make_int2((int)min(from, (int64_t)count), (int)min(from + per, (int64_t)count));
 }
 
-// kT rows of D elements on their way through kThreads threads' registers into LDS, 16 bytes a piece.
-template <int D, int kT, int kThreads>
-struct Staged {
-  static constexpr int kPieces = kT * D / 8 / kThreads, kRows = kThreads / (D / 8);  // rows a piece of all threads
-  uint4 x[kPieces];
-  static __device__ __forceinline__ int row(int i, int tid) { return tid / (D / 8) + i * kRows; }
-  static __device__ __forceinline__ int column(int tid) { return tid % (D / 8) * 8; }
-  // rows [0, len) of token rows at p; the others are zeros
-  __device__ __forceinline__ void load(const uint16_t* p, int stride, int len, int tid) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(p), 0, len > 0 ? ((len - 1) * stride + D) * 2 : 0, kBufferWord3);
-    const int at = (row(0, tid) * stride + column(tid)) * 2;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) x[i] = load_b128(r, at + i * kRows * stride * 2);
-  }
-  __device__ __forceinline__ void store(uint16_t* tile, int tid) const {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(tile + at<D>(row(i, tid), column(tid))) = x[i];
-  }
-};
-
 // Tokens that a sequence had before, so that the positions of T more, rounded up to a tile, are 32 bits
 // whatever the caller's array holds.
 __device__ __forceinline__ int past_of(const KvPages& c, int seq, int T) {
   return __builtin_amdgcn_readfirstlane(min(max(c.offsets[seq], -(1 << 30)), 0x7fffff00 - T));
 }
-// the page of the key at position j, or 0 for none
-__device__ __forceinline__ int page_of(const KvPages& c, int seq, int j, int keys) {
-  if (j < 0 || j >= keys) return 0;
+// Element offset of the row of position j of a sequence in the cache, or -1 where it has none.
+__device__ __forceinline__ int64_t row_at(const KvPages& c, int seq, int j, int64_t keys) {
+  if (j < 0 || j >= keys) return -1;
   const int col = divide(j, c.page);
-  if (col >= c.columns) return 0;
+  if (col >= c.columns) return -1;
   const int id = c.table[seq * c.table_stride + col];
-  return id < c.pages ? max(id, 0) : 0;
+  return id > 0 && id < c.pages ? id * c.page_stride + (j - col * c.page.by) * c.token_stride : -1;
 }
-// offset of a row of page id > 0
-__device__ __forceinline__ int64_t row_of(const KvPages& c, int id, int j) {
-  return id * c.page_stride + (j - divide(j, c.page) * c.page.by) * c.token_stride;
+__device__ const uint4 zeros[1] = {};
+__device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
+  const int lo = __shfl((int)x, lane), hi = __shfl((int)(x >> 32), lane);
+  return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
 }
+
+// kT rows of D elements from memory into LDS by kThreads threads, 16 bytes a lane, without a stop in
+// registers: request i of a wave fills the 64 pieces from (i waves + wave) 64 on, each lane fetching
+// the piece of its row that belongs there (see piece_of). A barrier waits for them. Buffers that are filled while
+// others are read are variables of their own: the compiler waits for a request in flight before any read
+// of the same variable.
+template <int D, int kT, int kThreads>
+struct Tile {
+  static constexpr int kPieces = kT * D / 8 / kThreads, kRows = kThreads / (D / 8);  // rows a request of all threads
+  static_assert(kPieces * kThreads * 8 == kT * D, "whole requests");
+  typedef uint16_t Lds[kT * D];
+  static __device__ __forceinline__ int row(int i, int tid) { return tid / (D / 8) + i * kRows; }
+  static __device__ __forceinline__ int column(int i, int tid) {
+    return (tid % (D / 8) ^ piece_of<D>(row(i, tid))) * 8;
+  }
+  static __device__ __forceinline__ __attribute__((address_space(3))) void* to(Lds& tile, int i, int tid) {
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    return (__attribute__((address_space(3))) void*)(tile + (i * (kThreads / 64) + wave) * 64 * 8);
+  }
+  // rows [0, len) of token rows at p; the others are past the resource: zeros
+  static __device__ __forceinline__ void load(Lds& tile, const uint16_t* p, int stride, int len, int tid) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(p), 0, len > 0 ? ((len - 1) * stride + D) * 2 : 0, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) request(tile, i, r, (row(i, tid) * stride + column(i, tid)) * 2, tid);
+  }
+  static __device__ __forceinline__ void request(Lds& tile, int i, __amdgpu_buffer_rsrc_t r, int byte_off, int tid) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to(tile, i, tid), 16, byte_off, 0, 0, 0);
+  }
+  // rows of a cache's pages: lane r of each wave has the offset of row r, or -1 for zeros
+  static __device__ __forceinline__ void gather(Lds& tile, const uint16_t* p, int64_t rows, int tid) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t off = from_lane(rows, row(i, tid) & 63);
+      const void* from = off >= 0 ? static_cast<const void*>(p + off + column(i, tid)) : zeros;
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)from, to(tile, i, tid), 16, 0, 0);
+    }
+  }
+};
 
 // 16 bytes for each lane from the accumulator of 32 x 32: rows 8 b + 4 (lane / 32) + r are columns of
 // the output. Lanes 0-31 get the 8 columns of b = 2 u, lanes 32-63 those of b = 2 u + 1.
@@ -117,6 +149,37 @@ __device__ __forceinline__ uint4 eight_columns(const f32x16& x, int u, float f) 
   }
   return make_uint4(a[0], a[1], b[0], b[1]);
 }
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// Keeps an accumulator where it is between the steps of a loop: in the accumulation registers where a wave
+// has a SIMD to itself (kAcc). The compiler's own choice moved it to other registers and back every
+// step, and spilled what they held.
+template <bool kAcc>
+__device__ __forceinline__ void keep_accumulated(f32x16& x) {
+  if constexpr (kAcc) asm volatile("" : "+a"(x));
+  else asm volatile("" : "+v"(x));
+}
+// a lane's value and the other half's
+__device__ __forceinline__ float2 both_halves(float x) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const float2 y = both_halves(x);
+  return y.x + y.y;
+}
+
+// Operand of a second product from the accumulator of the first: rows 16 h .. 16 h + 15 of it in the order
+// that transposing reads at rows 4 (lane / 32) and 8 + 4 (lane / 32) take.
+template <typename T>
+__device__ __forceinline__ uint4 operand(const f32x16& x, int h) {
+  return make_uint4(pack2<T>(x[8 * h], x[8 * h + 1]), pack2<T>(x[8 * h + 2], x[8 * h + 3]),
+                    pack2<T>(x[8 * h + 4], x[8 * h + 5]), pack2<T>(x[8 * h + 6], x[8 * h + 7]));
+}
+// Values whose place among the matrix instructions the compiler keeps: it moves what no instruction of a
+// block needs to the blocks behind it.
+__device__ __forceinline__ void stay_here(uint4& x) { asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w)); }
+__device__ __forceinline__ void zero16(f32x16& x) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) x[r] = 0.f;
+}
 
 }  // namespace gdn

@@ -54,12 +54,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a, int first)
     const int64_t pos = (int64_t)a.pages.offsets[at.seq] + at.at;
     if (lane == 0) {
       live[mine] = at.live;
-      int64_t row = -1;
-      if (at.live && pos >= 0 && pos < (int64_t)a.pages.columns * a.pages.page.by && pos < 0x7fffffff) {
-        const int id = page_of(a.pages, at.seq, (int)pos, 0x7fffffff);
-        if (id > 0) row = row_of(a.pages, id, (int)pos);
-      }
-      to[mine] = row;
+      to[mine] = at.live && pos >= 0 && pos < 0x7fffffff ? row_at(a.pages, at.seq, (int)pos, 0x7fffffff) : -1;
     }
     for (int j = kTokens == 1 ? tid : lane; j < pairs; j += kTokens == 1 ? 256 : 64) {
       const float2 t = turn_of(pos, a.inv_freq[j]);
