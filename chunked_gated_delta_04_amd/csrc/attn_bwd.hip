@@ -96,7 +96,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   f32x16 dq[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) zero16(dq[i]);
-  const float c = pk.scale * kLog2e, scale = pk.scale;
+  const float c = pk.scale * kLog2e, scale = pk.scale, scaled = scale * delta;
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
@@ -105,12 +105,12 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   // 64 keys from j0 in LDS, in two halves. The matrix instructions go in the order S0, dO V0^T, S1, dO V1^T, dq of
   // the first half, of the second, each with its LDS operand requested kAhead before; the vector unit
   // forms the weights and the scores' gradients of a half during the products that follow it.
-  auto part = [&](auto masked, const uint16_t* K, const uint16_t* V, int j0) {
-    constexpr bool kMask = decltype(masked)::value;
+  auto part = [&](const uint16_t* K, const uint16_t* V, int j0) {
     constexpr int kAhead = 3;
     f32x16 s[2], dp[2];
-    // positions relative to the lane's first key
-    const int first = j0 + 4 * hi, most = t - first, least = from - first, sunk = pk.sinks - first;
+    const int j1 = j0 + kT - 1;
+    bool mask = j1 > wlo;
+    if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
     const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
     uint4 op[kAhead], ds[4];
     auto read = [&](auto slot) {
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
         x = column8(K + (32 * (phase - 4) + 16 * (d / DB)) * D, c0 ^ (32 * (d % DB)), c1 ^ (32 * (d % DB)));
     };
     for_each<kAhead>(read);
-    for_each<6 * N>([&](auto slot) {
+    auto run = [&](auto slot) {
       constexpr int n = slot, phase = n / N, d = n % N;
       const uint4& x = op[n % kAhead];
       if constexpr (phase >= 4) dq[d % DB] = mfma32_of<T>(x, ds[2 * (phase - 4) + d / DB], dq[d % DB]);
@@ -135,12 +135,9 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
           constexpr int e = element;
           if constexpr (e * N / 16 == d) {
             if constexpr (phase % 2) {
-              constexpr int j = 32 * half + 8 * (e / 4) + e % 4;
-              const float w = exp2_fast(fmaf(s[half][e], c, -lse));
-              s[half][e] = !kMask || (j <= most && (j > least || j < sunk)) ? w : 0.f;
+              s[half][e] = exp2_fast(fmaf(s[half][e], c, -lse));
             } else {
-              const float x2 = s[half][e] * (dp[half][e] - delta) * scale;
-              dp[half][e] = !kMask || s[half][e] != 0.f ? x2 : 0.f;  // a masked key's dO V^T may be anything
+              dp[half][e] = s[half][e] * fmaf(dp[half][e], scale, -scaled);
             }
           }
         });
@@ -150,7 +147,21 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-    });
+    };
+    auto hide = [&](auto half) {
+      if (!mask) return;
+      // positions relative to the lane's first key
+      const int first = j0 + 4 * hi, most = t - first, least = from - first, sunk = pk.sinks - first;
+      for_each<16>([&](auto element) {
+        constexpr int e = element, j = 32 * half + 8 * (e / 4) + e % 4;
+        s[half][e] = j <= most && (j > least || j < sunk) ? s[half][e] : kMinusInf;
+      });
+    };
+    for_each<N>(run);
+    hide(std::integral_constant<int, 0>());
+    for_each<2 * N>([&](auto slot) { run(std::integral_constant<int, slot + N>()); });
+    hide(std::integral_constant<int, 1>());
+    for_each<3 * N>([&](auto slot) { run(std::integral_constant<int, slot + 3 * N>()); });
   };
   auto keep = [&] {
 #pragma unroll
@@ -164,12 +175,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     keep();
     bool some = i < kt.count && wlo <= whi && j0 <= whi;
     if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
-    if (some) {
-      bool mask = j1 > wlo;
-      if (pk.window) mask = mask || (j0 <= whi - pk.window && j1 >= pk.sinks);
-      if (mask) part(std::true_type(), k, v, j0);
-      else part(std::false_type(), k, v, j0);
-    }
+    if (some) part(k, v, j0);
     keep();
     __syncthreads();
   };
@@ -283,30 +289,33 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
   const float* lses = a.lse + (int64_t)kt.bos * pk.HQ + hk * G;
   const float* deltas = a.delta + (int64_t)kt.bos * pk.HQ + hk * G;
-  float lse = INFINITY, delta = 0.f;
+  const float c = pk.scale * kLog2e, scale = pk.scale;
+  float lse = INFINITY, delta = 0.f;  // of row tid: times log2(e) and the scale
+  const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
   auto load = [&](auto& qs, auto& gs, int r0) {
     // offsets from the step's first token: its rows are of at most kR + 1 tokens
-    const int first = divide(r0, pk.G);
+    const int first = __builtin_amdgcn_readfirstlane(divide(r0, pk.G)), before = r0 - first * G, rows = to - r0;
     const __amdgpu_buffer_rsrc_t rq =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(qbase) + first * a.q_stride, 0, 0x7ffffff0, kBufferWord3);
     const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<uint16_t*>(gbase) + (int64_t)first * pk.HQ * D, 0, 0x7ffffff0, kBufferWord3);
 #pragma unroll
     for (int i = 0; i < RTile::kPieces; ++i) {
-      const int r = r0 + RTile::row(i, tid), token = divide(r, pk.G), h = r - token * G;
+      const int r = before + RTile::row(i, tid), token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
       const int col = h * D + RTile::column(i, tid);
-      const bool ok = r < to;  // others are past the resource: zeros
-      RTile::request(qs, i, rq, ok ? ((token - first) * (int)a.q_stride + col) * 2 : -1, tid);
-      RTile::request(gs, i, rg, ok ? ((token - first) * pk.HQ * D + col) * 2 : -1, tid);
+      const bool ok = RTile::row(i, tid) < rows;  // others are past the resource: zeros
+      RTile::request(qs, i, rq, ok ? (__umul24(token, (int)a.q_stride) + col) * 2 : -1, tid);
+      RTile::request(gs, i, rg, ok ? (__umul24(token, pk.HQ * D) + col) * 2 : -1, tid);
     }
     if (tid < kR) {
-      const int r = r0 + tid, token = divide(r, pk.G), h = r - token * G;
+      const int r = before + tid, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
       lse = INFINITY;
       delta = 0.f;
-      if (r < to) {
-        lse = lses[(int64_t)token * pk.HQ + h] * kLog2e;
+      if (tid < rows) {
+        const int64_t at = (int64_t)(first + token) * pk.HQ + h;
+        lse = lses[at] * kLog2e;
         if (lse == kMinusInf) lse = INFINITY;
-        delta = deltas[(int64_t)token * pk.HQ + h];
+        delta = deltas[at] * scale;
       }
     }
   };
@@ -323,7 +332,6 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     zero16(dk[i]);
     zero16(dv[i]);
   }
-  const float c = pk.scale * kLog2e, scale = pk.scale;
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, col0 + vc), vb = at<D>(vr + 8, col0 + vc);
@@ -336,11 +344,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   // 32 rows at r0 with their q, dO and stats in LDS. The matrix instructions go in the order S, dO V^T, dv, dk, each
   // with its LDS operand requested kAhead before, and what the vector unit does in between: the weights
   // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.)
-  auto part = [&](auto masked, const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0) {
-    constexpr bool kMask = decltype(masked)::value;
+  auto part = [&](const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0) {
     constexpr int N = D / 16, M = 2 * DB, kSlots = 2 * N + 2 * M, kAhead = 3;
     f32x16 s, dp;
-    const int least = lo - r0 - 4 * hi, most = up - r0 - 4 * hi;  // relative to the lane's first row
     const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
     uint4 op[kAhead], p[2], ds[2];
     auto read = [&](auto slot) {
@@ -355,7 +361,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     };
     f32x4 stat;
     for_each<kAhead>(read);
-    for_each<kSlots>([&](auto slot) {
+    auto run = [&](auto slot) {
       constexpr int n = slot;
       const uint4& x = op[n % kAhead];
       if constexpr (n < N) {
@@ -375,14 +381,11 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         constexpr int e = element;
         if constexpr (n == N + e * N / 16) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(ls + 2 * e + 4 * hi);
-          const float w = exp2_fast(fmaf(s[e], c, -stat[e % 4]));
-          constexpr int row = 8 * (e / 4) + e % 4;
-          s[e] = !kMask || (row >= least && row < most) ? w : 0.f;
+          s[e] = exp2_fast(fmaf(s[e], c, -stat[e % 4]));
         }
         if constexpr (n == 2 * N + e * M / 16) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(de + 2 * e + 4 * hi);
-          const float g = s[e] * (dp[e] - stat[e % 4]) * scale;
-          dp[e] = !kMask || s[e] != 0.f ? g : 0.f;  // a masked row's dO V^T may be anything
+          dp[e] = s[e] * fmaf(dp[e], scale, -stat[e % 4]);
         }
       });
       if constexpr (n == 2 * N - 1) {
@@ -394,7 +397,16 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         ds[1] = operand<T>(dp, 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-    });
+    };
+    for_each<N>(run);
+    if (r0 < all_from || r0 + 32 > all_to) {
+      const int least = lo - r0 - 4 * hi, most = up - r0 - 4 * hi;  // relative to the lane's first row
+      for_each<16>([&](auto element) {
+        constexpr int e = element, row = 8 * (e / 4) + e % 4;
+        s[e] = row >= least && row < most ? s[e] : kMinusInf;
+      });
+    }
+    for_each<kSlots - N>([&](auto slot) { run(std::integral_constant<int, slot + N>()); });
   };
 
   auto keep = [&] {
@@ -414,8 +426,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
       keep();
       if (r + 32 > any_from && r < any_to && r < to && wlo < kt.len) {
         const float *ls = stats[buf][0] + i, *de = stats[buf][1] + i;
-        if (r < all_from || r + 32 > all_to) part(std::true_type(), q + i * D, g + i * D, ls, de, r);
-        else part(std::false_type(), q + i * D, g + i * D, ls, de, r);
+        part(q + i * D, g + i * D, ls, de, r);
       }
       keep();
     }

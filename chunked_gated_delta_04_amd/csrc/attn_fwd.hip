@@ -120,11 +120,11 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
 
   // One step: the weights p of a tile from its scores s, while the matrix unit forms the next tile's scores `next` from K
-  // and adds the tile before's weights times V, `before`, to O. A slot has one matrix instruction of each and a share of
-  // the vector unit's work; the LDS operands are requested kAhead slots before.
+  // and adds the tile before's weights times V, `before`, to O. A slot has one matrix instruction, of these in turn, and a
+  // share of the vector unit's work; the LDS operands are requested kAhead instructions of their kind before.
   auto step = [&](f32x16(&s)[2], f32x16(&next)[2], uint4(&p)[4], const uint4(&before)[4], const uint16_t* K,
                   const uint16_t* V, int j0, uint64_t seen) {
-    constexpr int kSlots = 2 * N, kTop = kSlots / 4, kAhead = 2;
+    constexpr int kSlots = 4 * N, kTop = kSlots / 4, kAhead = 3;
     bool mask = j0 + kT - 1 > wlo;
     if (pk.window) mask = mask || (j0 <= whi - pk.window && j0 + kT > pk.sinks);
     if constexpr (kPaged) mask = mask || ~seen != 0;
@@ -142,17 +142,19 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
     const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
     uint4 ko[kAhead], vo[kAhead];
     auto read = [&](auto slot) {
-      constexpr int n = slot;
-      ko[n % kAhead] = *reinterpret_cast<const uint4*>(K + (kf ^ (16 * (n / 2))) + 32 * (n % 2) * D);
-      vo[n % kAhead] = column8(V + 16 * (n / DB) * D, c0 ^ (32 * (n % DB)), c1 ^ (32 * (n % DB)));
+      constexpr int n = slot / 2;
+      if constexpr (slot % 2 == 0)
+        ko[n % kAhead] = *reinterpret_cast<const uint4*>(K + (kf ^ (16 * (n / 2))) + 32 * (n % 2) * D);
+      else
+        vo[n % kAhead] = column8(V + 16 * (n / DB) * D, c0 ^ (32 * (n % DB)), c1 ^ (32 * (n % DB)));
     };
-    for_each<kAhead>(read);
+    for_each<2 * kAhead>(read);
     float top = kMinusInf, base = 0.f, f = 1.f, sum[2] = {0.f, 0.f};
     for_each<kSlots>([&](auto slot) {
-      constexpr int n = slot;
-      next[n % 2] = mfma32_of<T>(ko[n % kAhead], q[n / 2], n < 2 ? f32x16{} : next[n % 2]);
-      o[n % DB] = mfma32_of<T>(vo[n % kAhead], before[n / DB], o[n % DB]);
-      if constexpr (n + kAhead < kSlots) read(std::integral_constant<int, n + kAhead>());
+      constexpr int n = slot, i = n / 2;
+      if constexpr (n % 2 == 0) next[i % 2] = mfma32_of<T>(ko[i % kAhead], q[i / 2], i < 2 ? f32x16{} : next[i % 2]);
+      else o[i % DB] = mfma32_of<T>(vo[i % kAhead], before[i / DB], o[i % DB]);
+      if constexpr (n + 2 * kAhead < kSlots) read(std::integral_constant<int, n + 2 * kAhead>());
       for_each<32>([&](auto element) {
         constexpr int e = element;
         if constexpr (e * kTop / 32 == n) top = fmaxf(top, s[e / 16][e % 16]);
@@ -176,6 +178,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
           if constexpr (e % 8 == 7) {
             p[e / 8] = operand<T>(s[e / 16], e / 8 % 2);
             stay_here(p[e / 8]);
+            stay_here(sum[0], sum[1]);
           }
         }
       });

@@ -177,6 +177,7 @@ __device__ __forceinline__ uint4 operand(const f32x16& x, int h) {
 // Values whose place among the matrix instructions the compiler keeps: it moves what no instruction of a
 // block needs to the blocks behind it.
 __device__ __forceinline__ void stay_here(uint4& x) { asm volatile("" : "+v"(x.x), "+v"(x.y), "+v"(x.z), "+v"(x.w)); }
+__device__ __forceinline__ void stay_here(float& x, float& y) { asm volatile("" : "+v"(x), "+v"(y)); }
 __device__ __forceinline__ void zero16(f32x16& x) {
 #pragma unroll
   for (int r = 0; r < 16; ++r) x[r] = 0.f;
