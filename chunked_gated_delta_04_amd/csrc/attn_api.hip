@@ -120,11 +120,12 @@ int splits_of(int64_t items, int64_t keys, int fill, int least) {
 }
 int fwd_splits(const gdn_attn_problem* p, const gdn_kv_cache* c) {
   const int64_t keys = c ? (int64_t)c->columns * c->page_size : p->T;
-  return splits_of(row_tiles(p) * p->HK, most_keys(p, keys, attn_rows(p->D) / group(p)), 2 * kCUs, 512);
+  return splits_of(row_tiles(p) * p->HK, most_keys(p, keys, attn_rows(p->D) / group(p)), kCUs, 512);
 }
 int64_t step_items(const gdn_attn_problem* p) { return (int64_t)p->N * p->HK * div_up(group(p), 16); }
 int step_splits(const gdn_attn_problem* p, const gdn_kv_cache* c) {
-  return splits_of(step_items(p), most_keys(p, (int64_t)c->columns * c->page_size, 1), 2 * kCUs, 256);
+  // a workgroup takes 128 keys at once; with 256 columns a CU holds one, else two
+  return splits_of(step_items(p), most_keys(p, (int64_t)c->columns * c->page_size, 1), (p->D == 256 ? 1 : 2) * kCUs, 128);
 }
 size_t part_bytes(const gdn_attn_problem* p, int splits) {
   return splits > 1 ? (size_t)splits * p->T * p->HQ * (p->D + 2) * sizeof(float) : 0;
@@ -171,7 +172,9 @@ struct GradCut {
 GradCut grad_cut(const gdn_attn_problem* p) {
   GradCut c{1, 0, 0, 0};
   const int64_t items = key_tiles(p) * p->HK;
-  const int64_t rows = most_keys(p, p->T, kAttnKeys) * group(p);  // of a tile, at most
+  // rows that see a tile of a sequence of four times the mean length
+  const int64_t mean = p->N > 0 ? div_up(p->T, p->N) : 0;
+  const int64_t rows = most_keys(p, std::min<int64_t>(4 * mean, p->T), kAttnKeys) * group(p);
   if (items > 0) c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({4 * kCUs / items, 8, rows / 512}));
   if (p->window && p->sinks && p->T > p->window) {
     c.far_tiles = (int)div_up(std::min<int64_t>(p->sinks, p->T), kAttnKeys);

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int hk = blockIdx.x % pk.HK;
   const int G = pk.G.by, per = attn_rows(D) / G;
-  const RowTile rt = find_tile(pk.cu, pk.N, pk.T, per, a.slots - 1 - blockIdx.x / pk.HK);
+  const RowTile rt = tile_of(pk.cu, pk.N, pk.T, per, a.slots, blockIdx.x / pk.HK, true, [](int) { return 0; });
   if (rt.tokens <= 0) return;
   const int t0 = rt.first;
   const KeyTiles kt = key_tiles<kT>(t0, t0 + rt.tokens - 1, rt.len, pk.window, pk.sinks);
@@ -87,10 +87,10 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k) + rt.bos * a.k_stride + hk * D;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v) + rt.bos * a.v_stride + hk * D;
-  auto load = [&](auto& k, auto& v, int i) {
-    const int j0 = kt.at(i) * kT, len = min(kT, rt.len - j0);
-    KTile::load(k, kbase + j0 * a.k_stride, (int)a.k_stride, len, tid);
-    KTile::load(v, vbase + j0 * a.v_stride, (int)a.v_stride, len, tid);
+  const TokenRows<KTile> kr((int)a.k_stride, tid), vr((int)a.v_stride, tid);
+  auto tokens = [&](const uint16_t* base, int64_t stride, int i) {
+    const int j0 = kt.at(i) * kT;
+    return TokenRows<KTile>::from(base + j0 * stride, (int)stride, i < kt.count ? min(kT, rt.len - j0) : 0, D);
   };
 
   f32x16 dq[DB];
@@ -98,14 +98,14 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   for (int i = 0; i < DB; ++i) zero16(dq[i]);
   const float c = pk.scale * kLog2e, scale = pk.scale, scaled = scale * delta;
   const int ka = at<D>(l32, 8 * hi);
-  const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
-  const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  const int j16 = lane & 15, vrow = 4 * hi + (j16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
+  const int va = at<D>(vrow, vcol), vb = at<D>(vrow + 8, vcol);
   const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
 
   // 64 keys from j0 in LDS, in two halves. The matrix instructions go in the order S0, dO V0^T, S1, dO V1^T, dq of
   // the first half, of the second, each with its LDS operand requested kAhead before; the vector unit
   // forms the weights and the scores' gradients of a half during the products that follow it.
-  auto part = [&](const uint16_t* K, const uint16_t* V, int j0) {
+  auto part = [&](const uint16_t* K, const uint16_t* V, int j0, const auto& fetch) {
     constexpr int kAhead = 3;
     f32x16 s[2], dp[2];
     const int j1 = j0 + kT - 1;
@@ -129,6 +129,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
       else if constexpr (phase % 2) dp[phase / 2] = mfma32_of<T>(x, g[d], d == 0 ? f32x16{} : dp[phase / 2]);
       else s[phase / 2] = mfma32_of<T>(x, q[d], d == 0 ? f32x16{} : s[phase / 2]);
       if constexpr (n + kAhead < 6 * N) read(std::integral_constant<int, n + kAhead>());
+      fetch(slot);
       if constexpr (phase >= 1 && phase <= 4) {
         constexpr int half = (phase - 1) / 2;
         for_each<16>([&](auto element) {
@@ -168,18 +169,29 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     for (int d = 0; d < DB; ++d) keep_accumulated<D == 256>(dq[d]);
   };
 
-  // one step: tile i in (k, v), the next one on its way to (nk, nv)
+  // one step: tile i in (k, v), the next one on its way to (nk, nv), a request every second slot
   auto step = [&](int i, auto& k, auto& v, auto& nk, auto& nv) {
     const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
-    if (i + 1 < kt.count) load(nk, nv, i + 1);
+    const auto krows = tokens(kbase, a.k_stride, i + 1), vrows = tokens(vbase, a.v_stride, i + 1);
+    constexpr int P = KTile::kPieces;
+    auto fetch = [&](auto slot) {
+      constexpr int n = slot, r = n / 2;
+      if constexpr (n % 2 == 0 && r < P) kr.request(nk, r, krows, tid);
+      if constexpr (n % 2 == 0 && r >= P && r < 2 * P) vr.request(nv, r - P, vrows, tid);
+    };
     keep();
     bool some = i < kt.count && wlo <= whi && j0 <= whi;
     if (pk.window) some = some && (j1 > wlo - pk.window || j0 < pk.sinks);
-    if (some) part(k, v, j0);
+    if (some) part(k, v, j0, fetch);
+    else for_each<4 * P>(fetch);
     keep();
     __syncthreads();
   };
-  if (kt.count > 0) load(k0, v0, 0);
+  const auto krows = tokens(kbase, a.k_stride, 0), vrows = tokens(vbase, a.v_stride, 0);
+  for_each<KTile::kPieces>([&](auto i) {
+    kr.request(k0, i, krows, tid);
+    vr.request(v0, i, vrows, tid);
+  });
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < kt.count; i += 2) {  // a step past the last tile does nothing
@@ -253,7 +265,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     b -= far_items;
     pieces = a.pieces;
     piece = b % pieces;
-    kt = find_tile(pk.cu, pk.N, pk.T, kAttnKeys, b / pieces);
+    kt = tile_of(pk.cu, pk.N, pk.T, kAttnKeys, a.key_slots, b / pieces, false, [](int) { return 0; });
   }
   if (kt.tokens <= 0) return;
   const RowRange all = rows_of(pk, kt.len, kt.first, far);
@@ -292,27 +304,36 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   const float c = pk.scale * kLog2e, scale = pk.scale;
   float lse = INFINITY, delta = 0.f;  // of row tid: times log2(e) and the scale
   const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
-  auto load = [&](auto& qs, auto& gs, int r0) {
-    // offsets from the step's first token: its rows are of at most kR + 1 tokens
-    const int first = __builtin_amdgcn_readfirstlane(divide(r0, pk.G)), before = r0 - first * G, rows = to - r0;
-    const __amdgpu_buffer_rsrc_t rq =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(qbase) + first * a.q_stride, 0, 0x7ffffff0, kBufferWord3);
-    const __amdgpu_buffer_rsrc_t rg = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(gbase) + (int64_t)first * pk.HQ * D, 0, 0x7ffffff0, kBufferWord3);
-#pragma unroll
-    for (int i = 0; i < RTile::kPieces; ++i) {
-      const int r = before + RTile::row(i, tid), token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
-      const int col = h * D + RTile::column(i, tid);
-      const bool ok = RTile::row(i, tid) < rows;  // others are past the resource: zeros
-      RTile::request(qs, i, rq, ok ? (__umul24(token, (int)a.q_stride) + col) * 2 : -1, tid);
-      RTile::request(gs, i, rg, ok ? (__umul24(token, pk.HQ * D) + col) * 2 : -1, tid);
-    }
+  // a step's rows from r0 on: offsets from its first token, its rows are of at most kR + 1 tokens
+  struct Rows {
+    __amdgpu_buffer_rsrc_t q, g;
+    int first, before, count;
+  };
+  auto rows_from = [&](int r0) {
+    Rows r;
+    r.first = __builtin_amdgcn_readfirstlane(divide(r0, pk.G));
+    r.before = r0 - r.first * G;
+    r.count = to - r0;
+    r.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(qbase) + r.first * a.q_stride, 0, 0x7ffffff0, kBufferWord3);
+    r.g = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(gbase) + (int64_t)r.first * pk.HQ * D, 0, 0x7ffffff0,
+                                            kBufferWord3);
+    return r;
+  };
+  auto request = [&](auto piece, auto& qs, auto& gs, const Rows& rows) {
+    constexpr int i = piece;
+    const int row = RTile::row(i, fresh(tid)), r = rows.before + row;
+    const int token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G), col = h * D + RTile::column(i, tid);
+    const bool ok = row < rows.count;  // others are past the resource: zeros
+    RTile::request(qs, i, rows.q, ok ? (__umul24(token, (int)a.q_stride) + col) * 2 : -1, tid);
+    RTile::request(gs, i, rows.g, ok ? (__umul24(token, pk.HQ * D) + col) * 2 : -1, tid);
+  };
+  auto load_stats = [&](const Rows& rows) {
     if (tid < kR) {
-      const int r = before + tid, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
+      const int r = rows.before + tid, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
       lse = INFINITY;
       delta = 0.f;
-      if (tid < rows) {
-        const int64_t at = (int64_t)(first + token) * pk.HQ + h;
+      if (tid < rows.count) {
+        const int64_t at = (int64_t)(rows.first + token) * pk.HQ + h;
         lse = lses[at] * kLog2e;
         if (lse == kMinusInf) lse = INFINITY;
         delta = deltas[at] * scale;
@@ -344,7 +365,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   // 32 rows at r0 with their q, dO and stats in LDS. The matrix instructions go in the order S, dO V^T, dv, dk, each
   // with its LDS operand requested kAhead before, and what the vector unit does in between: the weights
   // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.)
-  auto part = [&](const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0) {
+  auto part = [&](const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0, const auto& fetch) {
     constexpr int N = D / 16, M = 2 * DB, kSlots = 2 * N + 2 * M, kAhead = 3;
     f32x16 s, dp;
     const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
@@ -376,6 +397,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         dk[d % DB] = mfma32_of<T>(x, ds[d / DB], dk[d % DB]);
       }
       if constexpr (n + kAhead < kSlots) read(std::integral_constant<int, n + kAhead>());
+      fetch(slot);
       // the weights of 16 rows, then their gradients
       for_each<16>([&](auto element) {
         constexpr int e = element;
@@ -417,26 +439,32 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     }
   };
 
-  // one step: rows from r0 in (q, g), the next ones on their way to (nq, ng)
+  // one step: rows from r0 in (q, g), the next ones on their way to (nq, ng), a request every fourth slot
   auto step = [&](int r0, int buf, auto& q, auto& g, auto& nq, auto& ng) {
-    if (r0 + kR < to) load(nq, ng, r0 + kR);
-#pragma unroll 1
-    for (int i = 0; i < kR; i += 32) {
-      const int r = r0 + i;
+    const Rows next = rows_from(r0 + kR);
+    load_stats(next);
+    for_each<kR / 32>([&](auto half) {
+      constexpr int kParts = kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
+      const int i = half * 32, r = r0 + i;
+      auto fetch = [&](auto slot) {
+        constexpr int n = slot, piece = half * kEach + n / 4;
+        if constexpr (n % 4 == 0 && n / 4 < kEach && piece < RTile::kPieces)
+          request(std::integral_constant<int, piece>(), nq, ng, next);
+      };
       keep();
-      if (r + 32 > any_from && r < any_to && r < to && wlo < kt.len) {
-        const float *ls = stats[buf][0] + i, *de = stats[buf][1] + i;
-        part(q + i * D, g + i * D, ls, de, r);
-      }
+      if (r + 32 > any_from && r < any_to && r < to && wlo < kt.len)
+        part(q + i * D, g + i * D, stats[buf][0] + i, stats[buf][1] + i, r, fetch);
+      else
+        for_each<4 * kEach>(fetch);
       keep();
-    }
-    if (r0 + kR < to) store_stats(buf ^ 1);
+    });
+    store_stats(buf ^ 1);
     __syncthreads();
   };
-  if (from < to) {
-    load(q0, g0, from);
-    store_stats(0);
-  }
+  const Rows rows = rows_from(from);
+  for_each<RTile::kPieces>([&](auto i) { request(i, q0, g0, rows); });
+  load_stats(rows);
+  store_stats(0);
   __syncthreads();
 #pragma unroll 1
   for (int r0 = from; r0 < to; r0 += 2 * kR) {  // a step past the last row does nothing
@@ -494,8 +522,22 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a) {
   for (int i = threadIdx.x; i < keys * unit; i += 256) {
     const int j = kt.first + some + i / unit, at = i % unit * 4, hk = at / (2 * D), col = at % (2 * D);
     f32x4 x = zero4();
-    for (int n = 0; n < from_part; ++n) x += *reinterpret_cast<const f32x4*>(part_at(a, n, kt, j, hk, D) + col);
-    for (int n = 0; n < from_far; ++n) x += *reinterpret_cast<const f32x4*>(far_at(a, n, kt, j, hk, D) + col);
+    // eight requests at once
+    const auto add = [&](int parts, const float* p, int64_t pitch) {
+#pragma unroll 1
+      for (int n = 0; n < parts; n += 8) {
+        f32x4 y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = zero4();
+          if (n + e < parts) y[e] = *reinterpret_cast<const f32x4*>(p + (n + e) * pitch);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x += y[e];
+      }
+    };
+    add(from_part, part_at(a, 0, kt, j, hk, D) + col, (int64_t)pk.T * pk.HK * 2 * D);
+    add(from_far, far_at(a, 0, kt, j, hk, D) + col, far_rows(a) * pk.HK * 2 * D);
     uint16_t* to = static_cast<uint16_t*>(col < D ? a.dk : a.dv) + ((int64_t)(kt.bos + j) * pk.HK + hk) * D + col % D;
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
   }

@@ -34,19 +34,19 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
-  // the last rows of a sequence, which see the most keys, first
   int b = blockIdx.x;
   const int hk = b % pk.HK;
   b /= pk.HK;
   const int split = b % a.splits;
   const int G = pk.G.by, per = attn_rows(D) / G;
-  const RowTile rt = find_tile(pk.cu, pk.N, pk.T, per, a.slots - 1 - b / a.splits);
+  const RowTile rt = tile_of(pk.cu, pk.N, pk.T, per, a.slots, b / a.splits, true,
+                             [&](int n) { return kPaged ? past_of(a.pages, n, pk.T) : 0; });
   if (rt.tokens <= 0) return;
 
   int past = 0;
   int64_t keys = rt.len;
   if constexpr (kPaged) {
-    past = past_of(a.pages, rt.seq, pk.T);
+    past = __builtin_amdgcn_readfirstlane(past_of(a.pages, rt.seq, pk.T));
     keys = min((int64_t)past + rt.len, (int64_t)a.pages.columns * a.pages.page.by);
   }
   const int t0 = past + rt.first;  // position of the tile's first token
@@ -100,13 +100,12 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   auto look = [&](int i) -> int64_t {
     return kPaged && i < part.y ? row_at(a.pages, rt.seq, kt.at(i) * kT + lane, keys) : -1;
   };
-  auto load = [&](auto& to, const uint16_t* base, int64_t stride, int i, int64_t at) {
-    if constexpr (kPaged) {
-      KTile::gather(to, base, at, tid);
-    } else {
-      const int j0 = kt.at(i) * kT;
-      KTile::load(to, base + j0 * stride, (int)stride, min(kT, rt.len - j0), tid);
-    }
+  const TokenRows<KTile> kr((int)a.k_stride, tid), vr((int)a.v_stride, tid);
+  int64_t off = -1;  // paged: where this lane's piece of the next request is
+  // resource of tile i's token rows; past the last tile empty, or rows that nobody reads
+  auto tokens = [&](const uint16_t* base, int64_t stride, int i) {
+    const int j0 = kt.at(i) * kT;
+    return TokenRows<KTile>::from(base + j0 * stride, (int)stride, min(kT, rt.len - j0), D);
   };
 
   f32x16 o[DB];
@@ -115,15 +114,16 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   float m = kMinusInf, l = 0.f;
   const float c = pk.scale * kLog2e;
   const int ka = at<D>(l32, 8 * hi);
-  const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
-  const int va = at<D>(vr, vc), vb = at<D>(vr + 8, vc);
+  const int j16 = lane & 15, vrow = 4 * hi + (j16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
+  const int va = at<D>(vrow, vcol), vb = at<D>(vrow + 8, vcol);
   const int from = pk.window ? t - pk.window : -1;  // keys in the window are past this
 
   // One step: the weights p of a tile from its scores s, while the matrix unit forms the next tile's scores `next` from K
   // and adds the tile before's weights times V, `before`, to O. A slot has one matrix instruction, of these in turn, and a
-  // share of the vector unit's work; the LDS operands are requested kAhead instructions of their kind before.
+  // share of the vector unit's work and of the requests for the tiles to come (`fetch`: issued together they held the
+  // matrix unit up); the LDS operands are requested kAhead instructions of their kind before.
   auto step = [&](f32x16(&s)[2], f32x16(&next)[2], uint4(&p)[4], const uint4(&before)[4], const uint16_t* K,
-                  const uint16_t* V, int j0, uint64_t seen) {
+                  const uint16_t* V, int j0, uint64_t seen, const auto& fetch) {
     constexpr int kSlots = 4 * N, kTop = kSlots / 4, kAhead = 3;
     bool mask = j0 + kT - 1 > wlo;
     if (pk.window) mask = mask || (j0 <= whi - pk.window && j0 + kT > pk.sinks);
@@ -155,6 +155,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
       if constexpr (n % 2 == 0) next[i % 2] = mfma32_of<T>(ko[i % kAhead], q[i / 2], i < 2 ? f32x16{} : next[i % 2]);
       else o[i % DB] = mfma32_of<T>(vo[i % kAhead], before[i / DB], o[i % DB]);
       if constexpr (n + 2 * kAhead < kSlots) read(std::integral_constant<int, n + 2 * kAhead>());
+      fetch(slot);
       for_each<32>([&](auto element) {
         constexpr int e = element;
         if constexpr (e * kTop / 32 == n) top = fmaxf(top, s[e / 16][e % 16]);
@@ -202,8 +203,16 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   for (int i = 0; i < 4; ++i) p1[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int n = 0; n < 3; ++n) rows[n] = look(part.x + n);
-  load(k0, kbase, a.k_stride, part.x, rows[0]);
-  if (part.x + 1 < part.y) load(k1, kbase, a.k_stride, part.x + 1, rows[1]);
+  const auto first = tokens(kbase, a.k_stride, part.x), second = tokens(kbase, a.k_stride, part.x + 1);
+  for_each<KTile::kPieces>([&](auto i) {
+    if constexpr (kPaged) {
+      KTile::request_page(k0, i, kbase, KTile::place(rows[0], i, tid), tid);
+      KTile::request_page(k1, i, kbase, KTile::place(rows[1], i, tid), tid);
+    } else {
+      kr.request(k0, i, first, tid);
+      kr.request(k1, i, second, tid);
+    }
+  });
   for (int i = tid; i < kT * D / 8; i += kThreads) reinterpret_cast<uint4*>(v1)[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
 #pragma unroll
@@ -218,14 +227,28 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
                   uint4(&p)[4], const uint4(&before)[4]) {
     uint64_t seen = ~0ull;
     if constexpr (kPaged) seen = __ballot(rows[0] >= 0);
-    if (i + 2 < part.y) load(nk, kbase, a.k_stride, i + 2, rows[2]);
-    if (i < part.y) load(nv, vbase, a.v_stride, i, rows[0]);
-    rows[0] = rows[1];
-    rows[1] = rows[2];
-    rows[2] = look(i + 3);
+    const auto krows = tokens(kbase, a.k_stride, i + 2), vrows = tokens(vbase, a.v_stride, i);
+    const int64_t kat = rows[2], vat = rows[0];
+    // request r in slot 2 r (of V after those of K), a page's offset two slots before it
+    auto fetch = [&](auto slot) {
+      constexpr int n = slot, P = KTile::kPieces, r = n / 2;
+      if constexpr (kPaged) {
+        if constexpr (n % 2 == 0 && n > 0 && r <= P) KTile::request_page(nk, r - 1, kbase, off, tid);
+        if constexpr (n % 2 == 0 && r > P && r <= 2 * P) KTile::request_page(nv, r - 1 - P, vbase, off, tid);
+        if constexpr (n % 2 == 0 && r < 2 * P) off = KTile::place(r < P ? kat : vat, r % P, tid);
+        if constexpr (n == 4 * P + 2) {
+          rows[0] = rows[1];
+          rows[1] = rows[2];
+          rows[2] = look(i + 3);
+        }
+      } else {
+        if constexpr (n % 2 == 0 && r < P) kr.request(nk, r, krows, tid);
+        if constexpr (n % 2 == 0 && r >= P && r < 2 * P) vr.request(nv, r - P, vrows, tid);
+      }
+    };
     keep();
     // past the last tile no row sees anything
-    step(s, next, p, before, K, V, i < part.y ? kt.at(i) * kT : whi + 64, seen);
+    step(s, next, p, before, K, V, i < part.y ? kt.at(i) * kT : whi + 64, seen, fetch);
     keep();
     __syncthreads();
   };
@@ -265,44 +288,63 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   }
 }
 
-// o and lse of a row from its parts: sums of weights relative to their own maxima. A workgroup takes
-// a row, its threads D / 4 columns each and a share of the parts.
-template <typename T, int D>
-__global__ __launch_bounds__(512) void attn_join_kernel(AttnArgs a) {
-  constexpr int kColumns = D / 4;
-  __shared__ float sums[512 * 4];
-  __shared__ float ls[512 / kColumns];
+// o and lse of a row from its parts: sums of weights relative to their own maxima. 16 lanes take 64
+// columns of a row, kShares such groups a share of the parts each, of which a lane requests eight at once.
+template <typename T, int D, int kShares>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  constexpr int kBlocks = D / 64, kUnits = 16 / kShares;  // columns blocks of a row; units of a workgroup
   const AttnPack& pk = a.pack;
-  const int64_t row = blockIdx.x, rows = (int64_t)pk.T * pk.HQ;
-  if (pk.cu && row / pk.HQ >= pk.cu[pk.N]) return;  // behind the last sequence
+  const int64_t rows = (int64_t)pk.T * pk.HQ;
+  const int group = threadIdx.x >> 4, lane = threadIdx.x & 15, share = group % kShares;
+  const int64_t unit = (int64_t)blockIdx.x * kUnits + group / kShares, row = unit / kBlocks;
+  // behind the last sequence, or the last unit: nothing is written
+  const bool live = row < (pk.cu ? min((int64_t)min(max(pk.cu[pk.N], 0), pk.T) * pk.HQ, rows) : rows);
+  const int col = (int)(unit % kBlocks) * 64 + lane * 4;
   const float2* ml = reinterpret_cast<const float2*>(a.part + rows * a.splits * D) + row;
-  const int share = threadIdx.x / kColumns, shares = blockDim.x / kColumns, col = threadIdx.x % kColumns * 4;
-  float m = kMinusInf;
-  for (int s = threadIdx.x & 63; s < a.splits; s += 64) m = fmaxf(m, ml[s * rows].x);
-  for (int x = 1; x < 64; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-  const float base = m == kMinusInf ? 0.f : m;
-  float l = 0.f;
+  float m = kMinusInf, l = 0.f, base = 0.f;
   f32x4 o = zero4();
-#pragma unroll 4
-  for (int s = share; s < a.splits; s += shares) {
-    const float2 x = ml[s * rows];
-    const float w = exp2_fast(x.x - base);
-    if (x.x != kMinusInf || x.y != 0.f) {
-      const f32x4 y = *reinterpret_cast<const f32x4*>(a.part + (row + s * rows) * D + col);
-      o += y * w;
-      l += x.y * w;
+  if (live) {
+    for (int s = lane; s < a.splits; s += 16) m = fmaxf(m, ml[s * rows].x);
+    for (int x = 1; x < 16; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+    base = m == kMinusInf ? 0.f : m;
+#pragma unroll 1
+    for (int s0 = share; s0 < a.splits; s0 += 8 * kShares) {
+      float2 x[8];
+      f32x4 y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = s0 + i * kShares;
+        x[i] = make_float2(kMinusInf, 0.f);
+        if (s < a.splits) x[i] = ml[s * rows];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = zero4();  // a part without weight holds no sums
+        if (x[i].x != kMinusInf || x[i].y != 0.f)
+          y[i] = *reinterpret_cast<const f32x4*>(a.part + (row + (s0 + i * kShares) * rows) * D + col);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = exp2_fast(x[i].x - base);
+        l = fmaf(x[i].y, w, l);
+        o += y[i] * w;
+      }
     }
   }
-  if (shares > 1) {
-    *reinterpret_cast<f32x4*>(sums + 4 * threadIdx.x) = o;
-    if (col == 0) ls[share] = l;
+  if constexpr (kShares > 1) {
+    __shared__ float sums[16][16][5];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[group][lane][i] = o[i];
+    sums[group][lane][4] = l;
     __syncthreads();
     if (share > 0) return;
-    for (int i = 1; i < shares; ++i) {
-      o += *reinterpret_cast<const f32x4*>(sums + 4 * (threadIdx.x + i * kColumns));
-      l += ls[i];
+    for (int i = 1; i < kShares; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[c] += sums[group + i][lane][c];
+      l += sums[group + i][lane][4];
     }
   }
+  if (!live) return;
   const float f = l > 0.f || l != l ? 1.f / l : 0.f;
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + row * D + col) =
       make_uint2(pack2<T>(o[0] * f, o[1] * f), pack2<T>(o[2] * f, o[3] * f));
@@ -323,18 +365,20 @@ hipError_t fwd_of(int D, bool paged, const AttnArgs& a, hipStream_t s) {
 #undef GDN_FWD
   return hipGetLastError();
 }
-template <typename T>
-hipError_t join_of(int D, const AttnArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)((int64_t)a.pack.T * a.pack.HQ));
-  // as many threads as parts read at once, eight of them each
-  const int columns = D / 4;
-  int shares = std::max(64 / columns, 1);
-  while (shares * columns < 512 && shares * 4 < a.splits) shares *= 2;
-  const dim3 block(shares * columns);
-  if (D == 64) hipLaunchKernelGGL((attn_join_kernel<T, 64>), grid, block, 0, s, a);
-  else if (D == 128) hipLaunchKernelGGL((attn_join_kernel<T, 128>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((attn_join_kernel<T, 256>), grid, block, 0, s, a);
+template <typename T, int D>
+hipError_t join_of(const AttnArgs& a, hipStream_t s) {
+  const int64_t units = (int64_t)a.pack.T * a.pack.HQ * (D / 64);
+  const dim3 block(256);
+  // a lane's eight requests hold every part where the rows alone fill no chip
+  if (a.splits > 16 && units < 4096)
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 16>), dim3((uint32_t)units), block, 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 1>), dim3((uint32_t)((units + 15) / 16)), block, 0, s, a);
   return hipGetLastError();
+}
+template <typename T>
+hipError_t join_type(int D, const AttnArgs& a, hipStream_t s) {
+  return D == 64 ? join_of<T, 64>(a, s) : D == 128 ? join_of<T, 128>(a, s) : join_of<T, 256>(a, s);
 }
 
 }  // namespace
@@ -343,7 +387,7 @@ hipError_t launch_attn_fwd(Elem type, int D, bool paged, const AttnArgs& a, hipS
   return type == Elem::kBf16 ? fwd_of<Bf16>(D, paged, a, s) : fwd_of<Fp16>(D, paged, a, s);
 }
 hipError_t launch_attn_join(Elem type, int D, const AttnArgs& a, hipStream_t s) {
-  return type == Elem::kBf16 ? join_of<Bf16>(D, a, s) : join_of<Fp16>(D, a, s);
+  return type == Elem::kBf16 ? join_type<Bf16>(D, a, s) : join_type<Fp16>(D, a, s);
 }
 
 }  // namespace gdn

@@ -18,25 +18,29 @@ namespace {
 
 constexpr int kStepKeys = 32;
 
-// kT rows of D elements of a cache on their way through a wave's registers into its LDS, 16 bytes a piece.
+// kT rows of keys and values of a cache on their way through a wave's registers into its LDS, 16 bytes a piece.
 template <int D, int kT>
 struct Staged {
   static constexpr int kPieces = kT * D / 8 / 64, kRows = 64 / (D / 8);  // rows a piece of all lanes
-  uint4 x[kPieces];
+  uint4 k[kPieces], v[kPieces];
   static __device__ __forceinline__ int row(int i, int lane) { return lane / (D / 8) + i * kRows; }
   static __device__ __forceinline__ int column(int lane) { return lane % (D / 8) * 8; }
   // lane r has the offset of row r, or -1 for zeros
-  __device__ __forceinline__ void gather(const uint16_t* p, int64_t rows, int lane) {
+  __device__ __forceinline__ void gather(const uint16_t* pk, const uint16_t* pv, int64_t rows, int lane) {
+    int64_t off[kPieces];  // all exchanged before the first is waited for
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) off[i] = from_lane(rows, row(i, lane));
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int64_t off = from_lane(rows, row(i, lane));
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (off >= 0) x[i] = *reinterpret_cast<const uint4*>(p + off + column(lane));
+      k[i] = load16(off[i] >= 0 ? (Global*)(pk + off[i] + column(lane)) : (Global*)zeros);
+      v[i] = load16(off[i] >= 0 ? (Global*)(pv + off[i] + column(lane)) : (Global*)zeros);
     }
   }
-  __device__ __forceinline__ void store(uint16_t* tile, int lane) const {
+  __device__ __forceinline__ void store(uint16_t* K, uint16_t* V, int lane) const {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(tile + at<D>(row(i, lane), column(lane))) = x[i];
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(K + at<D>(row(i, lane), column(lane))) = k[i];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(V + at<D>(row(i, lane), column(lane))) = v[i];
   }
 };
 
@@ -56,10 +60,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   b /= row_tiles;
   const int split = b % a.splits, seq = b / a.splits;
 
-  const int t = past_of(a.pages, seq, 1);
+  const int t = __builtin_amdgcn_readfirstlane(past_of(a.pages, seq, 1));
   const int64_t keys = min((int64_t)t + 1, (int64_t)a.pages.columns * a.pages.page.by);
   const KeyTiles kt = key_tiles<kT>(t, t, keys, pk.window, pk.sinks);
-  const int2 part = split_of(kt.count, a.splits, split, 8);
+  const int2 part = split_of(kt.count, a.splits, split, 4);
   const int from = pk.window ? t - pk.window : -1;
 
   const bool live = g0 + i16 < G;
@@ -77,7 +81,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   const uint16_t* vbase = static_cast<const uint16_t*>(a.pages.v) + hk * a.pages.head_stride;
   uint16_t *K = lds + wave * 2 * kT * D, *V = K + kT * D;
 
-  Staged<D, kT> ks, vs;
+  Staged<D, kT> staged;
   int64_t at_next = -1;   // where row lane % 32 of the tile after the next is, -1 where it is not seen
   uint32_t seen_next = 0; // the rows of the next tile that are seen
   auto look = [&](int i) {
@@ -89,8 +93,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   };
   auto load = [&](int i) {
     seen_next = (uint32_t)__ballot(at_next >= 0);
-    ks.gather(kbase, at_next, lane);
-    vs.gather(vbase, at_next, lane);
+    staged.gather(kbase, vbase, at_next, lane);
     look(i + 4);
   };
 
@@ -107,8 +110,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   if (i < part.y) load(i);
   for (; i < part.y; i += 4) {
     const uint32_t seen = seen_next;
-    ks.store(K, lane);
-    vs.store(V, lane);
+    staged.store(K, V, lane);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();  // a wave's LDS requests are done in order
     if (i + 4 < part.y) load(i + 4);

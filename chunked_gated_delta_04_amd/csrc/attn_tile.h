@@ -2,6 +2,8 @@
 // and a tile's way from memory into LDS.
 #pragma once
 
+#include <limits.h>
+
 #include <utility>
 
 #include "attn.h"
@@ -53,6 +55,39 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* cu, int N, int T, in
   return t;
 }
 
+// The tile of number `item`, the one with the most work first: up to 64 sequences are taken in the order of their keys
+// (before(n): those that sequence n had before), a wave comparing all of them, and a sequence's tiles from the last on
+// (back) or from the first. More sequences are taken in the pack's order. (8 prompts of 512 tokens, four of them after 1000
+// to 2000: 160 us in the pack's order.)
+template <class Before>
+__device__ __forceinline__ RowTile tile_of(const int32_t* cu, int N, int T, int per, int slots, int item, bool back,
+                                           const Before& before) {
+  if (N > 64) return find_tile(cu, N, T, per, back ? slots - 1 - item : item);
+  const int lane = threadIdx.x & 63;
+  int bos = 0, len = 0, keys = INT_MIN;
+  if (lane < N) {
+    bos = min(max(cu[lane], 0), T);
+    len = min(max(cu[lane + 1], bos), T) - bos;
+    keys = len + before(lane);
+  }
+  const int tiles = (len + per - 1) / per;
+  int first = 0;  // tiles of the sequences before this lane's
+  for (int n = 0; n < N; ++n) {
+    const int k = __builtin_amdgcn_readlane(keys, n), t = __builtin_amdgcn_readlane(tiles, n);
+    if (k > keys || (k == keys && n < lane)) first += t;
+  }
+  const uint64_t mine = __ballot(lane < N && item >= first && item < first + tiles);
+  RowTile t{0, 0, 0, 0, 0};
+  if (mine == 0) return t;
+  t.seq = __builtin_ctzll(mine);
+  t.bos = __builtin_amdgcn_readlane(bos, t.seq);
+  t.len = __builtin_amdgcn_readlane(len, t.seq);
+  const int i = item - __builtin_amdgcn_readlane(first, t.seq);
+  t.first = (back ? __builtin_amdgcn_readlane(tiles, t.seq) - 1 - i : i) * per;
+  t.tokens = min(per, t.len - t.first);
+  return t;
+}
+
 // The key tiles that queries at positions lo .. hi (hi the last) may see, kT keys each, of `keys` keys:
 // those with sinks, then those from the first one in a window on. (lo and hi may be negative.)
 struct KeyTiles {
@@ -79,7 +114,7 @@ __device__ __forceinline__ int2 split_of(int count, int splits, int split, int l
 // Tokens that a sequence had before, so that the positions of T more, rounded up to a tile, are 32 bits
 // whatever the caller's array holds.
 __device__ __forceinline__ int past_of(const KvPages& c, int seq, int T) {
-  return __builtin_amdgcn_readfirstlane(min(max(c.offsets[seq], -(1 << 30)), 0x7fffff00 - T));
+  return min(max(c.offsets[seq], -(1 << 30)), 0x7fffff00 - T);
 }
 // Element offset of the row of position j of a sequence in the cache, or -1 where it has none.
 __device__ __forceinline__ int64_t row_at(const KvPages& c, int seq, int j, int64_t keys) {
@@ -89,7 +124,13 @@ __device__ __forceinline__ int64_t row_at(const KvPages& c, int seq, int j, int6
   const int id = c.table[seq * c.table_stride + col];
   return id > 0 && id < c.pages ? id * c.page_stride + (j - col * c.page.by) * c.token_stride : -1;
 }
+// what rows without a place are read from
 __device__ const uint4 zeros[1] = {};
+typedef __attribute__((address_space(1))) const void Global;
+__device__ __forceinline__ uint4 load16(Global* p) {
+  const u32x4 x = *(__attribute__((address_space(1))) const u32x4*)p;
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
 __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
   const int lo = __shfl((int)x, lane), hi = __shfl((int)(x >> 32), lane);
   return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
@@ -113,27 +154,37 @@ struct Tile {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     return (__attribute__((address_space(3))) void*)(tile + (i * (kThreads / 64) + wave) * 64 * 8);
   }
-  // rows [0, len) of token rows at p; the others are past the resource: zeros
-  static __device__ __forceinline__ void load(Lds& tile, const uint16_t* p, int stride, int len, int tid) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(p), 0, len > 0 ? ((len - 1) * stride + D) * 2 : 0, kBufferWord3);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) request(tile, i, r, (row(i, tid) * stride + column(i, tid)) * 2, tid);
-  }
   static __device__ __forceinline__ void request(Lds& tile, int i, __amdgpu_buffer_rsrc_t r, int byte_off, int tid) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to(tile, i, tid), 16, byte_off, 0, 0, 0);
   }
-  // rows of a cache's pages: lane r of each wave has the offset of row r, or -1 for zeros
-  static __device__ __forceinline__ void gather(Lds& tile, const uint16_t* p, int64_t rows, int tid) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int64_t off = from_lane(rows, row(i, tid) & 63);
-      const void* from = off >= 0 ? static_cast<const void*>(p + off + column(i, tid)) : zeros;
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)from, to(tile, i, tid), 16, 0, 0);
-    }
+  // Of a cache's rows at p: this lane's at an element offset, or -1 for zeros. `rows` in lane r of each wave is where row r of
+  // the tile is; a request's offset is exchanged (place) some time before it goes out.
+  static __device__ __forceinline__ int64_t place(int64_t rows, int i, int tid) { return from_lane(rows, row(i, tid) & 63); }
+  static __device__ __forceinline__ void request_page(Lds& tile, int i, const uint16_t* p, int64_t off, int tid) {
+    Global* from = off >= 0 ? (Global*)(p + off + column(i, tid)) : (Global*)zeros;
+    __builtin_amdgcn_global_load_lds(from, to(tile, i, tid), 16, 0, 0);
   }
 };
 
+// Requests for token rows at a stride: a lane's byte offsets of request 0 (and of request 1 less a step, where the
+// permutation differs), the others a step of kRows rows apart each.
+template <class Tile>
+struct TokenRows {
+  int lane[2], step;
+  __device__ __forceinline__ TokenRows(int stride, int tid) {
+    step = Tile::kRows * stride * 2;
+    lane[0] = (Tile::row(0, tid) * stride + Tile::column(0, tid)) * 2;
+    lane[1] = lane[0] + (Tile::column(1, tid) - Tile::column(0, tid)) * 2;
+  }
+  // rows [0, len) from p; the others are past the resource: zeros
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t from(const uint16_t* p, int stride, int len, int D) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p), 0, len > 0 ? ((len - 1) * stride + D) * 2 : 0,
+                                             kBufferWord3);
+  }
+  __device__ __forceinline__ void request(typename Tile::Lds& tile, int i, __amdgpu_buffer_rsrc_t r, int tid) const {
+    Tile::request(tile, i, r, fresh(lane[i % 2]) + i * step, tid);
+  }
+};
 // 16 bytes for each lane from the accumulator of 32 x 32: rows 8 b + 4 (lane / 32) + r are columns of
 // the output. Lanes 0-31 get the 8 columns of b = 2 u, lanes 32-63 those of b = 2 u + 1.
 template <typename T>

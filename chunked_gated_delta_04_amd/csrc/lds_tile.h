@@ -8,14 +8,14 @@ namespace gdn {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Rows of D 16-bit elements in LDS, 16-byte pieces of a row permuted by the row's number
-// (xor): the 16 rows of a row-wise operand read, and the 4 rows x 2 pieces that a
-// lane group's transposing read takes, then all lie in different banks (with rows
-// padded by 16 bytes instead, nearly half of the LDS cycles were conflicts). The
-// permutation has a period of 16 rows, so it is a constant of the lane.
+// (xor), for 64 banks of 4 bytes: the 16 rows that a cycle of a row-wise operand read takes,
+// one piece each, and the 4 rows x 4 pieces of half a wave's transposing read then all lie in
+// different banks (with the rows' numbers as they are, every transposing read took twice as long).
+// The permutation has a period of 16 rows, so it is a constant of the lane.
 template <int D>
 __device__ __forceinline__ int piece_of(int row) {
-  const int x = D >= 128 ? row & 15 : (row >> 1) & 7;
-  return ((x & 3) << 1) | ((x >> 2) & 1) | (x & 8);
+  if constexpr (D >= 128) return ((row & 3) << 2) | ((row >> 2) & 3);  // 16 pieces to the banks
+  else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);              // 8 pieces, two rows
 }
 // element offset of column c (a multiple of 4) of a row
 template <int D>
