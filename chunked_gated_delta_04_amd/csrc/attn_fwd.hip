@@ -25,11 +25,15 @@ namespace {
 
 constexpr int kFwdKeys = 64;  // keys a tile
 
+// where the keys are: token rows, pages whose rows come in groups of 8 (see request_group), other pages
+enum { kTokens, kGroups, kPages };
+
 }  // namespace
 
-template <typename T, int D, bool kPaged>
+template <typename T, int D, int kKeys>
 __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArgs a) {
   constexpr int kT = kFwdKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
+  constexpr bool kPaged = kKeys != kTokens;
   typedef Tile<D, kT, kThreads> KTile;
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
@@ -101,7 +105,15 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
     return kPaged && i < part.y ? row_at(a.pages, rt.seq, kt.at(i) * kT + lane, keys) : -1;
   };
   const TokenRows<KTile> kr((int)a.k_stride, tid), vr((int)a.v_stride, tid);
-  int64_t off = -1;  // paged: where this lane's piece of the next request is
+  int64_t off = -1;  // kPages: where this lane's piece of the next request is
+  const int pitch = (int)a.pages.token_stride;  // kGroups: of a page's rows, and this lane's places in a group
+  const int group[2] = {KTile::in_group(0, pitch, tid), KTile::in_group(1, pitch, tid)};
+  auto page_rows = [&](auto& to, auto i, const uint16_t* base, int64_t at, int tile) {
+    if constexpr (kKeys == kGroups)
+      KTile::request_group(to, i, base, at, (int)min(keys - (int64_t)kt.at(tile) * kT, (int64_t)kT), pitch, fresh(group[i % 2]), tid);
+    else
+      KTile::request_page(to, i, base, KTile::place(at, i, tid), tid);
+  };
   // resource of tile i's token rows; past the last tile empty, or rows that nobody reads
   auto tokens = [&](const uint16_t* base, int64_t stride, int i) {
     const int j0 = kt.at(i) * kT;
@@ -206,8 +218,8 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
   const auto first = tokens(kbase, a.k_stride, part.x), second = tokens(kbase, a.k_stride, part.x + 1);
   for_each<KTile::kPieces>([&](auto i) {
     if constexpr (kPaged) {
-      KTile::request_page(k0, i, kbase, KTile::place(rows[0], i, tid), tid);
-      KTile::request_page(k1, i, kbase, KTile::place(rows[1], i, tid), tid);
+      page_rows(k0, i, kbase, rows[0], part.x);
+      page_rows(k1, i, kbase, rows[1], part.x + 1);
     } else {
       kr.request(k0, i, first, tid);
       kr.request(k1, i, second, tid);
@@ -232,18 +244,21 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
     // request r in slot 2 r (of V after those of K), a page's offset two slots before it
     auto fetch = [&](auto slot) {
       constexpr int n = slot, P = KTile::kPieces, r = n / 2;
-      if constexpr (kPaged) {
+      if constexpr (kKeys == kGroups) {
+        if constexpr (n % 2 == 0 && r < P) page_rows(nk, std::integral_constant<int, r>(), kbase, kat, i + 2);
+        if constexpr (n % 2 == 0 && r >= P && r < 2 * P) page_rows(nv, std::integral_constant<int, r - P>(), vbase, vat, i);
+      } else if constexpr (kPaged) {
         if constexpr (n % 2 == 0 && n > 0 && r <= P) KTile::request_page(nk, r - 1, kbase, off, tid);
         if constexpr (n % 2 == 0 && r > P && r <= 2 * P) KTile::request_page(nv, r - 1 - P, vbase, off, tid);
         if constexpr (n % 2 == 0 && r < 2 * P) off = KTile::place(r < P ? kat : vat, r % P, tid);
-        if constexpr (n == 4 * P + 2) {
-          rows[0] = rows[1];
-          rows[1] = rows[2];
-          rows[2] = look(i + 3);
-        }
       } else {
         if constexpr (n % 2 == 0 && r < P) kr.request(nk, r, krows, tid);
         if constexpr (n % 2 == 0 && r >= P && r < 2 * P) vr.request(nv, r - P, vrows, tid);
+      }
+      if constexpr (kPaged && n == 4 * P + 2) {
+        rows[0] = rows[1];
+        rows[1] = rows[2];
+        rows[2] = look(i + 3);
       }
     };
     keep();
@@ -356,9 +371,10 @@ namespace {
 template <typename T>
 hipError_t fwd_of(int D, bool paged, const AttnArgs& a, hipStream_t s) {
   const dim3 grid(a.slots * a.pack.HK * a.splits), block(2 * attn_rows(D));
-#define GDN_FWD(d)                                                                                \
-  if (paged) hipLaunchKernelGGL((attn_fwd_kernel<T, d, true>), grid, block, 0, s, a);             \
-  else hipLaunchKernelGGL((attn_fwd_kernel<T, d, false>), grid, block, 0, s, a)
+#define GDN_FWD(d)                                                                                                 \
+  if (!paged) hipLaunchKernelGGL((attn_fwd_kernel<T, d, kTokens>), grid, block, 0, s, a);                          \
+  else if (in_groups(a.pages)) hipLaunchKernelGGL((attn_fwd_kernel<T, d, kGroups>), grid, block, 0, s, a);         \
+  else hipLaunchKernelGGL((attn_fwd_kernel<T, d, kPages>), grid, block, 0, s, a)
   if (D == 64) GDN_FWD(64);
   else if (D == 128) GDN_FWD(128);
   else GDN_FWD(256);

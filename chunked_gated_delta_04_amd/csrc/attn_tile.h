@@ -164,7 +164,25 @@ struct Tile {
     Global* from = off >= 0 ? (Global*)(p + off + column(i, tid)) : (Global*)zeros;
     __builtin_amdgcn_global_load_lds(from, to(tile, i, tid), 16, 0, 0);
   }
+  // The same where the rows of a wave's request, at most 8, are in one page and less than 2^24 elements apart: their place is
+  // uniform, and so costs no vector work. `lane` is this lane's byte offset in them, `keys` how many rows of the tile are there.
+  static constexpr int kGroup = 512 / D;
+  static __device__ __forceinline__ int in_group(int i, int stride, int tid) {
+    return ((tid & 63) / (D / 8) * stride + column(i, tid)) * 2;
+  }
+  static __device__ __forceinline__ void request_group(Lds& tile, int i, const uint16_t* p, int64_t rows, int keys, int stride,
+                                                       int lane, int tid) {
+    const int first = (i * (kThreads / 64) + __builtin_amdgcn_readfirstlane(tid >> 6)) * kGroup;
+    const int lo = __builtin_amdgcn_readlane((int)rows, first), hi = __builtin_amdgcn_readlane((int)(rows >> 32), first);
+    const int64_t off = (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+    const int n = off >= 0 ? min(keys - first, kGroup) : 0;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p) + (off >= 0 ? off : 0), 0,
+                                                                      n > 0 ? ((n - 1) * stride + D) * 2 : 0, kBufferWord3);
+    request(tile, i, r, lane, tid);
+  }
 };
+// whether request_group holds for a cache
+__host__ __device__ inline bool in_groups(const KvPages& c) { return c.page.by % 8 == 0 && c.token_stride < (1 << 24); }
 
 // Requests for token rows at a stride: a lane's byte offsets of request 0 (and of request 1 less a step, where the
 // permutation differs), the others a step of kRows rows apart each.
