@@ -182,11 +182,13 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
         f = exp2_fast(m - base);
         m = now;
       }
+      // a weight's argument, exponential and share of the sum in slots of their own: none waits for the one before
       for_each<32>([&](auto element) {
-        constexpr int e = element;
-        if constexpr (kTop + e * (kSlots - kTop) / 32 == n) {
-          const float x = exp2_fast(fmaf(s[e / 16][e % 16], c, -base));
-          s[e / 16][e % 16] = x;
+        constexpr int e = element, at = kTop + e * (kSlots - kTop - 2) / 32;
+        float x = s[e / 16][e % 16];
+        if constexpr (n == at) x = fmaf(x, c, -base);
+        if constexpr (n == at + 1) x = exp2_fast(x);
+        if constexpr (n == at + 2) {
           sum[e % 2] += x;
           if constexpr (e % 8 == 7) {
             p[e / 8] = operand<T>(s[e / 16], e / 8 % 2);
@@ -194,6 +196,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
             stay_here(sum[0], sum[1]);
           }
         }
+        s[e / 16][e % 16] = x;
       });
       __builtin_amdgcn_sched_barrier(0);
     });
