@@ -39,7 +39,7 @@ gdn_status check_bounds(int N, int T, const int32_t* cu) {
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int group(const gdn_attn_problem* p) { return p->HQ / p->HK; }
 int64_t row_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / (attn_rows(p->D) / group(p)) + p->N; }
-int64_t key_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / kAttnKeys + p->N; }
+int64_t key_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / attn_keys(p->D) + p->N; }
 
 gdn_status check_attn(const gdn_attn_problem* p) {
   if (!p) return GDN_ERR_NULL;
@@ -174,15 +174,15 @@ GradCut grad_cut(const gdn_attn_problem* p) {
   const int64_t items = key_tiles(p) * p->HK;
   // rows that see a tile of a sequence of four times the mean length
   const int64_t mean = p->N > 0 ? div_up(p->T, p->N) : 0;
-  const int64_t rows = most_keys(p, std::min<int64_t>(4 * mean, p->T), kAttnKeys) * group(p);
+  const int64_t rows = most_keys(p, std::min<int64_t>(4 * mean, p->T), attn_keys(p->D)) * group(p);
   if (items > 0) c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({4 * kCUs / items, 8, rows / 512}));
   if (p->window && p->sinks && p->T > p->window) {
-    c.far_tiles = (int)div_up(std::min<int64_t>(p->sinks, p->T), kAttnKeys);
-    c.far_rows = std::min<int64_t>((int64_t)p->N * c.far_tiles * kAttnKeys, p->T);
+    c.far_tiles = (int)div_up(std::min<int64_t>(p->sinks, p->T), attn_keys(p->D));
+    c.far_rows = std::min<int64_t>((int64_t)p->N * c.far_tiles * attn_keys(p->D), p->T);
     // at most four times dk's and dv's rows are kept
     const int64_t most = std::min<int64_t>({64, std::max<int64_t>(4 * (int64_t)p->T / c.far_rows, 1),
                                             std::max<int64_t>(kMaxBlocks / 2 / ((int64_t)p->N * c.far_tiles * p->HK), 1)});
-    c.far_pieces = (int)std::min(div_up((int64_t)p->T - p->window, (int64_t)p->window + kAttnKeys), most);
+    c.far_pieces = (int)std::min(div_up((int64_t)p->T - p->window, (int64_t)p->window + attn_keys(p->D)), most);
   }
   return c;
 }

@@ -20,12 +20,7 @@ namespace gdn {
 namespace {
 
 constexpr int kGradKeys = 64;  // keys a step of dq's kernel
-// rows a step of dk's and dv's kernel, in parts of 32
-template <int D>
-constexpr int kGradRows = D == 256 ? 32 : 64;
-// workgroups that share a key tile's columns of dk and dv, with the scores formed in each
-template <int D>
-constexpr int kGradHalves = D == 256 ? 2 : 1;
+constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, in parts of 32
 
 template <typename T>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
@@ -132,14 +127,15 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
       fetch(slot);
       if constexpr (phase >= 1 && phase <= 4) {
         constexpr int half = (phase - 1) / 2;
+        // the argument or difference in one slot, the rest in the next
         for_each<16>([&](auto element) {
-          constexpr int e = element;
-          if constexpr (e * N / 16 == d) {
-            if constexpr (phase % 2) {
-              s[half][e] = exp2_fast(fmaf(s[half][e], c, -lse));
-            } else {
-              dp[half][e] = s[half][e] * fmaf(dp[half][e], scale, -scaled);
-            }
+          constexpr int e = element, at = e * (N - 1) / 16;
+          if constexpr (phase % 2) {
+            if constexpr (d == at) s[half][e] = fmaf(s[half][e], c, -lse);
+            if constexpr (d == at + 1) s[half][e] = exp2_fast(s[half][e]);
+          } else {
+            if constexpr (d == at) dp[half][e] = fmaf(dp[half][e], scale, -scaled);
+            if constexpr (d == at + 1) dp[half][e] *= s[half][e];
           }
         });
         if constexpr (phase % 2 == 0 && d == N - 1) {
@@ -207,25 +203,25 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
       *reinterpret_cast<uint4*>(p + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dq[d], u, 1.f);
 }
 
-// The rows of a sequence that see some of its keys j0 .. j0 + kAttnKeys - 1: in the window, or behind it
+// The rows of a sequence that see some of its keys j0 .. j0 + keys - 1: in the window, or behind it
 // (far, sinks only). In rows of the G query heads, r = token G + head.
 struct RowRange {
   int from, to;
 };
-__device__ __forceinline__ RowRange rows_of(const AttnPack& pk, int len, int j0, bool far) {
+__device__ __forceinline__ RowRange rows_of(const AttnPack& pk, int len, int j0, int keys, bool far) {
   const int W = pk.window, G = pk.G.by;
   if (far) return {min(j0 + W, len) * G, len * G};
-  return {j0 * G, (W ? min(j0 + kAttnKeys - 1 + W, len) : len) * G};
+  return {j0 * G, (W ? min(j0 + keys - 1 + W, len) : len) * G};
 }
 
 // Where a part of the gradients of key tokens goes: [parts][tokens][HK][dk, dv][D] fp32. The parts of
 // sinks hold the first `far_tiles` tiles of every sequence, side by side, or where that is more than the
 // pack's tokens, by token.
-__device__ __forceinline__ int64_t far_rows(const AttnGradArgs& a) {
-  return min((int64_t)a.pack.N * a.far_tiles * kAttnKeys, (int64_t)a.pack.T);
+__device__ __forceinline__ int64_t far_rows(const AttnGradArgs& a, int D) {
+  return min((int64_t)a.pack.N * a.far_tiles * attn_keys(D), (int64_t)a.pack.T);
 }
 __device__ __forceinline__ float* far_at(const AttnGradArgs& a, int part, const RowTile& kt, int token, int hk, int D) {
-  const int64_t rows = far_rows(a), dense = (int64_t)a.far_tiles * kAttnKeys;
+  const int64_t rows = far_rows(a, D), dense = (int64_t)a.far_tiles * attn_keys(D);
   const int64_t r = rows < a.pack.N * dense ? kt.bos + token : kt.seq * dense + token;
   return a.far + (((part * rows + r) * a.pack.HK + hk) * 2) * D;
 }
@@ -235,18 +231,22 @@ __device__ __forceinline__ float* part_at(const AttnGradArgs& a, int part, const
 
 template <typename T, int D>
 __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(AttnGradArgs a) {
-  constexpr int kR = kGradRows<D>, kHalves = kGradHalves<D>, DB = D / 32 / kHalves;
+  // With 256 columns the accumulators of 32 keys would fill all registers, so two waves share them: each forms the scores of
+  // half of a step's rows, they exchange the weights and the scores' gradients as operands through LDS, and each
+  // adds all rows up in half of the columns.
+  constexpr bool kPair = D == 256;
+  constexpr int kR = kGradRows, kKeys = attn_keys(D), N = D / 16, DB = D / 32 / (kPair ? 2 : 1), M = 2 * DB;
   typedef Tile<D, kR, 256> RTile;
   __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
   __shared__ __attribute__((aligned(16))) float stats[2][2][kR];               // [buffer][lse, delta]
+  __shared__ uint4 exchange[kPair ? 4 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int G = pk.G.by;
   int b = blockIdx.x;
   const int hk = b % pk.HK;
   b /= pk.HK;
-  const int col0 = b % kHalves * (D / kHalves);
-  b /= kHalves;
+  const int role = kPair ? wave & 1 : 0, keys0 = (kPair ? wave >> 1 : wave) * 32, col0 = role * (D / 2);
   // first the rows behind the windows of the sinks' tiles, then all tiles' rows
   const int far_items = a.far_pieces * a.far_tiles * pk.N;
   const bool far = b < far_items;
@@ -259,20 +259,20 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     kt.seq = b / a.far_tiles;
     kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
     kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
-    kt.first = b % a.far_tiles * kAttnKeys;
-    kt.tokens = min(kAttnKeys, kt.len - kt.first);
+    kt.first = b % a.far_tiles * kKeys;
+    kt.tokens = min(kKeys, kt.len - kt.first);
   } else {
     b -= far_items;
     pieces = a.pieces;
     piece = b % pieces;
-    kt = tile_of(pk.cu, pk.N, pk.T, kAttnKeys, a.key_slots, b / pieces, false, [](int) { return 0; });
+    kt = tile_of(pk.cu, pk.N, pk.T, kKeys, a.key_slots, b / pieces, false, [](int) { return 0; });
   }
   if (kt.tokens <= 0) return;
-  const RowRange all = rows_of(pk, kt.len, kt.first, far);
+  const RowRange all = rows_of(pk, kt.len, kt.first, kKeys, far);
   const int steps = (all.to - all.from + kR - 1) / kR, share = (steps + pieces - 1) / pieces;
   const int from = all.from + min(piece * share, steps) * kR, to = min(all.to, from + share * kR);
 
-  const int key = wave * 32 + l32, j = kt.first + key;
+  const int key = keys0 + l32, j = kt.first + key;
   const bool live = key < kt.tokens;
   uint4 k[D / 16], v[D / 16];
   {
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     }
   }
   // rows that see this lane's key, and the wave's keys
-  const int W = pk.window, wlo = kt.first + wave * 32, whi = wlo + 31;
+  const int W = pk.window, wlo = kt.first + keys0, whi = wlo + 31;
   const int64_t none = (int64_t)1 << 40, lim = (int64_t)kt.len * G;
   int64_t seen_from = (int64_t)j * G, seen_to = W ? min(((int64_t)j + W) * G, lim) : lim;
   if (far) {
@@ -353,7 +353,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     zero16(dk[i]);
     zero16(dv[i]);
   }
-  const int ka = at<D>(l32, 8 * hi);
+  const int own = role * 32 * D, others = (1 - role) * 32 * D;  // kPair: the waves' halves of a step's rows
+  const int ka = at<D>(l32, 8 * hi) + own;
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, col0 + vc), vb = at<D>(vr + 8, col0 + vc);
   // rows that see any and all of the wave's keys
@@ -364,11 +365,13 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
 
   // 32 rows at r0 with their q, dO and stats in LDS. The matrix instructions go in the order S, dO V^T, dv, dk, each
   // with its LDS operand requested kAhead before, and what the vector unit does in between: the weights
-  // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.)
+  // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.) kPair: Q and O hold both
+  // waves' rows, r0 is this wave's; after its own dv and dk come those of the other's rows.
   auto part = [&](const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0, const auto& fetch) {
-    constexpr int N = D / 16, M = 2 * DB, kSlots = 2 * N + 2 * M, kAhead = 3;
+    constexpr int kOwn = 2 * N + 2 * M, kSlots = kOwn + (kPair ? 2 * M : 0), kAhead = 3;
     f32x16 s, dp;
-    const int kf = fresh(ka), c0 = fresh(va), c1 = fresh(vb);
+    const int kf = fresh(ka), c0 = fresh(va) + own, c1 = fresh(vb) + own;
+    const int e0 = fresh(va) + others, e1 = fresh(vb) + others;
     uint4 op[kAhead], p[2], ds[2];
     auto read = [&](auto slot) {
       constexpr int n = slot;
@@ -377,7 +380,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         x = *reinterpret_cast<const uint4*>((n < N ? Q : O) + (kf ^ (16 * (n % N))));
       } else {
         constexpr int d = (n - 2 * N) % M;
-        x = column8((n < 2 * N + M ? O : Q) + 16 * (d / DB) * D, c0 ^ (32 * (d % DB)), c1 ^ (32 * (d % DB)));
+        const uint16_t* rows = ((n - 2 * N) / M % 2 ? Q : O) + 16 * (d / DB) * D;
+        x = column8(rows, (n < kOwn ? c0 : e0) ^ (32 * (d % DB)), (n < kOwn ? c1 : e1) ^ (32 * (d % DB)));
       }
     };
     f32x4 stat;
@@ -389,26 +393,28 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         s = mfma32_of<T>(x, k[n], n == 0 ? f32x16{} : s);
       } else if constexpr (n < 2 * N) {
         dp = mfma32_of<T>(x, v[n - N], n == N ? f32x16{} : dp);
-      } else if constexpr (n < 2 * N + M) {
-        constexpr int d = n - 2 * N;
+      } else if constexpr ((n - 2 * N) / M % 2 == 0) {
+        constexpr int d = (n - 2 * N) % M;
         dv[d % DB] = mfma32_of<T>(x, p[d / DB], dv[d % DB]);
       } else {
-        constexpr int d = n - 2 * N - M;
+        constexpr int d = (n - 2 * N) % M;
         dk[d % DB] = mfma32_of<T>(x, ds[d / DB], dk[d % DB]);
       }
       if constexpr (n + kAhead < kSlots) read(std::integral_constant<int, n + kAhead>());
       fetch(slot);
-      // the weights of 16 rows, then their gradients
+      // the weights of 16 rows, then their gradients: the argument or difference in one slot, the rest in the next
       for_each<16>([&](auto element) {
-        constexpr int e = element;
-        if constexpr (n == N + e * N / 16) {
+        constexpr int e = element, weight = N + e * (N - 1) / 16, gradient = 2 * N + e * (M - 1) / 16;
+        if constexpr (n == weight) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(ls + 2 * e + 4 * hi);
-          s[e] = exp2_fast(fmaf(s[e], c, -stat[e % 4]));
+          s[e] = fmaf(s[e], c, -stat[e % 4]);
         }
-        if constexpr (n == 2 * N + e * M / 16) {
+        if constexpr (n == weight + 1) s[e] = exp2_fast(s[e]);
+        if constexpr (n == gradient) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(de + 2 * e + 4 * hi);
-          dp[e] = s[e] * fmaf(dp[e], scale, -stat[e % 4]);
+          dp[e] = fmaf(dp[e], scale, -stat[e % 4]);
         }
+        if constexpr (n == gradient + 1) dp[e] *= s[e];
       });
       if constexpr (n == 2 * N - 1) {
         p[0] = operand<T>(s, 0);
@@ -417,6 +423,13 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
       if constexpr (n == 2 * N + M - 1) {
         ds[0] = operand<T>(dp, 0);
         ds[1] = operand<T>(dp, 1);
+      }
+      if constexpr (kPair && n == 2 * N + M) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          exchange[wave][i][lane] = p[i];
+          exchange[wave][2 + i][lane] = ds[i];
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
@@ -428,7 +441,16 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
         s[e] = row >= least && row < most ? s[e] : kMinusInf;
       });
     }
-    for_each<kSlots - N>([&](auto slot) { run(std::integral_constant<int, slot + N>()); });
+    for_each<kOwn - N>([&](auto slot) { run(std::integral_constant<int, slot + N>()); });
+    if constexpr (kPair) {
+      lds_barrier();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p[i] = exchange[wave ^ 1][i][lane];
+        ds[i] = exchange[wave ^ 1][2 + i][lane];
+      }
+      for_each<kSlots - kOwn>([&](auto slot) { run(std::integral_constant<int, slot + kOwn>()); });
+    }
   };
 
   auto keep = [&] {
@@ -443,19 +465,20 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   auto step = [&](int r0, int buf, auto& q, auto& g, auto& nq, auto& ng) {
     const Rows next = rows_from(r0 + kR);
     load_stats(next);
-    for_each<kR / 32>([&](auto half) {
-      constexpr int kParts = kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
-      const int i = half * 32, r = r0 + i;
+    constexpr int kParts = kPair ? 1 : kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
+    for_each<kParts>([&](auto half) {
+      const int i = kPair ? role * 32 : half * 32, r = r0 + i;
       auto fetch = [&](auto slot) {
         constexpr int n = slot, piece = half * kEach + n / 4;
         if constexpr (n % 4 == 0 && n / 4 < kEach && piece < RTile::kPieces)
           request(std::integral_constant<int, piece>(), nq, ng, next);
       };
       keep();
-      if (r + 32 > any_from && r < any_to && r < to && wlo < kt.len)
-        part(q + i * D, g + i * D, stats[buf][0] + i, stats[buf][1] + i, r, fetch);
-      else
-        for_each<4 * kEach>(fetch);
+      // a pair's waves meet in every step: their rows or keys may be masked, but are not left out
+      const bool some = kPair ? r0 < to : r + 32 > any_from && r < any_to && r < to && wlo < kt.len;
+      const int at = kPair ? 0 : i * D;
+      if (some) part(q + at, g + at, stats[buf][0] + i, stats[buf][1] + i, r, fetch);
+      else for_each<4 * kEach>(fetch);
       keep();
     });
     store_stats(buf ^ 1);
@@ -472,7 +495,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     step(r0 + kR, 1, q1, g1, q0, g0);
   }
   if (!live) return;
-  const bool sunk = j / kAttnKeys < a.far_tiles;
+  const bool sunk = j / kKeys < a.far_tiles;
   if (far || a.pieces > 1 || sunk) {
     float* p = far ? far_at(a, piece, kt, j, hk, D)
                    : a.pieces > 1 ? part_at(a, piece, kt, j, hk, D) : far_at(a, a.far_pieces, kt, j, hk, D);
@@ -501,22 +524,23 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
 // workgroup takes eight keys of a tile; without parts of the windows, of the sinks' tiles alone.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a) {
+  constexpr int kKeys = attn_keys(D);
   const AttnPack& pk = a.pack;
   int b = blockIdx.x;
-  const int some = b % (kAttnKeys / 8) * 8;
-  b /= kAttnKeys / 8;
+  const int some = b % (kKeys / 8) * 8;
+  b /= kKeys / 8;
   RowTile kt;
   if (a.pieces > 1) {
-    kt = find_tile(pk.cu, pk.N, pk.T, kAttnKeys, b);
+    kt = find_tile(pk.cu, pk.N, pk.T, kKeys, b);
   } else {
     kt.seq = b / a.far_tiles;
     kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
     kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
-    kt.first = b % a.far_tiles * kAttnKeys;
-    kt.tokens = min(kAttnKeys, kt.len - kt.first);
+    kt.first = b % a.far_tiles * kKeys;
+    kt.tokens = min(kKeys, kt.len - kt.first);
   }
   const int keys = min(8, kt.tokens - some), unit = 2 * pk.HK * D / 4;
-  const bool sunk = kt.first / kAttnKeys < a.far_tiles;
+  const bool sunk = kt.first / kKeys < a.far_tiles;
   const int from_part = a.pieces > 1 ? a.pieces : 0;
   const int from_far = sunk ? a.far_pieces + (a.pieces > 1 ? 0 : 1) : 0;
   for (int i = threadIdx.x; i < keys * unit; i += 256) {
@@ -537,7 +561,7 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a) {
       }
     };
     add(from_part, part_at(a, 0, kt, j, hk, D) + col, (int64_t)pk.T * pk.HK * 2 * D);
-    add(from_far, far_at(a, 0, kt, j, hk, D) + col, far_rows(a) * pk.HK * 2 * D);
+    add(from_far, far_at(a, 0, kt, j, hk, D) + col, far_rows(a, D) * pk.HK * 2 * D);
     uint16_t* to = static_cast<uint16_t*>(col < D ? a.dk : a.dv) + ((int64_t)(kt.bos + j) * pk.HK + hk) * D + col % D;
     *reinterpret_cast<uint2*>(to) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
   }
@@ -553,11 +577,11 @@ hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int items = a.far_pieces * a.far_tiles * pk.N + a.pieces * a.key_slots;
-  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK * kGradHalves<D>), block, 0, s, a);
+  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), block, 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int tiles = a.pieces > 1 ? a.key_slots : a.far_tiles * pk.N;
-  if (tiles > 0) hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(tiles * (kAttnKeys / 8)), block, 0, s, a);
+  if (tiles > 0) hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(tiles * (attn_keys(D) / 8)), block, 0, s, a);
   return hipGetLastError();
 }
 
