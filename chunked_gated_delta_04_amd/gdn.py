@@ -1121,30 +1121,43 @@ def _half(t, name):
     return _HALF[t.dtype]
 
 
-def _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev):
-    """The gdn_kv_cache of tensors [pages, page_size, HK, D] in any order of memory."""
+def _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev):
+    """Why these are no cache and table of a call, as an exception."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            return TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+            return ValueError(f"{name} must be on {dev}, got {t.device}")
         if t.dim() != 4 or t.shape[2] != HK or t.shape[3] != D or t.shape != k_cache.shape:
-            raise ValueError(f"{name} must be [pages, page_size, {HK}, {D}], got {tuple(t.shape)}")
-        if t.stride() != k_cache.stride() or (t.stride(3) != 1 and D > 1):
-            raise ValueError("k_cache and v_cache must have the same strides and dense columns")
-    pages, size = k_cache.shape[:2]
-    # an extent of 1 has no stride of its own
-    strides = [max(s, D) if n == 1 else s for n, s in zip(k_cache.shape[:3], k_cache.stride()[:3])]
+            return ValueError(f"{name} must be [pages, page_size, {HK}, {D}], got {tuple(t.shape)}")
     if page_table.dtype is not torch.int32 or page_table.device != dev:
-        raise ValueError(f"page_table must be int32 on {dev}")
+        return ValueError(f"page_table must be int32 on {dev}")
     if page_table.dim() != 2 or page_table.shape[0] != N:
-        raise ValueError(f"page_table must be [{N}, columns], got {tuple(page_table.shape)}")
-    columns = page_table.shape[1]
-    if (page_table.stride(1) != 1 and columns > 1) or (page_table.stride(0) < columns and N > 1):
-        raise ValueError(f"page_table must have dense rows apart, got strides {page_table.stride()}")
+        return ValueError(f"page_table must be [{N}, columns], got {tuple(page_table.shape)}")
+    if page_table.stride(1) != 1 or page_table.stride(0) < page_table.shape[1]:
+        return ValueError(f"page_table must have dense rows apart, got strides {page_table.stride()}")
+    return ValueError(f"k_cache and v_cache must have the same strides and dense columns, got "
+                      f"{k_cache.stride()} and {v_cache.stride()}")
+
+
+def _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev):
+    """The gdn_kv_cache of tensors [pages, page_size, HK, D] in any order of memory."""
+    shape, strides, table = k_cache.shape, k_cache.stride(), page_table.stride()
+    if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.device != dev
+            or v_cache.device != dev or v_cache.shape != shape or len(shape) != 4 or shape[2] != HK
+            or shape[3] != D or v_cache.stride() != strides or (strides[3] != 1 and D > 1)
+            or page_table.dtype is not torch.int32 or page_table.device != dev or len(table) != 2):
+        raise _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev)
+    rows, columns = page_table.shape
+    if rows != N or (table[1] != 1 and columns > 1) or (table[0] < columns and N > 1):
+        raise _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev)
+    pages, size = shape[0], shape[1]
+    page, token, head = strides[:3]
+    # an extent of 1 has no stride of its own
     return GdnKvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, columns,
-                      page_table.stride(0) if N > 1 else 0, *strides, page_table.data_ptr(),
-                      _dev(offsets, (N,), torch.int32, "offsets", dev))
+                      table[0] if N > 1 else 0, page if pages > 1 else max(page, D),
+                      token if size > 1 else max(token, D), head if HK > 1 else max(head, D),
+                      page_table.data_ptr(), _dev(offsets, (N,), torch.int32, "offsets", dev))
 
 
 def _bounds(cu_seqlens, cu_seqlens_host, dev):
@@ -1175,35 +1188,37 @@ def kv_append(k, v, k_cache, v_cache, page_table, offsets, cu_seqlens=None, q=No
     [N, columns] and offsets [N] (tokens that each sequence had before) int32. cu_seqlens [N+1] int32, or
     None for one token of each sequence. inv_freq [R / 2] fp32, or None: nothing turns. q_out: where q's
     result goes (q itself: in place), by default a new tensor. Returns q_out, or None without q."""
-    dev = _on_device(k, "k")
-    dtype = _half(k, "k")
-    T, HK, D = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
+    dev, kind = _on_device(k, "k"), _half(k, "k")
+    dtype, shape = k.dtype, k.shape
+    T, HK, D = shape
+    if v.shape != shape:
+        raise ValueError(f"v must be {tuple(shape)}, got {tuple(v.shape)}")
     HQ = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D:
-            raise ValueError(f"q must be [{T}, HQ, {D}], got {tuple(q.shape)}")
-        HQ = q.shape[1]
+        wide = q.shape
+        if len(wide) != 3 or wide[0] != T or wide[2] != D:
+            raise ValueError(f"q must be [{T}, HQ, {D}], got {tuple(wide)}")
+        HQ = wide[1]
     N, cu, host = T, None, None
     if cu_seqlens is not None:
         N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
-    kp, ks = _rows(k, k.dtype, "k", dev)
-    vp, vs = _rows(v, k.dtype, "v", dev)
-    qp, qs = _rows(q, k.dtype, "q", dev) if HQ else (None, 0)
+    kp, ks = _rows(k, dtype, "k", dev)
+    vp, vs = _rows(v, dtype, "v", dev)
+    qp, qs = _rows(q, dtype, "q", dev) if HQ else (None, 0)
     R = 2 * inv_freq.numel() if inv_freq is not None else 0
-    p = GdnKvAppendProblem(N, T, HQ, HK, D, R, bool(interleaved), dtype, mscale, cu, host, qs, ks, vs, 0)
+    p = GdnKvAppendProblem(N, T, HQ, HK, D, R, bool(interleaved), kind, mscale, cu, host, qs, ks, vs, 0)
     freq = _dev(inv_freq, (R // 2,), _f32, "inv_freq", dev)
-    cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, k.dtype, dev)
+    cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev)
 
     def call(s):
         out, op = q_out, None
-        if HQ:
-            if out is None:
-                out = torch.empty(T, HQ, D, dtype=k.dtype, device=dev)
-            elif out.shape != q.shape:
-                raise ValueError(f"q_out must have the shape {tuple(q.shape)}, got {tuple(out.shape)}")
-            op, p.q_out_stride = _rows(out, k.dtype, "q_out", dev)
+        if HQ and out is None:
+            out = torch.empty(wide, dtype=dtype, device=dev)
+            op = out.data_ptr()
+        elif HQ:
+            if out.shape != wide:
+                raise ValueError(f"q_out must have the shape {tuple(wide)}, got {tuple(out.shape)}")
+            op, p.q_out_stride = _rows(out, dtype, "q_out", dev)
         _check(_lib.gdn_kv_append(ctypes.byref(p), ctypes.byref(cache), freq, qp, kp, vp, op, s),
                "gdn_kv_append")
         return out if HQ else None
@@ -1214,14 +1229,15 @@ def kv_append(k, v, k_cache, v_cache, page_table, offsets, cu_seqlens=None, q=No
 
 def _attn_call(name, p, cache, q, want_lse, ptrs):
     """call(stream) of one forward: allocates o, lse and the workspace."""
-    T, HQ, D = q.shape
+    size, run, dev = getattr(_lib, name + "_workspace_size"), getattr(_lib, name), q.device
     args = [ctypes.byref(p)] + ([ctypes.byref(cache)] if cache is not None else [])
 
     def call(s):
-        o = torch.empty(T, HQ, D, dtype=q.dtype, device=q.device)
-        lse = torch.empty(T, HQ, dtype=_f32, device=q.device) if want_lse else None
-        ws = _alloc_bytes(getattr(_lib, name + "_workspace_size")(*args), q.device)
-        _check(getattr(_lib, name)(*args, *ptrs, o.data_ptr(), _at(lse), _at(ws), _bytes(ws), s), name)
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        lse = torch.empty(q.shape[:2], dtype=_f32, device=dev) if want_lse else None
+        n = size(*args)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        _check(run(*args, *ptrs, o.data_ptr(), _at(lse), _at(ws), n, s), name)
         return o, lse
 
     return call
