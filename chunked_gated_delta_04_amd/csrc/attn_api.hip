@@ -175,7 +175,7 @@ GradCut grad_cut(const gdn_attn_problem* p) {
   // rows that see a tile of a sequence of four times the mean length
   const int64_t mean = p->N > 0 ? div_up(p->T, p->N) : 0;
   const int64_t rows = most_keys(p, std::min<int64_t>(4 * mean, p->T), attn_keys(p->D)) * group(p);
-  if (items > 0) c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({4 * kCUs / items, 8, rows / 512}));
+  if (items > 0) c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({4 * kCUs / items, 8, rows / 256}));
   if (p->window && p->sinks && p->T > p->window) {
     c.far_tiles = (int)div_up(std::min<int64_t>(p->sinks, p->T), attn_keys(p->D));
     c.far_rows = std::min<int64_t>((int64_t)p->N * c.far_tiles * attn_keys(p->D), p->T);

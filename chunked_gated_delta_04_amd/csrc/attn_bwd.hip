@@ -57,28 +57,22 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   const int whi = t0 + min(divide(wave * 32 + 31, pk.G), rt.tokens - 1);
   const int64_t out = (int64_t)(rt.bos + t0 + token) * pk.HQ + head;
 
-  uint4 q[N], g[N];
-  float delta = 0.f, lse = INFINITY;  // weights of rows that see nothing are zeros
+  // Rows past the tile's tokens read its last token, and have no weights. All requests go out before one is waited for.
+  const int64_t from_token = rt.bos + t0 + min(token, rt.tokens - 1), from_row = from_token * pk.HQ + head;
+  uint4 q[N], g[N], y[N];
   {
-    const uint16_t* pq = static_cast<const uint16_t*>(a.q) + (int64_t)(rt.bos + t0 + token) * a.q_stride + head * D + 8 * hi;
-    const uint16_t* pg = static_cast<const uint16_t*>(a.dO) + out * D + 8 * hi;
-    const uint16_t* po = static_cast<const uint16_t*>(a.o) + out * D + 8 * hi;
+    const uint16_t* pq = static_cast<const uint16_t*>(a.q) + from_token * a.q_stride + head * D + 8 * hi;
+    const uint16_t* pg = static_cast<const uint16_t*>(a.dO) + from_row * D + 8 * hi;
+    const uint16_t* po = static_cast<const uint16_t*>(a.o) + from_row * D + 8 * hi;
 #pragma unroll
     for (int s = 0; s < N; ++s) {
-      q[s] = g[s] = make_uint4(0, 0, 0, 0);
-      if (live) {
-        q[s] = *reinterpret_cast<const uint4*>(pq + 16 * s);
-        g[s] = *reinterpret_cast<const uint4*>(pg + 16 * s);
-        delta += dot8<T>(*reinterpret_cast<const uint4*>(po + 16 * s), g[s]);
-      }
-    }
-    delta = sum_halves(delta);
-    if (live) {
-      lse = a.lse[out] * kLog2e;
-      if (lse == kMinusInf) lse = INFINITY;
-      if (hi == 0) a.delta[out] = delta;
+      q[s] = *reinterpret_cast<const uint4*>(pq + 16 * s);
+      g[s] = *reinterpret_cast<const uint4*>(pg + 16 * s);
+      y[s] = *reinterpret_cast<const uint4*>(po + 16 * s);
     }
   }
+  float lse = a.lse[from_row] * kLog2e, delta = 0.f;
+  if (!live || lse == kMinusInf) lse = INFINITY;  // weights of rows that see nothing are zeros
 
   const uint16_t* kbase = static_cast<const uint16_t*>(a.k) + rt.bos * a.k_stride + hk * D;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.v) + rt.bos * a.v_stride + hk * D;
@@ -91,7 +85,8 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   f32x16 dq[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) zero16(dq[i]);
-  const float c = pk.scale * kLog2e, scale = pk.scale, scaled = scale * delta;
+  const float c = pk.scale * kLog2e, scale = pk.scale;
+  float scaled = 0.f;  // scale times delta
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vrow = 4 * hi + (j16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vrow, vcol), vb = at<D>(vrow + 8, vcol);
@@ -188,6 +183,11 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     kr.request(k0, i, krows, tid);
     vr.request(v0, i, vrows, tid);
   });
+#pragma unroll
+  for (int s = 0; s < N; ++s) delta += dot8<T>(y[s], g[s]);
+  delta = sum_halves(delta);
+  if (live && hi == 0) a.delta[out] = delta;
+  scaled = scale * delta;
   __syncthreads();
 #pragma unroll 1
   for (int i = 0; i < kt.count; i += 2) {  // a step past the last tile does nothing
@@ -274,17 +274,16 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
 
   const int key = keys0 + l32, j = kt.first + key;
   const bool live = key < kt.tokens;
-  uint4 k[D / 16], v[D / 16];
+  uint4 k[N], v[N];
   {
-    const uint16_t* pkk = static_cast<const uint16_t*>(a.k) + (int64_t)(kt.bos + j) * a.k_stride + hk * D + 8 * hi;
-    const uint16_t* pv = static_cast<const uint16_t*>(a.v) + (int64_t)(kt.bos + j) * a.v_stride + hk * D + 8 * hi;
+    // keys past the tile's tokens read its last token; no row sees them
+    const int64_t token = kt.bos + kt.first + min(key, kt.tokens - 1);
+    const uint16_t* pkk = static_cast<const uint16_t*>(a.k) + token * a.k_stride + hk * D + 8 * hi;
+    const uint16_t* pv = static_cast<const uint16_t*>(a.v) + token * a.v_stride + hk * D + 8 * hi;
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      k[s] = v[s] = make_uint4(0, 0, 0, 0);
-      if (live) {
-        k[s] = *reinterpret_cast<const uint4*>(pkk + 16 * s);
-        v[s] = *reinterpret_cast<const uint4*>(pv + 16 * s);
-      }
+    for (int s = 0; s < N; ++s) {
+      k[s] = *reinterpret_cast<const uint4*>(pkk + 16 * s);
+      v[s] = *reinterpret_cast<const uint4*>(pv + 16 * s);
     }
   }
   // rows that see this lane's key, and the wave's keys
@@ -302,7 +301,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   const float* lses = a.lse + (int64_t)kt.bos * pk.HQ + hk * G;
   const float* deltas = a.delta + (int64_t)kt.bos * pk.HQ + hk * G;
   const float c = pk.scale * kLog2e, scale = pk.scale;
-  float lse = INFINITY, delta = 0.f;  // of row tid: times log2(e) and the scale
+  float lse = INFINITY, delta = 0.f;  // of row tid of the next step
   const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
   // a step's rows from r0 on: offsets from its first token, its rows are of at most kR + 1 tokens
   struct Rows {
@@ -334,16 +333,15 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
       delta = 0.f;
       if (tid < rows.count) {
         const int64_t at = (int64_t)(rows.first + token) * pk.HQ + h;
-        lse = lses[at] * kLog2e;
-        if (lse == kMinusInf) lse = INFINITY;
-        delta = deltas[at] * scale;
+        lse = lses[at];
+        delta = deltas[at];
       }
     }
   };
   auto store_stats = [&](int buf) {
     if (tid < kR) {
-      stats[buf][0][tid] = lse;
-      stats[buf][1][tid] = delta;
+      stats[buf][0][tid] = lse == kMinusInf ? INFINITY : lse * kLog2e;  // weights of rows that see nothing are zeros
+      stats[buf][1][tid] = delta * scale;
     }
   };
 

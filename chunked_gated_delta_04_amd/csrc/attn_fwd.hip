@@ -82,12 +82,11 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
 
   uint4 q[N];
   {
-    const uint16_t* p = static_cast<const uint16_t*>(a.q) + (int64_t)(rt.bos + rt.first + token) * a.q_stride + head * D + 8 * hi;
+    // rows past the tile's tokens read its last token, and are not stored
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) +
+                        (int64_t)(rt.bos + rt.first + min(token, rt.tokens - 1)) * a.q_stride + head * D + 8 * hi;
 #pragma unroll
-    for (int s = 0; s < N; ++s) {
-      q[s] = make_uint4(0, 0, 0, 0);
-      if (live) q[s] = *reinterpret_cast<const uint4*>(p + 16 * s);
-    }
+    for (int s = 0; s < N; ++s) q[s] = *reinterpret_cast<const uint4*>(p + 16 * s);
   }
 
   const uint16_t* kbase = static_cast<const uint16_t*>(kPaged ? a.pages.k : a.k);

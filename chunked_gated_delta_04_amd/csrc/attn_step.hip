@@ -66,16 +66,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
   const int2 part = split_of(kt.count, a.splits, split, 4);
   const int from = pk.window ? t - pk.window : -1;
 
-  const bool live = g0 + i16 < G;
   const int head = hk * G + g0 + i16;
   uint4 q[D / 32];
   {
-    const uint16_t* p = static_cast<const uint16_t*>(a.q) + seq * a.q_stride + head * D + 8 * q4;
+    // rows past the group read its last head, and are not stored
+    const uint16_t* p = static_cast<const uint16_t*>(a.q) + seq * a.q_stride + min(head, hk * G + G - 1) * D + 8 * q4;
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      q[s] = make_uint4(0, 0, 0, 0);
-      if (live) q[s] = *reinterpret_cast<const uint4*>(p + 32 * s);
-    }
+    for (int s = 0; s < D / 32; ++s) q[s] = *reinterpret_cast<const uint4*>(p + 32 * s);
   }
   const uint16_t* kbase = static_cast<const uint16_t*>(a.pages.k) + hk * a.pages.head_stride;
   const uint16_t* vbase = static_cast<const uint16_t*>(a.pages.v) + hk * a.pages.head_stride;
