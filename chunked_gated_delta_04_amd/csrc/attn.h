@@ -64,7 +64,7 @@ struct AttnGradArgs {
   const void *q, *k, *v, *o, *dO;
   int64_t q_stride, k_stride, v_stride;
   const float* lse;
-  float* delta;  // [T, HQ]: dO . o of each row
+  float* stats;  // [2][T, HQ]: of each row, lse in base 2 (infinite where it sees nothing), scale dO . o
   void *dq, *dk, *dv;
   int slots;                 // row tiles
   int key_slots;             // key tiles

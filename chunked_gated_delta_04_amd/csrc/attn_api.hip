@@ -186,15 +186,15 @@ GradCut grad_cut(const gdn_attn_problem* p) {
   }
   return c;
 }
-// bytes of the workspace: delta, then the parts of the windows, then those of the sinks
+// bytes of the workspace: the rows' statistics, then the parts of the windows, then those of the sinks
 struct GradBytes {
-  size_t delta, part, far;
-  size_t all() const { return delta + part + far; }
+  size_t stats, part, far;
+  size_t all() const { return stats + part + far; }
 };
 GradBytes grad_bytes(const gdn_attn_problem* p) {
   const GradCut c = grad_cut(p);
   const size_t row = (size_t)p->HK * 2 * p->D * sizeof(float);
-  GradBytes b{((size_t)p->T * p->HQ * sizeof(float) + 15) / 16 * 16, 0, 0};
+  GradBytes b{(2 * (size_t)p->T * p->HQ * sizeof(float) + 15) / 16 * 16, 0, 0};
   if (c.pieces > 1) b.part = c.pieces * (size_t)p->T * row;
   if (c.far_tiles) b.far = (size_t)(c.far_pieces + (c.pieces > 1 ? 0 : 1)) * c.far_rows * row;
   return b;
@@ -304,9 +304,9 @@ GDN_API int gdn_attn_bwd(const gdn_attn_problem* p, const void* q, const void* k
   a.far_pieces = cut.far_pieces;
   a.far_tiles = cut.far_tiles;
   char* ws = static_cast<char*>(workspace);
-  a.delta = reinterpret_cast<float*>(ws);
-  a.part = reinterpret_cast<float*>(ws + bytes.delta);
-  a.far = reinterpret_cast<float*>(ws + bytes.delta + bytes.part);
+  a.stats = reinterpret_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(ws + bytes.stats);
+  a.far = reinterpret_cast<float*>(ws + bytes.stats + bytes.part);
   GDN_TRY(launch_attn_bwd(static_cast<Elem>(p->dtype), p->D, a, reinterpret_cast<hipStream_t>(stream)));
   return GDN_OK;
 }

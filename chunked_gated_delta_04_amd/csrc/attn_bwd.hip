@@ -3,8 +3,8 @@
 //   dS = scale P (dO V^T - delta):   dq = dS K,   dk = dS^T q,   dv = P^T dO,
 // the rows of all query heads of a key head summed in dk and dv.
 //
-// Two kernels, without atomics: one goes over the keys for 128 rows (dq, and
-// delta on the way), the other over the rows for 128 keys (dk, dv). Both form
+// Two kernels, without atomics: one goes over the keys for its rows (dq, and
+// the rows' statistics on the way), the other over the rows for 128 keys (dk, dv). Both form
 // the scores and dO V^T again: seven products instead of the five that one
 // kernel with atomic sums of dq would take. As in the forward, each operand
 // that follows from scores is used where it stands in the accumulator.
@@ -20,7 +20,11 @@ namespace gdn {
 namespace {
 
 constexpr int kGradKeys = 64;  // keys a step of dq's kernel
-constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, in parts of 32
+// Steps between the request for a tile and its use: two where a third buffer fits the LDS. The requests of one step
+// alone took longer than it: dk and dv of 2 x 8192 tokens, window 1024, 16 + 4 heads of 128, 478 us, now NEWKV; dq 247 us, now NEWQ.
+template <int D>
+constexpr int kGradAhead = D == 256 ? 1 : 2;
+constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, one to a lane, in parts of 32
 
 template <typename T>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
@@ -39,7 +43,9 @@ template <typename T, int D>
 __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
   constexpr int kT = kGradKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
   typedef Tile<D, kT, kThreads> KTile;
+  constexpr int kAheadTiles = kGradAhead<D>;
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
+  __shared__ __attribute__((aligned(16))) uint16_t k2[kAheadTiles == 2 ? kT * D : 8], v2[kAheadTiles == 2 ? kT * D : 8];
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int hk = blockIdx.x % pk.HK;
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   // the first half, of the second, each with its LDS operand requested kAhead before; the vector unit
   // forms the weights and the scores' gradients of a half during the products that follow it.
   auto part = [&](const uint16_t* K, const uint16_t* V, int j0, const auto& fetch) {
-    constexpr int kAhead = 3;
+    constexpr int kAhead = 6;
     f32x16 s[2], dp[2];
     const int j1 = j0 + kT - 1;
     bool mask = j1 > wlo;
@@ -160,11 +166,11 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     for (int d = 0; d < DB; ++d) keep_accumulated<D == 256>(dq[d]);
   };
 
-  // one step: tile i in (k, v), the next one on its way to (nk, nv), a request every second slot
+  // one step: tile i in (k, v), the one kAheadTiles later on its way to (nk, nv), a request every second slot
+  constexpr int P = KTile::kPieces;
   auto step = [&](int i, auto& k, auto& v, auto& nk, auto& nv) {
     const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
-    const auto krows = tokens(kbase, a.k_stride, i + 1), vrows = tokens(vbase, a.v_stride, i + 1);
-    constexpr int P = KTile::kPieces;
+    const auto krows = tokens(kbase, a.k_stride, i + kAheadTiles), vrows = tokens(vbase, a.v_stride, i + kAheadTiles);
     auto fetch = [&](auto slot) {
       constexpr int n = slot, r = n / 2;
       if constexpr (n % 2 == 0 && r < P) kr.request(nk, r, krows, tid);
@@ -176,23 +182,36 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     if (some) part(k, v, j0, fetch);
     else for_each<4 * P>(fetch);
     keep();
-    __syncthreads();
+    end_step<(kAheadTiles - 1) * 2 * P>();
   };
-  const auto krows = tokens(kbase, a.k_stride, 0), vrows = tokens(vbase, a.v_stride, 0);
-  for_each<KTile::kPieces>([&](auto i) {
-    kr.request(k0, i, krows, tid);
-    vr.request(v0, i, vrows, tid);
-  });
+  auto fill = [&](int i, auto& k, auto& v) {
+    const auto krows = tokens(kbase, a.k_stride, i), vrows = tokens(vbase, a.v_stride, i);
+    for_each<P>([&](auto n) {
+      kr.request(k, n, krows, tid);
+      vr.request(v, n, vrows, tid);
+    });
+  };
+  fill(0, k0, v0);
+  if constexpr (kAheadTiles == 2) fill(1, k1, v1);
 #pragma unroll
   for (int s = 0; s < N; ++s) delta += dot8<T>(y[s], g[s]);
   delta = sum_halves(delta);
-  if (live && hi == 0) a.delta[out] = delta;
   scaled = scale * delta;
+  if (live && hi == 0) {
+    a.stats[out] = lse;
+    a.stats[(int64_t)pk.T * pk.HQ + out] = scaled;
+  }
   __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < kt.count; i += 2) {  // a step past the last tile does nothing
-    step(i, k0, v0, k1, v1);
-    step(i + 1, k1, v1, k0, v0);
+  for (int i = 0; i < kt.count; i += kAheadTiles + 1) {  // steps past the last tile do nothing
+    if constexpr (kAheadTiles == 2) {
+      step(i, k0, v0, k2, v2);
+      step(i + 1, k1, v1, k0, v0);
+      step(i + 2, k2, v2, k1, v1);
+    } else {
+      step(i, k0, v0, k1, v1);
+      step(i + 1, k1, v1, k0, v0);
+    }
   }
   if (!live) return;
   uint16_t* p = static_cast<uint16_t*>(a.dq) + out * D;
@@ -237,8 +256,10 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   constexpr bool kPair = D == 256;
   constexpr int kR = kGradRows, kKeys = attn_keys(D), N = D / 16, DB = D / 32 / (kPair ? 2 : 1), M = 2 * DB;
   typedef Tile<D, kR, 256> RTile;
+  constexpr int kAheadTiles = kGradAhead<D>;
   __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
-  __shared__ __attribute__((aligned(16))) float stats[2][2][kR];               // [buffer][lse, delta]
+  __shared__ __attribute__((aligned(16))) uint16_t q2[kAheadTiles == 2 ? kR * D : 8], g2[kAheadTiles == 2 ? kR * D : 8];
+  __shared__ __attribute__((aligned(16))) float stats0[2 * kR], stats1[2 * kR], stats2[2 * kR];  // lse, then delta
   __shared__ uint4 exchange[kPair ? 4 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
@@ -298,10 +319,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
 
   const uint16_t* qbase = static_cast<const uint16_t*>(a.q) + kt.bos * a.q_stride + hk * G * D;
   const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
-  const float* lses = a.lse + (int64_t)kt.bos * pk.HQ + hk * G;
-  const float* deltas = a.delta + (int64_t)kt.bos * pk.HQ + hk * G;
   const float c = pk.scale * kLog2e, scale = pk.scale;
-  float lse = INFINITY, delta = 0.f;  // of row tid of the next step
   const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
   // a step's rows from r0 on: offsets from its first token, its rows are of at most kR + 1 tokens
   struct Rows {
@@ -326,23 +344,14 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     RTile::request(qs, i, rows.q, ok ? (__umul24(token, (int)a.q_stride) + col) * 2 : -1, tid);
     RTile::request(gs, i, rows.g, ok ? (__umul24(token, pk.HQ * D) + col) * 2 : -1, tid);
   };
-  auto load_stats = [&](const Rows& rows) {
-    if (tid < kR) {
-      const int r = rows.before + tid, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
-      lse = INFINITY;
-      delta = 0.f;
-      if (tid < rows.count) {
-        const int64_t at = (int64_t)(rows.first + token) * pk.HQ + h;
-        lse = lses[at];
-        delta = deltas[at];
-      }
-    }
-  };
-  auto store_stats = [&](int buf) {
-    if (tid < kR) {
-      stats[buf][0][tid] = lse == kMinusInf ? INFINITY : lse * kLog2e;  // weights of rows that see nothing are zeros
-      stats[buf][1][tid] = delta * scale;
-    }
+  // The rows' statistics as the other kernel wrote them: even waves request lse, odd ones delta, one request each in every wave.
+  auto request_stats = [&](auto& stats, const Rows& rows) {
+    const int r = rows.before + lane, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
+    const float* p = a.stats + ((wave & 1) * (int64_t)pk.T + kt.bos + rows.first) * pk.HQ + hk * G;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, 0x7ffffff0, kBufferWord3),
+        (__attribute__((address_space(3))) void*)(stats + (wave & 1) * kR), 4,
+        lane < rows.count ? (__umul24(token, pk.HQ) + h) * 4 : -1, 0, 0, 0);
   };
 
   f32x16 dk[DB], dv[DB];
@@ -366,7 +375,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   // during dO V^T, the scores' gradients during dv. (The compiler keeps the order of the slots.) kPair: Q and O hold both
   // waves' rows, r0 is this wave's; after its own dv and dk come those of the other's rows.
   auto part = [&](const uint16_t* Q, const uint16_t* O, const float* ls, const float* de, int r0, const auto& fetch) {
-    constexpr int kOwn = 2 * N + 2 * M, kSlots = kOwn + (kPair ? 2 * M : 0), kAhead = 3;
+    constexpr int kOwn = 2 * N + 2 * M, kSlots = kOwn + (kPair ? 2 * M : 0), kAhead = 6;
     f32x16 s, dp;
     const int kf = fresh(ka), c0 = fresh(va) + own, c1 = fresh(vb) + own;
     const int e0 = fresh(va) + others, e1 = fresh(vb) + others;
@@ -459,10 +468,10 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     }
   };
 
-  // one step: rows from r0 in (q, g), the next ones on their way to (nq, ng), a request every fourth slot
-  auto step = [&](int r0, int buf, auto& q, auto& g, auto& nq, auto& ng) {
-    const Rows next = rows_from(r0 + kR);
-    load_stats(next);
+  // one step: rows from r0 in (q, g), those kAheadTiles later on their way to (nq, ng), a request every fourth slot
+  auto step = [&](int r0, auto& q, auto& g, auto& stats, auto& nq, auto& ng, auto& nstats) {
+    const Rows next = rows_from(r0 + kAheadTiles * kR);
+    request_stats(nstats, next);
     constexpr int kParts = kPair ? 1 : kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
     for_each<kParts>([&](auto half) {
       const int i = kPair ? role * 32 : half * 32, r = r0 + i;
@@ -475,22 +484,30 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
       // a pair's waves meet in every step: their rows or keys may be masked, but are not left out
       const bool some = kPair ? r0 < to : r + 32 > any_from && r < any_to && r < to && wlo < kt.len;
       const int at = kPair ? 0 : i * D;
-      if (some) part(q + at, g + at, stats[buf][0] + i, stats[buf][1] + i, r, fetch);
+      if (some) part(q + at, g + at, stats + i, stats + kR + i, r, fetch);
       else for_each<4 * kEach>(fetch);
       keep();
     });
-    store_stats(buf ^ 1);
-    __syncthreads();
+    end_step<(kAheadTiles - 1) * (2 * RTile::kPieces + 1)>();
   };
-  const Rows rows = rows_from(from);
-  for_each<RTile::kPieces>([&](auto i) { request(i, q0, g0, rows); });
-  load_stats(rows);
-  store_stats(0);
+  auto fill = [&](int r0, auto& q, auto& g, auto& stats) {
+    const Rows rows = rows_from(r0);
+    request_stats(stats, rows);
+    for_each<RTile::kPieces>([&](auto i) { request(i, q, g, rows); });
+  };
+  fill(from, q0, g0, stats0);
+  if constexpr (kAheadTiles == 2) fill(from + kR, q1, g1, stats1);
   __syncthreads();
 #pragma unroll 1
-  for (int r0 = from; r0 < to; r0 += 2 * kR) {  // a step past the last row does nothing
-    step(r0, 0, q0, g0, q1, g1);
-    step(r0 + kR, 1, q1, g1, q0, g0);
+  for (int r0 = from; r0 < to; r0 += (kAheadTiles + 1) * kR) {  // steps past the last row do nothing
+    if constexpr (kAheadTiles == 2) {
+      step(r0, q0, g0, stats0, q2, g2, stats2);
+      step(r0 + kR, q1, g1, stats1, q0, g0, stats0);
+      step(r0 + 2 * kR, q2, g2, stats2, q1, g1, stats1);
+    } else {
+      step(r0, q0, g0, stats0, q1, g1, stats1);
+      step(r0 + kR, q1, g1, stats1, q0, g0, stats0);
+    }
   }
   if (!live) return;
   const bool sunk = j / kKeys < a.far_tiles;
