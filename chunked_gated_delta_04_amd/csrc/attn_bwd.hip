@@ -228,9 +228,10 @@ struct RowRange {
   int from, to;
 };
 __device__ __forceinline__ RowRange rows_of(const AttnPack& pk, int len, int j0, int keys, bool far) {
-  const int W = pk.window, G = pk.G.by;
-  if (far) return {min(j0 + W, len) * G, len * G};
-  return {j0 * G, (W ? min(j0 + keys - 1 + W, len) : len) * G};
+  const int G = pk.G.by;
+  const int64_t W = pk.window;
+  if (far) return {(int)min(j0 + W, (int64_t)len) * G, len * G};
+  return {j0 * G, (int)(W ? min(j0 + keys - 1 + W, (int64_t)len) : len) * G};
 }
 
 // Where a part of the gradients of key tokens goes: [parts][tokens][HK][dk, dv][D] fp32. The parts of
@@ -370,9 +371,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   const int j16 = lane & 15, vr = 4 * hi + (j16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vr, col0 + vc), vb = at<D>(vr + 8, col0 + vc);
   // rows that see any and all of the wave's keys
-  const int64_t any_from = far ? (int64_t)(wlo + W) * G : (int64_t)wlo * G;
+  const int64_t any_from = far ? ((int64_t)wlo + W) * G : (int64_t)wlo * G;
   const int64_t any_to = far ? (wlo < pk.sinks ? lim : 0) : W ? ((int64_t)whi + W) * G : lim;
-  const int64_t all_from = far ? (whi < pk.sinks ? (int64_t)(whi + W) * G : none) : (int64_t)whi * G;
+  const int64_t all_from = far ? (whi < pk.sinks ? ((int64_t)whi + W) * G : none) : (int64_t)whi * G;
   const int64_t all_to = !far && W ? ((int64_t)wlo + W) * G : lim;
 
   // 32 rows at r0 with their q, dO and stats in LDS. The matrix instructions go in the order S, dO V^T, dv, dk, each
