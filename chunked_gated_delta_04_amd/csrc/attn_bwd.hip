@@ -20,10 +20,6 @@ namespace gdn {
 namespace {
 
 constexpr int kGradKeys = 64;  // keys a step of dq's kernel
-// Steps between the request for a tile and its use: two where a third buffer fits the LDS. The requests of one step
-// alone took longer than it: dk and dv of 2 x 8192 tokens, window 1024, 16 + 4 heads of 128, 478 us, now NEWKV; dq 247 us, now NEWQ.
-template <int D>
-constexpr int kGradAhead = D == 256 ? 1 : 2;
 constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, one to a lane, in parts of 32
 
 template <typename T>
@@ -43,9 +39,7 @@ template <typename T, int D>
 __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
   constexpr int kT = kGradKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
   typedef Tile<D, kT, kThreads> KTile;
-  constexpr int kAheadTiles = kGradAhead<D>;
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
-  __shared__ __attribute__((aligned(16))) uint16_t k2[kAheadTiles == 2 ? kT * D : 8], v2[kAheadTiles == 2 ? kT * D : 8];
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int hk = blockIdx.x % pk.HK;
@@ -166,11 +160,12 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     for (int d = 0; d < DB; ++d) keep_accumulated<D == 256>(dq[d]);
   };
 
-  // one step: tile i in (k, v), the one kAheadTiles later on its way to (nk, nv), a request every second slot
+  // one step: tile i in (k, v), the next on its way to (nk, nv), a request every second slot. (A third buffer, with requests two
+  // steps ahead, gained nothing in either kernel: 2 x 8192 tokens, window 1024, 16 + 4 heads of 128, 740 us for both, 723 without.)
   constexpr int P = KTile::kPieces;
   auto step = [&](int i, auto& k, auto& v, auto& nk, auto& nv) {
     const int j0 = kt.at(i) * kT, j1 = j0 + kT - 1;
-    const auto krows = tokens(kbase, a.k_stride, i + kAheadTiles), vrows = tokens(vbase, a.v_stride, i + kAheadTiles);
+    const auto krows = tokens(kbase, a.k_stride, i + 1), vrows = tokens(vbase, a.v_stride, i + 1);
     auto fetch = [&](auto slot) {
       constexpr int n = slot, r = n / 2;
       if constexpr (n % 2 == 0 && r < P) kr.request(nk, r, krows, tid);
@@ -182,7 +177,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     if (some) part(k, v, j0, fetch);
     else for_each<4 * P>(fetch);
     keep();
-    end_step<(kAheadTiles - 1) * 2 * P>();
+    __syncthreads();
   };
   auto fill = [&](int i, auto& k, auto& v) {
     const auto krows = tokens(kbase, a.k_stride, i), vrows = tokens(vbase, a.v_stride, i);
@@ -192,7 +187,6 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     });
   };
   fill(0, k0, v0);
-  if constexpr (kAheadTiles == 2) fill(1, k1, v1);
 #pragma unroll
   for (int s = 0; s < N; ++s) delta += dot8<T>(y[s], g[s]);
   delta = sum_halves(delta);
@@ -203,15 +197,9 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   }
   __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < kt.count; i += kAheadTiles + 1) {  // steps past the last tile do nothing
-    if constexpr (kAheadTiles == 2) {
-      step(i, k0, v0, k2, v2);
-      step(i + 1, k1, v1, k0, v0);
-      step(i + 2, k2, v2, k1, v1);
-    } else {
-      step(i, k0, v0, k1, v1);
-      step(i + 1, k1, v1, k0, v0);
-    }
+  for (int i = 0; i < kt.count; i += 2) {  // a step past the last tile does nothing
+    step(i, k0, v0, k1, v1);
+    step(i + 1, k1, v1, k0, v0);
   }
   if (!live) return;
   uint16_t* p = static_cast<uint16_t*>(a.dq) + out * D;
@@ -257,10 +245,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   constexpr bool kPair = D == 256;
   constexpr int kR = kGradRows, kKeys = attn_keys(D), N = D / 16, DB = D / 32 / (kPair ? 2 : 1), M = 2 * DB;
   typedef Tile<D, kR, 256> RTile;
-  constexpr int kAheadTiles = kGradAhead<D>;
   __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
-  __shared__ __attribute__((aligned(16))) uint16_t q2[kAheadTiles == 2 ? kR * D : 8], g2[kAheadTiles == 2 ? kR * D : 8];
-  __shared__ __attribute__((aligned(16))) float stats0[2 * kR], stats1[2 * kR], stats2[2 * kR];  // lse, then delta
+  __shared__ __attribute__((aligned(16))) float stats0[2 * kR], stats1[2 * kR];  // lse, then delta
   __shared__ uint4 exchange[kPair ? 4 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
@@ -474,10 +460,10 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     }
   };
 
-  // one step: its rows in (q, g), those of kAheadTiles later on their way to (nq, ng), a request every fourth slot
+  // one step: its rows in (q, g), the next step's on their way to (nq, ng), a request every fourth slot
   auto step = [&](int index, auto& q, auto& g, auto& stats, auto& nq, auto& ng, auto& nstats) {
     const int r0 = row_of(index);
-    const Rows next = rows_from(index + kAheadTiles);
+    const Rows next = rows_from(index + 1);
     request_stats(nstats, next);
     constexpr int kParts = kPair ? 1 : kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
     for_each<kParts>([&](auto half) {
@@ -495,7 +481,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
       else for_each<4 * kEach>(fetch);
       keep();
     });
-    end_step<(kAheadTiles - 1) * (2 * RTile::kPieces + 1)>();
+    __syncthreads();
   };
   auto fill = [&](int index, auto& q, auto& g, auto& stats) {
     const Rows rows = rows_from(index);
@@ -503,18 +489,11 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
     for_each<RTile::kPieces>([&](auto i) { request(i, q, g, rows); });
   };
   fill(0, q0, g0, stats0);
-  if constexpr (kAheadTiles == 2) fill(1, q1, g1, stats1);
   __syncthreads();
 #pragma unroll 1
-  for (int i = 0; i < n_steps; i += kAheadTiles + 1) {  // steps past the last one do nothing
-    if constexpr (kAheadTiles == 2) {
-      step(i, q0, g0, stats0, q2, g2, stats2);
-      step(i + 1, q1, g1, stats1, q0, g0, stats0);
-      step(i + 2, q2, g2, stats2, q1, g1, stats1);
-    } else {
-      step(i, q0, g0, stats0, q1, g1, stats1);
-      step(i + 1, q1, g1, stats1, q0, g0, stats0);
-    }
+  for (int i = 0; i < n_steps; i += 2) {  // a step past the last one does nothing
+    step(i, q0, g0, stats0, q1, g1, stats1);
+    step(i + 1, q1, g1, stats1, q0, g0, stats0);
   }
   if (!live) return;
   const bool sunk = j / kKeys < a.far_tiles;

@@ -184,19 +184,6 @@ struct Tile {
 // whether request_group holds for a cache
 __host__ __device__ inline bool in_groups(const KvPages& c) { return c.page.by % 8 == 0 && c.token_stride < (1 << 24); }
 
-// The end of a step that issued kLater requests after those that the next step reads: they are waited for, those kLater stay
-// in flight, and the waves meet.
-template <int kLater>
-__device__ __forceinline__ void end_step() {
-  static_assert(kLater < 64, "six bits");
-  if constexpr (kLater == 0) {
-    __syncthreads();
-  } else {
-    __builtin_amdgcn_s_waitcnt((kLater & 15) | (kLater >> 4) << 14 | 7 << 4 | 15 << 8);
-    lds_barrier();
-  }
-}
-
 // Requests for token rows at a stride: a lane's byte offsets of request 0 (and of request 1 less a step, where the
 // permutation differs), the others a step of kRows rows apart each.
 template <class Tile>
