@@ -69,7 +69,8 @@ struct AttnGradArgs {
   int slots;                 // row tiles
   int key_slots;             // key tiles
   int pieces;                // parts of a key tile's rows
-  int far_pieces, far_tiles; // parts of the rows that see a sequence's sinks from behind the window; key tiles with sinks
+  // parts of the rows that see a sequence's sinks from behind the window; its key tiles with sinks; all those tiles' places
+  int far_pieces, far_tiles, far_slots;
   float *part, *far;         // partial dk and dv
 };
 

@@ -166,11 +166,11 @@ int run_fwd(const gdn_attn_problem* p, bool paged, const AttnArgs& a, hipStream_
 // the rows that see the sinks from behind the window, of one tile or few, into parts as long as the
 // other tiles' rows. Both from the extents alone.
 struct GradCut {
-  int pieces, far_pieces, far_tiles;
+  int pieces, far_pieces, far_tiles, far_slots;
   int64_t far_rows;
 };
 GradCut grad_cut(const gdn_attn_problem* p) {
-  GradCut c{1, 0, 0, 0};
+  GradCut c{1, 0, 0, 0, 0};
   const int64_t items = key_tiles(p) * p->HK;
   // rows that see a tile of a sequence of four times the mean length
   const int64_t mean = p->N > 0 ? div_up(p->T, p->N) : 0;
@@ -178,10 +178,11 @@ GradCut grad_cut(const gdn_attn_problem* p) {
   if (items > 0) c.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({4 * kCUs / items, 8, rows / 256}));
   if (p->window && p->sinks && p->T > p->window) {
     c.far_tiles = (int)div_up(std::min<int64_t>(p->sinks, p->T), attn_keys(p->D));
+    c.far_slots = (int)std::min((int64_t)p->N * c.far_tiles, key_tiles(p));
     c.far_rows = std::min<int64_t>((int64_t)p->N * c.far_tiles * attn_keys(p->D), p->T);
     // at most four times dk's and dv's rows are kept
     const int64_t most = std::min<int64_t>({64, std::max<int64_t>(4 * (int64_t)p->T / c.far_rows, 1),
-                                            std::max<int64_t>(kMaxBlocks / 2 / ((int64_t)p->N * c.far_tiles * p->HK), 1)});
+                                            std::max<int64_t>(kMaxBlocks / 2 / ((int64_t)c.far_slots * p->HK), 1)});
     c.far_pieces = (int)std::min(div_up((int64_t)p->T - p->window, (int64_t)p->window + attn_keys(p->D)), most);
   }
   return c;
@@ -303,6 +304,7 @@ GDN_API int gdn_attn_bwd(const gdn_attn_problem* p, const void* q, const void* k
   a.pieces = cut.pieces;
   a.far_pieces = cut.far_pieces;
   a.far_tiles = cut.far_tiles;
+  a.far_slots = cut.far_slots;
   char* ws = static_cast<char*>(workspace);
   a.stats = reinterpret_cast<float*>(ws);
   a.part = reinterpret_cast<float*>(ws + bytes.stats);

@@ -237,6 +237,24 @@ __device__ __forceinline__ float* part_at(const AttnGradArgs& a, int part, const
   return a.part + ((((int64_t)part * a.pack.T + kt.bos + token) * a.pack.HK + hk) * 2) * D;
 }
 
+// Tile i of those with sinks: of every sequence its first far_tiles, or where that is more than all tiles there may be,
+// all slots in the pack's order.
+__device__ __forceinline__ RowTile far_tile(const AttnGradArgs& a, int i, int keys) {
+  const AttnPack& pk = a.pack;
+  RowTile t;
+  if ((int64_t)pk.N * a.far_tiles > a.far_slots) {
+    t = find_tile(pk.cu, pk.N, pk.T, keys, i);
+    if (t.first / keys >= a.far_tiles) t.tokens = 0;
+    return t;
+  }
+  t.seq = i / a.far_tiles;
+  t.bos = min(max(pk.cu[t.seq], 0), pk.T);
+  t.len = min(max(pk.cu[t.seq + 1], t.bos), pk.T) - t.bos;
+  t.first = i % a.far_tiles * keys;
+  t.tokens = min(keys, t.len - t.first);
+  return t;
+}
+
 template <typename T, int D>
 __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(AttnGradArgs a) {
   // With 256 columns the accumulators of 32 keys would fill all registers, so two waves share them: each forms the scores of
@@ -256,19 +274,14 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   b /= pk.HK;
   const int role = kPair ? wave & 1 : 0, keys0 = (kPair ? wave >> 1 : wave) * 32, col0 = role * (D / 2);
   // first the rows behind the windows of the sinks' tiles, then all tiles' rows
-  const int far_items = a.far_pieces * a.far_tiles * pk.N;
+  const int far_items = a.far_pieces * a.far_slots;
   const bool far = b < far_items;
   int piece, pieces;
   RowTile kt;
   if (far) {
     pieces = a.far_pieces;
     piece = b % pieces;
-    b /= pieces;
-    kt.seq = b / a.far_tiles;
-    kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
-    kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
-    kt.first = b % a.far_tiles * kKeys;
-    kt.tokens = min(kKeys, kt.len - kt.first);
+    kt = far_tile(a, b / pieces, kKeys);
   } else {
     b -= far_items;
     pieces = a.pieces;
@@ -524,22 +537,11 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
 // The parts of dk and dv, in order: first those in the window, then those of the rows behind it. A
 // workgroup takes eight keys of a tile; without parts of the windows, of the sinks' tiles alone.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a) {
+__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, int first) {
   constexpr int kKeys = attn_keys(D);
   const AttnPack& pk = a.pack;
-  int b = blockIdx.x;
-  const int some = b % (kKeys / 8) * 8;
-  b /= kKeys / 8;
-  RowTile kt;
-  if (a.pieces > 1) {
-    kt = find_tile(pk.cu, pk.N, pk.T, kKeys, b);
-  } else {
-    kt.seq = b / a.far_tiles;
-    kt.bos = min(max(pk.cu[kt.seq], 0), pk.T);
-    kt.len = min(max(pk.cu[kt.seq + 1], kt.bos), pk.T) - kt.bos;
-    kt.first = b % a.far_tiles * kKeys;
-    kt.tokens = min(kKeys, kt.len - kt.first);
-  }
+  const int some = blockIdx.x % (kKeys / 8) * 8, b = blockIdx.x / (kKeys / 8) + first;
+  const RowTile kt = a.pieces > 1 ? find_tile(pk.cu, pk.N, pk.T, kKeys, b) : far_tile(a, b, kKeys);
   const int keys = min(8, kt.tokens - some), unit = 2 * pk.HK * D / 4;
   const bool sunk = kt.first / kKeys < a.far_tiles;
   const int from_part = a.pieces > 1 ? a.pieces : 0;
@@ -577,13 +579,16 @@ hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((attn_grad_q_kernel<T, D>), dim3(a.slots * pk.HK), dim3(2 * attn_rows(D)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int items = a.far_pieces * a.far_tiles * pk.N + a.pieces * a.key_slots;
+  const int items = a.far_pieces * a.far_slots + a.pieces * a.key_slots;
   hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), block, 0, s, a);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int tiles = a.pieces > 1 ? a.key_slots : a.far_tiles * pk.N;
-  if (tiles > 0) hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(tiles * (attn_keys(D) / 8)), block, 0, s, a);
-  return hipGetLastError();
+  const int tiles = a.pieces > 1 ? a.key_slots : a.far_slots, most = 1 << 19;  // most: 2^23 workgroups
+  for (int first = 0; first < tiles && e == hipSuccess; first += most) {
+    const int n = std::min(tiles - first, most);
+    hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(n * (attn_keys(D) / 8)), block, 0, s, a, first);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace

@@ -657,9 +657,10 @@ int gdn_rmsnorm_bwd(const gdn_rmsnorm_problem* p, const void* s, const void* wei
  *               the heads' columns and below 2^23, or 0 for dense rows
  * Rows of the outputs at or past cu_seqlens[N] are left as they were. No output
  * overlaps an input. A NaN or infinity in a token's k or v can spoil the outputs
- * of its sequence's tokens that share a tile of rows (128 / (HQ / HK) tokens)
- * or keys (64) with one that sees it; its q or dO, the gradients of k and v of
- * the keys that share a tile (128) with one that it sees. */
+ * of its sequence's tokens that share a tile of rows (256 / (HQ / HK) tokens,
+ * half as many with D = 256) or keys (64) with one that sees it; its q or dO, the
+ * gradients of k and v of the keys that share a tile (128, 64 with D = 256) with
+ * one that it sees. */
 typedef struct {
   int32_t N, T, HQ, HK, D, dtype;
   int32_t window, sinks;

@@ -201,6 +201,50 @@ def test_many_sequences(n, window, sinks):
         check(name, g[name], ref[name], bound[name], "bf16")
 
 
+def test_far_and_negative_offsets():
+    """Positions past the table and below zero, to the ends of 32 bits."""
+    far, low = [(1 << 31) - 300, 1 << 30, 900], [-(1 << 31), -(1 << 30), -60]
+    q, k, v = bf(150, 4, 64), bf(150, 2, 64, seed=1), bf(150, 2, 64, seed=2)
+    kc, vc = bf(60, SIZE, 2, 64, seed=3), bf(60, SIZE, 2, 64, seed=4)
+    table = torch.arange(1, 31, device="cuda").int().expand(3, 30).contiguous()  # 480 positions
+    cu, one = ints(0, 50, 100, 150), dict(page_table=table, want_lse=True)
+    for mask in (dict(), dict(window=100, sinks=3)):
+        was = kc.clone(), vc.clone()
+        for past in (far, low):
+            gdn.kv_append(k, v, kc, vc, table, ints(*past), cu_seqlens=cu)
+            gdn.kv_append(k[:3], v[:3], kc, vc, table, ints(*past))
+        assert torch.equal(kc, was[0]) and torch.equal(vc, was[1])
+        rows = torch.cat([q[:50]] * 3)
+        o, lse = gdn.attn_fwd_paged(rows, kc, vc, cu_seqlens=cu, offsets=ints(*far), **one, **mask)
+        for n in (0, 1):
+            assert torch.equal(o[50 * n:50 * n + 50], o[100:]) and torch.equal(lse[50 * n:50 * n + 50], lse[100:])
+        assert bool(lse.isfinite().all())
+        s, ls = gdn.attn_step(torch.cat([q[:1]] * 3), kc, vc, offsets=ints(*far), **one, **mask)
+        assert torch.equal(s[0], s[2]) and torch.equal(s[1], s[2]) and torch.equal(ls[0], ls[2]) and bool(ls.isfinite().all())
+        o, lse = gdn.attn_fwd_paged(rows, kc, vc, cu_seqlens=cu, offsets=ints(*low), **one, **mask)
+        s, ls = gdn.attn_step(q[:3], kc, vc, offsets=ints(*low), **one, **mask)
+        assert not o.any() and not s.any() and bool((lse == -torch.inf).all()) and bool((ls == -torch.inf).all())
+
+
+def test_sinks_beyond_every_sequence():
+    """All keys are sinks: what no window gives, also where the sequences' tiles are far fewer than sinks would be."""
+    r = np.random.default_rng(1)
+    lens = r.integers(0, 6, 1000).tolist()
+    lens[500], lens[20] = 700, 131
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T = cu[-1]
+    q, k, v, dO = bf(T, 2, 64), bf(T, 1, 64, seed=1), bf(T, 1, 64, seed=2), bf(T, 2, 64, seed=3)
+    mask = dict(window=3, sinks=1 << 30)
+    o, lse = gdn.attn_fwd(q, k, v, ints(*cu), want_lse=True, **mask)
+    g = gdn.attn_bwd(q, k, v, ints(*cu), o, lse, dO, **mask)
+    args = [f64(x) for x in (q, k, v)]
+    bound = pack_bounds(*args, cu, 0, 0, "bf16", f64(dO))
+    ref = A.backward(*args, cu, f64(dO))
+    check("o", o, A.forward(*args, cu)[0], bound["o"])
+    for name in g:
+        check(name, g[name], ref[name], bound[name], "bf16")
+
+
 @pytest.mark.parametrize("HQ, HK, D, window", [(4, 2, 64, 0), (4, 1, 128, 9), (2, 1, 256, 0)])
 def test_gradients_against_differences(HQ, HK, D, window):
     """The kernels' gradients against differences of the kernels' own forward, along random directions: the loss sum(o dO) is
