@@ -76,7 +76,7 @@ struct AttnGradArgs {
 
 // rows of a workgroup's tile, 32 to a wave; with 256 columns a wave has a SIMD's registers to itself
 constexpr int attn_rows(int D) { return D == 256 ? 128 : 256; }
-// keys of a workgroup's tile in the backward, 32 to a wave, or with 256 columns to two
+// keys of a workgroup's tile in the backward: 32 to a wave, from 128 columns on to two
 constexpr int attn_keys(int D) { return D == 256 ? 64 : 128; }
 constexpr int kAttnGroup = 128; // most query heads to a key head
 

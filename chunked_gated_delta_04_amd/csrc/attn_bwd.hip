@@ -4,10 +4,14 @@
 // the rows of all query heads of a key head summed in dk and dv.
 //
 // Two kernels, without atomics: one goes over the keys for its rows (dq, and
-// the rows' statistics on the way), the other over the rows for 128 keys (dk, dv). Both form
-// the scores and dO V^T again: seven products instead of the five that one
-// kernel with atomic sums of dq would take. As in the forward, each operand
-// that follows from scores is used where it stands in the accumulator.
+// the rows' statistics on the way), the other over the rows for 128 keys, 64 with
+// 256 columns (dk, dv). Both form the scores and dO V^T again: seven products instead
+// of the five that one kernel with atomic sums of dq would take. As in the forward,
+// each operand that follows from scores is used where it stands in the accumulator.
+//
+// Bound by the matrix unit and the waits around it. 2 x 8192 tokens, 16 + 2 heads
+// of 256 columns: dq 1.48 ms (1.11 PFLOP/s of its three products), dk and dv 2.6 ms
+// (0.85, of four); window 1024, 16 + 4 heads of 128: 245 us, 415 us, joining 13 us.
 //
 // P and dS are rounded once to the inputs' type, where they are multiplied; all
 // sums are fp32.
@@ -20,6 +24,7 @@ namespace gdn {
 namespace {
 
 constexpr int kGradKeys = 64;  // keys a step of dq's kernel
+constexpr int grad_threads(int D) { return D == 128 ? 512 : 256; }
 constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, one to a lane, in parts of 32
 
 template <typename T>
@@ -256,16 +261,18 @@ __device__ __forceinline__ RowTile far_tile(const AttnGradArgs& a, int i, int ke
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(AttnGradArgs a) {
-  // With 256 columns the accumulators of 32 keys would fill all registers, so two waves share them: each forms the scores of
-  // half of a step's rows, they exchange the weights and the scores' gradients as operands through LDS, and each
-  // adds all rows up in half of the columns.
-  constexpr bool kPair = D == 256;
+__global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_kv_kernel(AttnGradArgs a) {
+  // From 128 columns on two waves share the accumulators of 32 keys: each forms the scores of half of a step's rows, they
+  // exchange the weights and the scores' gradients as operands through LDS, and each adds all rows up in half of the
+  // columns. 256 columns would fill all registers otherwise; with 128 a SIMD then holds two waves instead of one (2 x 8192
+  // tokens, window 1024, 16 + 4 heads, backward: 727 us with a wave for 32 keys, 672 in pairs).
+  constexpr bool kPair = D >= 128;
+  constexpr int kThreads = grad_threads(D);
   constexpr int kR = kGradRows, kKeys = attn_keys(D), N = D / 16, DB = D / 32 / (kPair ? 2 : 1), M = 2 * DB;
-  typedef Tile<D, kR, 256> RTile;
+  typedef Tile<D, kR, kThreads> RTile;
   __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
   __shared__ __attribute__((aligned(16))) float stats0[2 * kR], stats1[2 * kR];  // lse, then delta
-  __shared__ uint4 exchange[kPair ? 4 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
+  __shared__ uint4 exchange[kPair ? kThreads / 64 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int G = pk.G.by;
@@ -468,8 +475,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
   auto keep = [&] {
 #pragma unroll
     for (int d = 0; d < DB; ++d) {
-      keep_accumulated<(D >= 128)>(dk[d]);
-      keep_accumulated<(D >= 128)>(dv[d]);
+      keep_accumulated<(D == 256)>(dk[d]);
+      keep_accumulated<(D == 256)>(dv[d]);
     }
   };
 
@@ -487,7 +494,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_grad_kv_kernel(Attn
           request(std::integral_constant<int, piece>(), nq, ng, next);
       };
       keep();
-      // a pair's waves meet in every step: their rows or keys may be masked, but are not left out
+      // a pair's waves meet in every step: their rows or keys may be masked, but are not left out (a branch around them
+      // cost registers: 2 x 8192 tokens, 16 + 2 heads of 256 columns, backward 4090 us without, 4265 with it)
       const bool some = index < n_steps && (kPair || (r + 32 > any_from && r < any_to && r < to && wlo < kt.len));
       const int at = kPair ? 0 : i * D;
       if (some) part(q + at, g + at, stats + i, stats + kR + i, r, fetch);
@@ -580,7 +588,7 @@ hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int items = a.far_pieces * a.far_slots + a.pieces * a.key_slots;
-  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), block, 0, s, a);
+  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), dim3(grad_threads(D)), 0, s, a);
   e = hipGetLastError();
   const int tiles = a.pieces > 1 ? a.key_slots : a.far_slots, most = 1 << 19;  // most: 2^23 workgroups
   for (int first = 0; first < tiles && e == hipSuccess; first += most) {
