@@ -33,7 +33,7 @@ namespace {
 constexpr int kFwdKeys = 64;  // keys a tile
 
 // where the keys are: token rows, pages whose rows come in groups of 8 (see request_group; 8 x 512 tokens, four after 1000 to
-// 2000, 152.7 us, by rows 165.4), other pages
+// 2000, 152.7 us, by rows 165.4), other pages, and a window's, whose edge may leave part of a group unread
 enum { kTokens, kGroups, kPages };
 
 }  // namespace
@@ -106,10 +106,14 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
     kbase += rt.bos * a.k_stride + hk * D;
     vbase += rt.bos * a.v_stride + hk * D;
   }
-  // paged: where row `lane` of tiles i, i + 1 and i + 2 is
+  // paged: where row `lane` of tiles i, i + 1 and i + 2 is; rows that no token of the tile has in its window are not read
+  // (a freed page may hold anything)
   int64_t rows[3] = {-1, -1, -1};
   auto look = [&](int i) -> int64_t {
-    return kPaged && i < part.y ? row_at(a.pages, rt.seq, kt.at(i) * kT + lane, keys) : -1;
+    if (!kPaged || i >= part.y) return -1;
+    const int j = kt.at(i) * kT + lane;
+    if (kKeys == kPages && pk.window && j <= t0 - pk.window && j >= pk.sinks) return -1;
+    return row_at(a.pages, rt.seq, j, keys);
   };
   const TokenRows<KTile> kr((int)a.k_stride, tid), vr((int)a.v_stride, tid);
   int64_t off = -1;  // kPages: where this lane's piece of the next request is
@@ -383,7 +387,7 @@ hipError_t fwd_of(int D, bool paged, const AttnArgs& a, hipStream_t s) {
   const dim3 grid(a.slots * a.pack.HK * a.splits), block(2 * attn_rows(D));
 #define GDN_FWD(d)                                                                                                 \
   if (!paged) hipLaunchKernelGGL((attn_fwd_kernel<T, d, kTokens>), grid, block, 0, s, a);                          \
-  else if (in_groups(a.pages)) hipLaunchKernelGGL((attn_fwd_kernel<T, d, kGroups>), grid, block, 0, s, a);         \
+  else if (in_groups(a)) hipLaunchKernelGGL((attn_fwd_kernel<T, d, kGroups>), grid, block, 0, s, a);         \
   else hipLaunchKernelGGL((attn_fwd_kernel<T, d, kPages>), grid, block, 0, s, a)
   if (D == 64) GDN_FWD(64);
   else if (D == 128) GDN_FWD(128);

@@ -181,8 +181,10 @@ struct Tile {
     request(tile, i, r, lane, tid);
   }
 };
-// whether request_group holds for a cache
-__host__ __device__ inline bool in_groups(const KvPages& c) { return c.page.by % 8 == 0 && c.token_stride < (1 << 24); }
+// whether request_group holds for a call
+inline bool in_groups(const AttnArgs& a) {
+  return a.pages.page.by % 8 == 0 && a.pages.token_stride < (1 << 24) && !a.pack.window;
+}
 
 // Requests for token rows at a stride: a lane's byte offsets of request 0 (and of request 1 less a step, where the
 // permutation differs), the others a step of kRows rows apart each.

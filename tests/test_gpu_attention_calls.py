@@ -226,6 +226,26 @@ def test_far_and_negative_offsets():
         assert not o.any() and not s.any() and bool((lse == -torch.inf).all()) and bool((ls == -torch.inf).all())
 
 
+@pytest.mark.parametrize("size", [16, 17])
+@pytest.mark.parametrize("D, window, sinks", [(64, 100, 3), (128, 33, 0), (256, 7, 70)])
+def test_pages_behind_the_window_hold_anything(size, D, window, sinks):
+    past, lens, cu = [900, 40], [30, 300], ints(0, 30, 330)
+    q, cols = bf(330, 4, D), -(-930 // size)
+    kc, vc = bf(2 * cols + 1, size, 2, D, seed=1), bf(2 * cols + 1, size, 2, D, seed=2)
+    table = (torch.randperm(2 * cols, generator=torch.Generator().manual_seed(size)) + 1).int().view(2, cols).cuda()
+    args = dict(page_table=table, cu_seqlens=cu, offsets=ints(*past), window=window, sinks=sinks, want_lse=True)
+    want = gdn.attn_fwd_paged(q, kc, vc, **args)
+    one = dict(page_table=table, offsets=ints(930, 340), window=window, sinks=sinks, want_lse=True)
+    step = gdn.attn_step(q[:2], kc, vc, **one)
+    kn, vn = torch.full_like(kc, torch.nan), torch.full_like(vc, torch.inf)
+    for n, (p, t) in enumerate(zip(past, lens)):
+        j = torch.tensor([j for j in range(p + t + 1) if j < sinks or j > p - window], device="cuda")
+        at = table[n, j // size].long(), j % size
+        kn[at], vn[at] = kc[at], vc[at]
+    assert same(gdn.attn_fwd_paged(q, kn, vn, **args), want)
+    assert same(gdn.attn_step(q[:2], kn, vn, **one), step)
+
+
 def test_sinks_beyond_every_sequence():
     """All keys are sinks: what no window gives, also where the sequences' tiles are far fewer than sinks would be."""
     r = np.random.default_rng(1)
