@@ -64,7 +64,8 @@ struct AttnGradArgs {
   const void *q, *k, *v, *o, *dO;
   int64_t q_stride, k_stride, v_stride;
   const float* lse;
-  float* stats;  // [2][T, HQ]: of each row, lse in base 2 (infinite where it sees nothing), scale dO . o
+  float* stats;  // [grad_stats][T, HQ]: of each row, lse in base 2 (infinite where it sees nothing), scale dO . o,
+                 // with fp16 its largest score gradient
   void *dq, *dk, *dv;
   int slots;                 // row tiles
   int key_slots;             // key tiles
@@ -79,6 +80,10 @@ constexpr int attn_rows(int D) { return D == 256 ? 128 : 256; }
 // keys of a workgroup's tile in the backward: 32 to a wave, from 128 columns on to two
 constexpr int attn_keys(int D) { return D == 256 ? 64 : 128; }
 constexpr int kAttnGroup = 128; // most query heads to a key head
+// whether the backward's score gradients are multiplied in units of their own: where the type's range is short
+template <typename T>
+constexpr bool kHasUnits = std::is_same<T, Fp16>::value;
+constexpr int grad_stats(Elem type) { return type == Elem::kFp16 ? 3 : 2; }
 
 hipError_t launch_attn_fwd(Elem type, int D, bool paged, const AttnArgs& a, hipStream_t s);
 hipError_t launch_attn_step(Elem type, int D, const AttnArgs& a, hipStream_t s);

@@ -198,7 +198,7 @@ struct GradBytes {
 GradBytes grad_bytes(const gdn_attn_problem* p) {
   const GradCut c = grad_cut(p);
   const size_t row = (size_t)p->HK * 2 * p->D * sizeof(float);
-  GradBytes b{(2 * (size_t)p->T * p->HQ * sizeof(float) + 15) / 16 * 16, 0, 0};
+  GradBytes b{(grad_stats(static_cast<Elem>(p->dtype)) * (size_t)p->T * p->HQ * sizeof(float) + 15) / 16 * 16, 0, 0};
   if (c.pieces > 1) b.part = c.pieces * (size_t)p->T * row;
   if (c.far_tiles) b.far = (size_t)(c.far_pieces + (c.pieces > 1 ? 0 : 1)) * c.far_rows * row;
   return b;

@@ -14,7 +14,11 @@
 // (0.85, of four); window 1024, 16 + 4 heads of 128: 245 us, 415 us, joining 13 us.
 //
 // P and dS are rounded once to the inputs' type, where they are multiplied; all
-// sums are fp32.
+// sums are fp32. fp16's range is short for dS, which falls with the number of keys
+// and with the cotangent's size: it is multiplied in units of a power of two that
+// follows its largest value (see refit), dq and dk are taken back at the end. 8192 keys of 128
+// columns, a cotangent of size 0.001: dq is 0.0005 of its norm off, of which 0.0004 is its own rounding;
+// in one unit for all it was 0.024. The units cost the backward of ten ragged sequences of 64 columns 4 of 62 us.
 #include <algorithm>
 
 #include "attn_tile.h"
@@ -38,11 +42,25 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
+// fp16: the factor for score gradients whose largest is `top` (in the present unit), 1 where they are between
+// 2^7 and 2^15: then none is past fp16's largest, and what is lost of one is at most 2^-32 of the largest. Else
+// the largest comes to 2^10 .. 2^11, and stays for some growth. unit: at most 2^40, so that sums in it are far
+// from fp32's end; zeros, infinities and NaN change nothing.
+constexpr float kUnitLeast = 128.f, kUnitMost = 32768.f, kUnitEnd = 1099511627776.f;
+__device__ __forceinline__ bool ill_fit(float top, float unit) {
+  return (top > kUnitMost && top < INFINITY) || (top < kUnitLeast && top > 0.f && unit < kUnitEnd);
+}
+__device__ __forceinline__ float refit(float top, float unit) {
+  const int most = 41 - __builtin_amdgcn_frexp_expf(unit);  // unit = 2^(its exponent - 1)
+  return ldexpf(1.f, min(11 - __builtin_amdgcn_frexp_expf(top), most));
+}
+
 }  // namespace
 
 template <typename T, int D>
 __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_q_kernel(AttnGradArgs a) {
   constexpr int kT = kGradKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
+  constexpr bool kUnits = kHasUnits<T>;
   typedef Tile<D, kT, kThreads> KTile;
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
@@ -90,8 +108,9 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   f32x16 dq[DB];
 #pragma unroll
   for (int i = 0; i < DB; ++i) zero16(dq[i]);
-  const float c = pk.scale * kLog2e, scale = pk.scale;
-  float scaled = 0.f;  // scale times delta
+  const float c = pk.scale * kLog2e;
+  float scale = pk.scale, scaled = 0.f;  // scaled: scale times delta
+  float unit = 1.f, largest = 0.f;       // kUnits: of this row's dS; scale, scaled and dq are in it
   const int ka = at<D>(l32, 8 * hi);
   const int j16 = lane & 15, vrow = 4 * hi + (j16 >> 2), vcol = 16 * ((lane >> 4) & 1) + 4 * (j16 & 3);
   const int va = at<D>(vrow, vcol), vb = at<D>(vrow + 8, vcol);
@@ -139,6 +158,30 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
           }
         });
         if constexpr (phase % 2 == 0 && d == N - 1) {
+          if constexpr (kUnits) {
+            float top = 0.f;
+            for_each<16>([&](auto element) {
+              constexpr int e = element;
+              top = fmaxf(top, fabsf(dp[half][e]));
+            });
+            const float2 tops = both_halves(top);
+            largest = fmaxf(largest, fmaxf(tops.x, tops.y));
+            const bool ill = ill_fit(largest, unit);
+            if (__any(ill)) {
+              const float by = ill ? refit(largest, unit) : 1.f;
+              unit *= by;
+              largest *= by;
+              scale *= by;
+              scaled *= by;
+              dp[half] *= by;
+#pragma unroll
+              for (int i = 0; i < DB; ++i) {
+                keep_accumulated<D == 256>(dq[i]);
+                dq[i] *= by;
+                keep_accumulated<D == 256>(dq[i]);
+              }
+            }
+          }
           ds[2 * half] = operand<T>(dp[half], 0);
           ds[2 * half + 1] = operand<T>(dp[half], 1);
         }
@@ -207,12 +250,14 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
     step(i + 1, k1, v1, k0, v0);
   }
   if (!live) return;
+  const float back = 1.f / unit;
+  if (kUnits && hi == 0) a.stats[2 * (int64_t)pk.T * pk.HQ + out] = largest * back;
   uint16_t* p = static_cast<uint16_t*>(a.dq) + out * D;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<uint4*>(p + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dq[d], u, 1.f);
+      *reinterpret_cast<uint4*>(p + 32 * d + 16 * u + 8 * hi) = eight_columns<T>(dq[d], u, back);
 }
 
 // The rows of a sequence that see some of its keys j0 .. j0 + keys - 1: in the window, or behind it
@@ -266,12 +311,13 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
   // exchange the weights and the scores' gradients as operands through LDS, and each adds all rows up in half of the
   // columns. 256 columns would fill all registers otherwise; with 128 a SIMD then holds two waves instead of one (2 x 8192
   // tokens, window 1024, 16 + 4 heads, backward: 727 us with a wave for 32 keys, 672 in pairs).
-  constexpr bool kPair = D >= 128;
+  constexpr bool kPair = D >= 128, kUnits = kHasUnits<T>;
   constexpr int kThreads = grad_threads(D);
   constexpr int kR = kGradRows, kKeys = attn_keys(D), N = D / 16, DB = D / 32 / (kPair ? 2 : 1), M = 2 * DB;
   typedef Tile<D, kR, kThreads> RTile;
   __shared__ __attribute__((aligned(16))) typename RTile::Lds q0, q1, g0, g1;  // q and dO
-  __shared__ __attribute__((aligned(16))) float stats0[2 * kR], stats1[2 * kR];  // lse, then delta
+  // lse, then delta; kUnits: and the largest dS
+  __shared__ __attribute__((aligned(16))) float stats0[(kUnits ? 3 : 2) * kR], stats1[(kUnits ? 3 : 2) * kR];
   __shared__ uint4 exchange[kPair ? kThreads / 64 : 1][4][64];  // [wave][two operands of weights, two of gradients][lane]
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
@@ -326,7 +372,9 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
 
   const uint16_t* qbase = static_cast<const uint16_t*>(a.q) + kt.bos * a.q_stride + hk * G * D;
   const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
-  const float c = pk.scale * kLog2e, scale = pk.scale;
+  const float c = pk.scale * kLog2e;
+  // kUnits: of dS, by the largest of a step's 64 rows, which all waves know; scale and dk are in it
+  float unit = 1.f, scale = pk.scale;
   const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
   // a step's rows from r0 on: offsets from its first token, its rows are of at most kR + 1 tokens
   struct Rows {
@@ -356,14 +404,19 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
     RTile::request(qs, i, rows.q, ok ? (__umul24(token, (int)a.q_stride) + col) * 2 : -1, tid);
     RTile::request(gs, i, rows.g, ok ? (__umul24(token, pk.HQ * D) + col) * 2 : -1, tid);
   };
-  // The rows' statistics as the other kernel wrote them: even waves request lse, odd ones delta, one request each in every wave.
-  auto request_stats = [&](auto& stats, const Rows& rows) {
+  // The rows' statistics as the other kernel wrote them: even waves request lse, odd ones delta, one request each in every wave
+  // (kUnits: and the rows' largest dS).
+  auto request_stat = [&](auto& stats, const Rows& rows, int which) {
     const int r = rows.before + lane, token = __umul24(r, per_token) >> 16, h = r - __umul24(token, G);
-    const float* p = a.stats + ((wave & 1) * (int64_t)pk.T + kt.bos + rows.first) * pk.HQ + hk * G;
+    const float* p = a.stats + (which * (int64_t)pk.T + kt.bos + rows.first) * pk.HQ + hk * G;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, 0x7ffffff0, kBufferWord3),
-        (__attribute__((address_space(3))) void*)(stats + (wave & 1) * kR), 4,
+        (__attribute__((address_space(3))) void*)(stats + which * kR), 4,
         lane < rows.count ? (__umul24(token, pk.HQ) + h) * 4 : -1, 0, 0, 0);
+  };
+  auto request_stats = [&](auto& stats, const Rows& rows) {
+    request_stat(stats, rows, wave & 1);
+    if constexpr (kUnits) request_stat(stats, rows, 2);
   };
 
   f32x16 dk[DB], dv[DB];
@@ -431,6 +484,7 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
         if constexpr (n == weight + 1) s[e] = exp2_fast(s[e]);
         if constexpr (n == gradient) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(de + 2 * e + 4 * hi);
+          if constexpr (kUnits) stat[e % 4] *= unit;
           dp[e] = fmaf(dp[e], scale, -stat[e % 4]);
         }
         if constexpr (n == gradient + 1) dp[e] *= s[e];
@@ -485,6 +539,22 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
     const int r0 = row_of(index);
     const Rows next = rows_from(index + 1);
     request_stats(nstats, next);
+    if constexpr (kUnits) {
+      // a step past the last one has old statistics, and adds nothing
+      const float top = stats[2 * kR + lane] * unit;
+      const uint64_t large = __ballot(top > kUnitMost), fits = __ballot(top >= kUnitLeast);
+      if (large || !fits) {
+        float most = top < INFINITY ? top : 0.f;
+        for (int x = 1; x < 64; x *= 2) most = fmaxf(most, __shfl_xor(most, x));
+        if (ill_fit(most, unit)) {
+          const float by = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(refit(most, unit))));
+          unit *= by;
+          scale *= by;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) dk[i] *= by;
+        }
+      }
+    }
     constexpr int kParts = kPair ? 1 : kR / 32, kEach = (RTile::kPieces + kParts - 1) / kParts;
     for_each<kParts>([&](auto half) {
       const int i = kPair ? role * 32 : half * 32, r = r0 + i;
@@ -517,6 +587,11 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
     step(i + 1, q1, g1, stats1, q0, g0, stats0);
   }
   if (!live) return;
+  const float back = 1.f / unit;
+  if constexpr (kUnits) {
+#pragma unroll
+    for (int i = 0; i < DB; ++i) dk[i] *= back;
+  }
   const bool sunk = j / kKeys < a.far_tiles;
   if (far || a.pieces > 1 || sunk) {
     float* p = far ? far_at(a, piece, kt, j, hk, D)

@@ -728,7 +728,7 @@ int gdn_kv_append(const gdn_kv_append_problem* p, const gdn_kv_cache* cache, con
                   const void* q, const void* k, const void* v, void* q_out, void* stream);
 
 /* Workspace bytes of the calls (0 on a bad problem, and for problems that need
- * none; workspace may then be NULL): from the extents, windows and, where the
+ * none; workspace may then be NULL): from the extents, types, windows and, where the
  * cache is read, its page size and columns only. Workspaces are 16-byte aligned
  * device memory, used only during the call, and need not be zeroed. */
 size_t gdn_attn_fwd_workspace_size(const gdn_attn_problem* p);
@@ -760,8 +760,8 @@ int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* cache, const vo
  *   dO          [T, HQ, D] cotangent of o (dense)
  *   dq          [T, HQ, D], dk, dv [T, HK, D] (dense)
  * The query heads of a key head are summed into dk and dv in fp32 in a fixed
- * order; no atomics. With fp16 the gradients of the scores are fp16 where they
- * are multiplied, so a cotangent as large as its range can pass it. Errors: as
+ * order; no atomics. With fp16 the gradients of the scores are multiplied in units
+ * of their own size, so that a cotangent may be anywhere in fp16's range. Errors: as
  * gdn_attn_fwd, GDN_ERR_NULL for o, lse, dO, dq, dk, dv. */
 int gdn_attn_bwd(const gdn_attn_problem* p, const void* q, const void* k, const void* v,
                  const void* o, const float* lse, const void* dO, void* dq, void* dk, void* dv,

@@ -1,0 +1,98 @@
+"""The softmax attention in fp16 where its numbers leave the middle of that type's range: small, large and unlike cotangents.
+Against fp64 on the GPU.
+
+u = 2^-11 is half a step of fp16 and 2^-25 half of its least one. A tensor is held by 2-norms, as in test_long of the attention: two
+roundings of any sign, a weight's or score gradient's and the output's own, are below 2 u of its norm, dq and dk have delta's too: 3 u.
+An output below fp16's normal numbers is off by at most 2^-25 besides, each element of it. The score gradients have
+full precision over fp16's normal numbers, down to 2^-21 of the largest of a step, and lie by at most 2^-32 of that off below:
+n keys or rows of equal size together n 2^-32, which is below u / 2^9 for the lengths here."""
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_attention import plain
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from chunked_gated_delta_04_amd import gdn
+
+U, LEAST = 2.0 ** -11, 2.0 ** -25
+FACTOR = dict(o=2, dv=2, dq=3, dk=3)
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+def make(lens, HQ, HK, D, seed):
+    gen = torch.Generator().manual_seed(seed)
+    T, cu = sum(lens), np.concatenate([[0], np.cumsum(lens)]).tolist()
+    r = lambda h: torch.randn(T, h, D, generator=gen).cuda()  # noqa: E731
+    return r(HQ), r(HK), r(HK), r(HQ), cu, torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+
+def gradients(q, k, v, dO, cu, dcu, window=0, sinks=0):
+    """(the kernels' outputs, the reference's)"""
+    o, lse = gdn.attn_fwd(q, k, v, dcu, window=window, sinks=sinks, want_lse=True)
+    got = dict(gdn.attn_bwd(q, k, v, dcu, o, lse, dO, window=window, sinks=sinks), o=o)
+    return got, plain(q, k, v, cu, window, sinks, q.shape[2] ** -0.5, dO)
+
+
+def near(name, got, want, factor=None):
+    off = float((got.double() - want).norm())
+    bound = (factor or FACTOR[name]) * U * float(want.norm()) + LEAST * want.numel() ** 0.5
+    say(name, off / float(want.norm()), bound / float(want.norm()))
+    assert off <= bound, name  # also where it is NaN
+
+
+CASES = [  # lens, HQ, HK, D, window, sinks
+    ([2100, 300], 4, 2, 64, 0, 0), ([2100], 4, 1, 128, 0, 0), ([1500, 7], 2, 2, 256, 0, 0), ([2500], 4, 2, 128, 300, 5),
+    ([3000, 2], 2, 1, 64, 200, 70), ([2000], 2, 1, 256, 500, 3), ([40] * 70, 3, 1, 64, 0, 0),
+]
+
+
+@pytest.mark.parametrize("size", [1.0, 0.1, 0.01, 0.001])
+@pytest.mark.parametrize("lens, HQ, HK, D, window, sinks", CASES)
+def test_small_cotangents(lens, HQ, HK, D, window, sinks, size):
+    say(lens[:4], HQ, HK, D, window, sinks, size)
+    q, k, v, dO, cu, dcu = make(lens, HQ, HK, D, D)
+    q, k, v, dO = q.half(), k.half(), v.half(), (dO * size).half()
+    got, want = gradients(q, k, v, dO, cu, dcu, window, sinks)
+    for n in ("dq", "dk", "dv"):
+        near(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("D, window, sinks", [(64, 0, 0), (128, 0, 0), (256, 0, 0), (128, 50, 3)])
+def test_large_cotangents(D, window, sinks):
+    """Score gradients past fp16's largest number whose products with q and k are not."""
+    say(D, window, sinks)
+    q, k, v, dO, cu, dcu = make([200, 31], 4, 2, D, D)
+    q, k, v, dO = (q * 2.0 ** -9).half(), (k * 2.0 ** -9).half(), (v * 64).half(), (dO * 2.0 ** 13).half()
+    got, want = gradients(q, k, v, dO, cu, dcu, window, sinks)
+    # the weight of a row's own key is near 1 / (row + 1): the scores are near 0
+    own = v.double().repeat_interleave(2, 1) - want["o"]
+    ds = (own * dO.double()).sum(-1)[:30] * D ** -0.5 / torch.arange(1, 31, device="cuda")[:, None]
+    assert float(ds.abs().max()) > 70000
+    for n in ("dq", "dk"):
+        near(n, got[n], want[n])
+
+
+SIZES = [10, 1e-4, 1, 1e-3, 100, 1e-2, 1e-4, 10, 1e-3]
+
+
+@pytest.mark.parametrize("HQ, HK, D, window, sinks", [(2, 1, 64, 0, 0), (2, 2, 128, 0, 0), (2, 1, 256, 0, 0), (2, 1, 64, 200, 4), (4, 1, 128, 150, 3),
+                                                      (2, 1, 256, 100, 0)])
+def test_unlike_cotangents(HQ, HK, D, window, sinks):
+    """A cotangent whose size changes by up to 2^20 from one 128 tokens to the next: each 128 tokens' gradients have their own
+    precision, small ones beside large ones too."""
+    say(HQ, HK, D, window, sinks)
+    q, k, v, dO, cu, dcu = make([128 * len(SIZES)], HQ, HK, D, D + HQ)
+    size = torch.tensor(SIZES, device="cuda").repeat_interleave(128)[:, None, None]
+    q, k, v, dO = q.half(), k.half(), v.half(), (dO * size).half()
+    got, want = gradients(q, k, v, dO, cu, dcu, window, sinks)
+    for n in ("dq", "dk"):
+        for i in range(0, len(q), 128):
+            near(n, got[n][i:i + 128], want[n][i:i + 128])
