@@ -18,7 +18,7 @@
 // and with the cotangent's size: it is multiplied in units of a power of two that
 // follows its largest value (see refit), dq and dk are taken back at the end. 8192 keys of 128
 // columns, a cotangent of size 0.001: dq is 0.0005 of its norm off, of which 0.0004 is its own rounding;
-// in one unit for all it was 0.024. The units cost the backward of ten ragged sequences of 64 columns 4 of 62 us.
+// in one unit for all it was 0.024. So are the weights, in one unit. The units cost the backward of ten ragged sequences of 64 columns 4 of 62 us.
 #include <algorithm>
 
 #include "attn_tile.h"
@@ -46,6 +46,8 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 // 2^7 and 2^15: then none is past fp16's largest, and what is lost of one is at most 2^-32 of the largest. Else
 // the largest comes to 2^10 .. 2^11, and stays for some growth. unit: at most 2^40, so that sums in it are far
 // from fp32's end; zeros, infinities and NaN change nothing.
+// and for weights, which are at most 1: in units of 2^-14 all down to 2^-28 have full precision
+constexpr int kWeightUnit = 14;
 constexpr float kUnitLeast = 128.f, kUnitMost = 32768.f, kUnitEnd = 1099511627776.f;
 __device__ __forceinline__ bool ill_fit(float top, float unit) {
   return (top > kUnitMost && top < INFINITY) || (top < kUnitLeast && top > 0.f && unit < kUnitEnd);
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
   delta = sum_halves(delta);
   scaled = scale * delta;
   if (live && hi == 0) {
-    a.stats[out] = lse;
+    a.stats[out] = kUnits ? lse - kWeightUnit : lse;  // the other kernel's weights are in their unit
     a.stats[(int64_t)pk.T * pk.HQ + out] = scaled;
   }
   __syncthreads();
@@ -373,8 +375,10 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
   const uint16_t* qbase = static_cast<const uint16_t*>(a.q) + kt.bos * a.q_stride + hk * G * D;
   const uint16_t* gbase = static_cast<const uint16_t*>(a.dO) + (int64_t)kt.bos * pk.HQ * D + hk * G * D;
   const float c = pk.scale * kLog2e;
-  // kUnits: of dS, by the largest of a step's 64 rows, which all waves know; scale and dk are in it
-  float unit = 1.f, scale = pk.scale;
+  // kUnits: of dS, by the largest of a step's 64 rows, which all waves know; dk is in it, and scale and low, the factors
+  // of what a weight, in its own unit, is multiplied by
+  constexpr float kWeight = kUnits ? 1.f / (1 << kWeightUnit) : 1.f;
+  float unit = 1.f, low = kWeight, scale = pk.scale * kWeight;
   const int per_token = (65535 + G) / G;  // r / G = r per_token / 2^16 for r below 2^9
   // a step's rows from r0 on: offsets from its first token, its rows are of at most kR + 1 tokens
   struct Rows {
@@ -484,7 +488,7 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
         if constexpr (n == weight + 1) s[e] = exp2_fast(s[e]);
         if constexpr (n == gradient) {
           if constexpr (e % 4 == 0) stat = *reinterpret_cast<const f32x4*>(de + 2 * e + 4 * hi);
-          if constexpr (kUnits) stat[e % 4] *= unit;
+          if constexpr (kUnits) stat[e % 4] *= low;
           dp[e] = fmaf(dp[e], scale, -stat[e % 4]);
         }
         if constexpr (n == gradient + 1) dp[e] *= s[e];
@@ -549,6 +553,7 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
         if (ill_fit(most, unit)) {
           const float by = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(refit(most, unit))));
           unit *= by;
+          low *= by;
           scale *= by;
 #pragma unroll
           for (int i = 0; i < DB; ++i) dk[i] *= by;
@@ -590,7 +595,10 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
   const float back = 1.f / unit;
   if constexpr (kUnits) {
 #pragma unroll
-    for (int i = 0; i < DB; ++i) dk[i] *= back;
+    for (int i = 0; i < DB; ++i) {
+      dk[i] *= back;
+      dv[i] *= kWeight;
+    }
   }
   const bool sunk = j / kKeys < a.far_tiles;
   if (far || a.pieces > 1 || sunk) {

@@ -1,9 +1,9 @@
-"""The softmax attention in fp16 where its numbers leave the middle of that type's range: small, large and unlike cotangents.
-Against fp64 on the GPU.
+"""The softmax attention in fp16 where its numbers leave the middle of that type's range: small, large and unlike cotangents, and
+weights far below a row's largest one. Against fp64 on the GPU.
 
 u = 2^-11 is half a step of fp16 and 2^-25 half of its least one. A tensor is held by 2-norms, as in test_long of the attention: two
 roundings of any sign, a weight's or score gradient's and the output's own, are below 2 u of its norm, dq and dk have delta's too: 3 u.
-An output below fp16's normal numbers is off by at most 2^-25 besides, each element of it. The score gradients have
+An output below fp16's normal numbers is off by at most 2^-25 besides, each element of it. The score gradients and the weights have
 full precision over fp16's normal numbers, down to 2^-21 of the largest of a step, and lie by at most 2^-32 of that off below:
 n keys or rows of equal size together n 2^-32, which is below u / 2^9 for the lengths here."""
 import sys
@@ -96,3 +96,27 @@ def test_unlike_cotangents(HQ, HK, D, window, sinks):
     for n in ("dq", "dk"):
         for i in range(0, len(q), 128):
             near(n, got[n][i:i + 128], want[n][i:i + 128])
+
+
+def with_sink(lens, HQ, HK, D, seed, gap=15.0):
+    """The first key of each sequence takes nearly all weight, e^gap of another's, and has no value: the others' weights, some
+    2^-22, are the outputs."""
+    q, k, v, dO, cu, dcu = make(lens, HQ, HK, D, seed)
+    q, k = q * 0.3, k * 0.3
+    q[..., 0], k[..., 0] = 8, 0
+    k[cu[:-1]] = 0
+    k[cu[:-1], :, 0] = gap / 8 * D ** 0.5
+    v = v * 16
+    v[cu[:-1]] = 0
+    return q.half(), k.half(), v.half(), (dO * 64).half(), cu, dcu
+
+
+@pytest.mark.parametrize("lens, HQ, HK, D, window, sinks", [([1500, 200], 4, 2, 64, 0, 0), ([1500], 2, 1, 128, 0, 0), ([1200], 2, 2, 256, 0, 0),
+                                                            ([1500], 4, 1, 128, 300, 1), ([2000, 900], 2, 1, 64, 700, 5)])
+def test_small_weights_in_dv(lens, HQ, HK, D, window, sinks):
+    say(lens, HQ, HK, D, window, sinks)
+    q, k, v, dO, cu, dcu = with_sink(lens, HQ, HK, D, D)
+    got, want = gradients(q, k, v, dO, cu, dcu, window, sinks)
+    others = torch.ones(len(v), dtype=torch.bool)
+    others[cu[:-1]] = False
+    near("dv", got["dv"][others], want["dv"][others])
