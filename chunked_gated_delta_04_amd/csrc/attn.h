@@ -83,6 +83,9 @@ constexpr int kAttnGroup = 128; // most query heads to a key head
 // whether the backward's score gradients are multiplied in units of their own: where the type's range is short
 template <typename T>
 constexpr bool kHasUnits = std::is_same<T, Fp16>::value;
+// log2 of a row's largest weight where weights are rounded: above 1 in fp16, so that those far below it are not lost
+template <typename T>
+constexpr float weight_lift(int fp16) { return std::is_same<T, Fp16>::value ? (float)fp16 : 0.f; }
 constexpr int grad_stats(Elem type) { return type == Elem::kFp16 ? 3 : 2; }
 
 hipError_t launch_attn_fwd(Elem type, int D, bool paged, const AttnArgs& a, hipStream_t s);

@@ -15,7 +15,9 @@
 // and the transposing reads of V take the same ones.
 //
 // Scores, maxima, sums and O are fp32; the weights are rounded once to the
-// inputs' type for the second product, while their sum takes them unrounded.
+// inputs' type for the second product, while their sum takes them unrounded. In
+// fp16 a row's largest weight is 2^7 to 2^15 for that, so that those down to 2^-21 of it keep full precision and
+// those down to 2^-31 some.
 //
 // Bound by the matrix unit and by what the vector unit adds to it: the slots of
 // a step interleave the scores of the next tile, the weights of this one and the
@@ -42,6 +44,7 @@ template <typename T, int D, int kKeys>
 __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_kernel(AttnArgs a) {
   constexpr int kT = kFwdKeys, N = D / 16, DB = D / 32, kThreads = 2 * attn_rows(D);
   constexpr bool kPaged = kKeys != kTokens;
+  constexpr float kLift = weight_lift<T>(7);  // and 8 for a maximum that grows
   typedef Tile<D, kT, kThreads> KTile;
   __shared__ __attribute__((aligned(16))) typename KTile::Lds k0, k1, v0, v1;
   const AttnPack& pk = a.pack;
@@ -186,9 +189,9 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_fwd_k
       if constexpr (n == kTop - 1) {
         const float2 tops = both_halves(top);
         top = fmaxf(tops.x, tops.y) * c;
-        // The maximum that weights are relative to follows only where the row's has grown by a
-        // factor of 2^8: weights up to that are as exact.
-        const float now = top > m + 8.f ? top : m;
+        // What weights are relative to follows the row's maximum only where that has grown by a factor of 2^8: weights
+        // up to that are as exact. The maximum's own weight is 2^kLift then.
+        const float now = top > m + (8.f + kLift) ? top - kLift : m;
         base = now == kMinusInf ? 0.f : now;  // a row that has seen nothing yet
         f = exp2_fast(m - base);
         m = now;

@@ -10,7 +10,7 @@
 // TB/s; one row over 131072 tokens, 16 + 2 heads of 256: 54 us, 5.0 TB/s, and the join 6.
 //
 // As in the forward, scores are S^T = K Q^T, so that the weights are the second
-// product's operand where they stand.
+// product's operand where they stand, in fp16 relative to a largest one of 2^14.
 #include "attn_tile.h"
 
 namespace gdn {
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_step_kernel(AttnAr
 #pragma unroll
     for (int r = 0; r < 4; ++r) top = fmaxf(top, fmaxf(s[0][r], s[1][r]));
     top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32)) * c;
+    top = fmaxf(top, __shfl_xor(top, 32)) * c - weight_lift<T>(14);
     const float now = fmaxf(m, top), base = now == kMinusInf ? 0.f : now;
     if (__any(now > m)) {
       const float f = exp2_fast(m - base);

@@ -12,6 +12,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import attention as A
+from tests.attention_bounds import score_error
+from tests.gpu_helpers import f64
 from tests.test_gpu_attention import plain
 
 pytestmark = pytest.mark.gpu
@@ -120,3 +123,64 @@ def test_small_weights_in_dv(lens, HQ, HK, D, window, sinks):
     others = torch.ones(len(v), dtype=torch.bool)
     others[cu[:-1]] = False
     near("dv", got["dv"][others], want["dv"][others])
+
+
+@pytest.mark.parametrize("lens, HQ, HK, D, window, sinks", [([1500, 200], 4, 2, 64, 0, 0), ([1500], 2, 1, 128, 0, 0), ([1200], 2, 2, 256, 0, 0),
+                                                            ([1500], 4, 1, 128, 300, 1), ([3000], 1, 1, 64, 0, 0)])
+def test_small_weights(lens, HQ, HK, D, window, sinks):
+    """o element by element: a weight and its product with v are off by u + e (e: its score's and the exponentials', as in
+    attention_bounds) and, below fp16's normal numbers, by 2^-25 where the row's largest weight is 2^7 at least; then o's own
+    rounding."""
+    say(lens, HQ, HK, D, window, sinks)
+    q, k, v, dO, cu, dcu = with_sink(lens, HQ, HK, D, D + 1)
+    got, want = gradients(q, k, v, dO, cu, dcu, window, sinks)
+    close(got["o"], want["o"], bounds(f64(q), f64(k), f64(v), cu, window, sinks, cu))
+    for n in ("o", "dq", "dk"):
+        near(n, got[n], want[n])
+
+
+def bounds(q, k, v, cu, window, sinks, kcu, past=None):
+    out = np.zeros(q.shape)
+    for n, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        first, last = kcu[n], kcu[n + 1]
+        seen = A.visible((0 if past is None else past[n]) + np.arange(b - a), np.arange(last - first), window, sinks)
+        for h in range(q.shape[1]):
+            g, D = h // (q.shape[1] // k.shape[1]), q.shape[2]
+            x, y, z = q[a:b, h], k[first:last, g], v[first:last, g]
+            o, _, w = A.head(x, y, z, seen, D ** -0.5)
+            e = 2 * score_error(x, y, seen, D ** -0.5) + 2.0 ** -18
+            out[a:b, h] = (U + e) * (w @ np.abs(z)) + 2.0 ** -32 * (seen @ np.abs(z)) + U * np.abs(o) + LEAST
+    return out
+
+
+def close(got, want, bound):
+    got, want = f64(got), f64(want)
+    assert np.isfinite(got).all() and (np.abs(got - want) <= bound).all(), float((np.abs(got - want) / bound).max())
+
+
+@pytest.mark.parametrize("totals, HQ, HK, D, window, sinks", [([1500, 30, 700], 4, 2, 64, 0, 0), ([6000], 2, 1, 128, 0, 0), ([900, 901], 16, 2, 256, 0, 0),
+                                                              ([1500, 2000], 4, 1, 128, 300, 1)])
+def test_small_weights_in_a_cache(totals, HQ, HK, D, window, sinks):
+    """One token's step and a prompt's last tokens over a cache."""
+    say(totals, HQ, HK, D, window, sinks)
+    q, k, v, _, cu, dcu = with_sink(totals, HQ, HK, D, D + 2)
+    size, N = 16, len(totals)
+    cols = [-(-t // size) for t in totals]
+    table = torch.zeros(N, max(cols), dtype=torch.int32)
+    for n, c in enumerate(cols):
+        table[n, :c] = torch.arange(c) + 1 + sum(cols[:n])
+    kc, vc = (torch.zeros(sum(cols) + 1, size, HK, D, dtype=torch.float16, device="cuda") for _ in range(2))
+    zero = torch.zeros(N, dtype=torch.int32, device="cuda")
+    gdn.kv_append(k, v, kc, vc, table.cuda(), zero, cu_seqlens=dcu)
+    exact = A.forward(f64(q), f64(k), f64(v), cu, window, sinks)[0]
+    for new in (1, 20):
+        rows = np.concatenate([np.arange(b - new, b) for b in cu[1:]])
+        past = [t - new for t in totals]
+        args = (q[torch.from_numpy(rows).cuda()], kc, vc, table.cuda())
+        p = torch.tensor(past, dtype=torch.int32, device="cuda")
+        few = (np.arange(N + 1) * new).tolist()
+        bound = bounds(f64(args[0]), f64(k), f64(v), few, window, sinks, cu, past)
+        if new == 1:
+            close(gdn.attn_step(*args, p, window=window, sinks=sinks)[0], torch.from_numpy(exact[rows]), bound)
+        close(gdn.attn_fwd_paged(*args, torch.tensor(few, dtype=torch.int32, device="cuda"), p, window=window, sinks=sinks)[0],
+              torch.from_numpy(exact[rows]), bound)
