@@ -41,7 +41,8 @@ int group(const gdn_attn_problem* p) { return p->HQ / p->HK; }
 int64_t row_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / (attn_rows(p->D) / group(p)) + p->N; }
 int64_t key_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / attn_keys(p->D) + p->N; }
 
-gdn_status check_attn(const gdn_attn_problem* p) {
+// packed: the sequences have boundaries (else one token each, and neither array of them is looked at)
+gdn_status check_attn(const gdn_attn_problem* p, bool packed = true) {
   if (!p) return GDN_ERR_NULL;
   if (p->N < 0 || p->T < 0 || p->HQ <= 0 || p->HK <= 0 || p->D <= 0 || p->window < 0 || p->sinks < 0)
     return GDN_ERR_SHAPE;
@@ -55,7 +56,7 @@ gdn_status check_attn(const gdn_attn_problem* p) {
   if (p->T > kMaxTokens || p->window > kMaxTokens || p->sinks > kMaxTokens ||
       (int64_t)p->T * p->HQ >= (int64_t)1 << 31 || (row_tiles(p) + key_tiles(p)) * p->HK > kMaxBlocks)
     return GDN_ERR_SHAPE;
-  return check_bounds(p->N, p->T, p->cu_seqlens_host);
+  return packed ? check_bounds(p->N, p->T, p->cu_seqlens_host) : GDN_OK;
 }
 
 gdn_status check_cache(const gdn_kv_cache* c, int N, int HK, int D) {
@@ -247,12 +248,12 @@ GDN_API int gdn_attn_fwd_paged(const gdn_attn_problem* p, const gdn_kv_cache* c,
 }
 
 GDN_API size_t gdn_attn_step_workspace_size(const gdn_attn_problem* p, const gdn_kv_cache* c) {
-  return check_attn(p) == GDN_OK && p->T == p->N && check_read_cache(c, p) == GDN_OK ? part_bytes(p, step_splits(p, c)) : 0;
+  return check_attn(p, false) == GDN_OK && p->T == p->N && check_read_cache(c, p) == GDN_OK ? part_bytes(p, step_splits(p, c)) : 0;
 }
 
 GDN_API int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* c, const void* q, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream) {
-  gdn_status st = check_attn(p);
+  gdn_status st = check_attn(p, false);
   if (st != GDN_OK) return st;
   if (p->T != p->N || step_items(p) > kMaxBlocks) return GDN_ERR_SHAPE;
   st = check_read_cache(c, p);

@@ -751,8 +751,9 @@ int gdn_attn_fwd(const gdn_attn_problem* p, const void* q, const void* k, const 
 int gdn_attn_fwd_paged(const gdn_attn_problem* p, const gdn_kv_cache* cache, const void* q, void* o,
                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
-/* One token a sequence: T = N rows of q, cu_seqlens not read, the token of row n
- * at position offsets[n] and in the cache already. Errors: as gdn_attn_fwd_paged. */
+/* One token a sequence: T = N rows of q, cu_seqlens and cu_seqlens_host not read,
+ * the token of row n at position offsets[n] and in the cache already. Errors: as
+ * gdn_attn_fwd_paged. */
 int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* cache, const void* q, void* o,
                   float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
