@@ -41,8 +41,9 @@ int group(const gdn_attn_problem* p) { return p->HQ / p->HK; }
 int64_t row_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / (attn_rows(p->D) / group(p)) + p->N; }
 int64_t key_tiles(const gdn_attn_problem* p) { return (int64_t)p->T / attn_keys(p->D) + p->N; }
 
-// packed: the sequences have boundaries (else one token each, and neither array of them is looked at)
-gdn_status check_attn(const gdn_attn_problem* p, bool packed = true) {
+// What a call reads of a problem: boundaries (or one token a sequence), and rows of keys and values (or a cache).
+enum Reads { kPack, kPagedPack, kPagedTokens };
+gdn_status check_attn(const gdn_attn_problem* p, Reads reads) {
   if (!p) return GDN_ERR_NULL;
   if (p->N < 0 || p->T < 0 || p->HQ <= 0 || p->HK <= 0 || p->D <= 0 || p->window < 0 || p->sinks < 0)
     return GDN_ERR_SHAPE;
@@ -51,12 +52,12 @@ gdn_status check_attn(const gdn_attn_problem* p, bool packed = true) {
     return GDN_ERR_UNSUPPORTED;
   if (p->N == 0 && p->T != 0) return GDN_ERR_SHAPE;
   const int64_t dq = (int64_t)p->HQ * p->D, dk = (int64_t)p->HK * p->D;
-  if (dq >= kMaxStride || bad_stride(p->q_stride, dq) || bad_stride(p->k_stride, dk) || bad_stride(p->v_stride, dk))
-    return GDN_ERR_SHAPE;
+  if (dq >= kMaxStride || bad_stride(p->q_stride, dq)) return GDN_ERR_SHAPE;
+  if (reads == kPack && (bad_stride(p->k_stride, dk) || bad_stride(p->v_stride, dk))) return GDN_ERR_SHAPE;
   if (p->T > kMaxTokens || p->window > kMaxTokens || p->sinks > kMaxTokens ||
       (int64_t)p->T * p->HQ >= (int64_t)1 << 31 || (row_tiles(p) + key_tiles(p)) * p->HK > kMaxBlocks)
     return GDN_ERR_SHAPE;
-  return packed ? check_bounds(p->N, p->T, p->cu_seqlens_host) : GDN_OK;
+  return reads == kPagedTokens ? GDN_OK : check_bounds(p->N, p->T, p->cu_seqlens_host);
 }
 
 gdn_status check_cache(const gdn_kv_cache* c, int N, int HK, int D) {
@@ -139,8 +140,6 @@ AttnArgs args_of(const gdn_attn_problem* p, const void* q, void* o, float* lse, 
   a.pack = pack_of(p);
   a.q = q;
   a.q_stride = p->q_stride ? p->q_stride : (int64_t)p->HQ * p->D;
-  a.k_stride = p->k_stride ? p->k_stride : (int64_t)p->HK * p->D;
-  a.v_stride = p->v_stride ? p->v_stride : (int64_t)p->HK * p->D;
   a.o = o;
   a.lse = lse;
   a.splits = splits;
@@ -208,12 +207,12 @@ GradBytes grad_bytes(const gdn_attn_problem* p) {
 }  // namespace
 
 GDN_API size_t gdn_attn_fwd_workspace_size(const gdn_attn_problem* p) {
-  return check_attn(p) == GDN_OK ? part_bytes(p, fwd_splits(p, nullptr)) : 0;
+  return check_attn(p, kPack) == GDN_OK ? part_bytes(p, fwd_splits(p, nullptr)) : 0;
 }
 
 GDN_API int gdn_attn_fwd(const gdn_attn_problem* p, const void* q, const void* k, const void* v, void* o, float* lse,
                          void* workspace, size_t workspace_bytes, void* stream) {
-  gdn_status st = check_attn(p);
+  gdn_status st = check_attn(p, kPack);
   if (st != GDN_OK) return st;
   if (p->T == 0) return GDN_OK;
   if (!k || !v || !p->cu_seqlens) return GDN_ERR_NULL;
@@ -224,16 +223,18 @@ GDN_API int gdn_attn_fwd(const gdn_attn_problem* p, const void* q, const void* k
   AttnArgs a = args_of(p, q, o, lse, splits, workspace);
   a.k = k;
   a.v = v;
+  a.k_stride = p->k_stride ? p->k_stride : (int64_t)p->HK * p->D;
+  a.v_stride = p->v_stride ? p->v_stride : (int64_t)p->HK * p->D;
   return run_fwd(p, false, a, reinterpret_cast<hipStream_t>(stream));
 }
 
 GDN_API size_t gdn_attn_fwd_paged_workspace_size(const gdn_attn_problem* p, const gdn_kv_cache* c) {
-  return check_attn(p) == GDN_OK && check_read_cache(c, p) == GDN_OK ? part_bytes(p, fwd_splits(p, c)) : 0;
+  return check_attn(p, kPagedPack) == GDN_OK && check_read_cache(c, p) == GDN_OK ? part_bytes(p, fwd_splits(p, c)) : 0;
 }
 
 GDN_API int gdn_attn_fwd_paged(const gdn_attn_problem* p, const gdn_kv_cache* c, const void* q, void* o, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream) {
-  gdn_status st = check_attn(p);
+  gdn_status st = check_attn(p, kPagedPack);
   if (st != GDN_OK) return st;
   st = check_read_cache(c, p);
   if (st != GDN_OK) return st;
@@ -248,12 +249,12 @@ GDN_API int gdn_attn_fwd_paged(const gdn_attn_problem* p, const gdn_kv_cache* c,
 }
 
 GDN_API size_t gdn_attn_step_workspace_size(const gdn_attn_problem* p, const gdn_kv_cache* c) {
-  return check_attn(p, false) == GDN_OK && p->T == p->N && check_read_cache(c, p) == GDN_OK ? part_bytes(p, step_splits(p, c)) : 0;
+  return check_attn(p, kPagedTokens) == GDN_OK && p->T == p->N && check_read_cache(c, p) == GDN_OK ? part_bytes(p, step_splits(p, c)) : 0;
 }
 
 GDN_API int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* c, const void* q, void* o, float* lse,
                           void* workspace, size_t workspace_bytes, void* stream) {
-  gdn_status st = check_attn(p, false);
+  gdn_status st = check_attn(p, kPagedTokens);
   if (st != GDN_OK) return st;
   if (p->T != p->N || step_items(p) > kMaxBlocks) return GDN_ERR_SHAPE;
   st = check_read_cache(c, p);
@@ -273,13 +274,13 @@ GDN_API int gdn_attn_step(const gdn_attn_problem* p, const gdn_kv_cache* c, cons
 }
 
 GDN_API size_t gdn_attn_bwd_workspace_size(const gdn_attn_problem* p) {
-  return check_attn(p) == GDN_OK ? grad_bytes(p).all() : 0;
+  return check_attn(p, kPack) == GDN_OK ? grad_bytes(p).all() : 0;
 }
 
 GDN_API int gdn_attn_bwd(const gdn_attn_problem* p, const void* q, const void* k, const void* v, const void* o,
                          const float* lse, const void* dO, void* dq, void* dk, void* dv, void* workspace,
                          size_t workspace_bytes, void* stream) {
-  const gdn_status st = check_attn(p);
+  const gdn_status st = check_attn(p, kPack);
   if (st != GDN_OK) return st;
   if (p->T == 0) return GDN_OK;
   if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv || !p->cu_seqlens) return GDN_ERR_NULL;

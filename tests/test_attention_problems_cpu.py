@@ -17,3 +17,14 @@ def test_step_reads_no_boundaries(G):
         # the arguments behind them are looked at
         assert call(G, "step", host=host, ptr=dict(o=ODD)) == ALIGN
         assert call(G, "step", host=host, ptr=dict(q=None)) == NULL
+
+
+@pytest.mark.parametrize("name", ["paged", "step"])
+def test_a_cache_has_its_own_strides(G, name):
+    """k_stride and v_stride are of token rows: with a cache they are not read."""
+    size = getattr(G._lib, dict(paged="gdn_attn_fwd_paged", step="gdn_attn_step")[name] + "_workspace_size")
+    big = cache(G, columns=4096)
+    want = size(ctypes.byref(problem(G, T=2)), ctypes.byref(big))
+    for odd in (dict(k_stride=-1), dict(k_stride=5), dict(v_stride=1 << 40)):
+        assert want > 0 and size(ctypes.byref(problem(G, T=2, **odd)), ctypes.byref(big)) == want
+        assert call(G, name, ptr=dict(o=ODD), **odd) == ALIGN
