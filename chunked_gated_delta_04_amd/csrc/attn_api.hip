@@ -19,7 +19,8 @@ namespace {
     if ((expr) != hipSuccess) return GDN_ERR_HIP;  \
   } while (0)
 
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // workgroups of 256 threads in one launch
+// Tiles of rows and of keys of a call together: a launch counts its threads in 32 bits, and has 512 for each row tile.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
 constexpr int64_t kMaxStride = (int64_t)1 << 23;  // a tile's rows span less than 2^31 bytes
 constexpr int64_t kMaxPitch = (int64_t)1 << 40;   // of a cache
 constexpr int kMaxTokens = 1 << 30;

@@ -307,8 +307,9 @@ __device__ __forceinline__ RowTile far_tile(const AttnGradArgs& a, int i, int ke
   return t;
 }
 
+// Workgroups from number `launched` on, as many as the grid has.
 template <typename T, int D>
-__global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_kv_kernel(AttnGradArgs a) {
+__global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_kv_kernel(AttnGradArgs a, int launched) {
   // From 128 columns on two waves share the accumulators of 32 keys: each forms the scores of half of a step's rows, they
   // exchange the weights and the scores' gradients as operands through LDS, and each adds all rows up in half of the
   // columns. 256 columns would fill all registers otherwise; with 128 a SIMD then holds two waves instead of one (2 x 8192
@@ -324,7 +325,7 @@ __global__ __launch_bounds__(grad_threads(D), D == 256 ? 1 : 2) void attn_grad_k
   const AttnPack& pk = a.pack;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l32 = lane & 31, hi = lane >> 5;
   const int G = pk.G.by;
-  int b = blockIdx.x;
+  int b = launched + blockIdx.x;
   const int hk = b % pk.HK;
   b /= pk.HK;
   const int role = kPair ? wave & 1 : 0, keys0 = (kPair ? wave >> 1 : wave) * 32, col0 = role * (D / 2);
@@ -670,10 +671,13 @@ hipError_t bwd_of(const AttnGradArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((attn_grad_q_kernel<T, D>), dim3(a.slots * pk.HK), dim3(2 * attn_rows(D)), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int items = a.far_pieces * a.far_slots + a.pieces * a.key_slots;
-  hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(items * pk.HK), dim3(grad_threads(D)), 0, s, a);
-  e = hipGetLastError();
-  const int tiles = a.pieces > 1 ? a.key_slots : a.far_slots, most = 1 << 19;  // most: 2^23 workgroups
+  // a launch counts its threads in 32 bits
+  const int items = (a.far_pieces * a.far_slots + a.pieces * a.key_slots) * pk.HK, launch = 1 << 22;
+  for (int i = 0; i < items && e == hipSuccess; i += launch) {
+    hipLaunchKernelGGL((attn_grad_kv_kernel<T, D>), dim3(std::min(items - i, launch)), dim3(grad_threads(D)), 0, s, a, i);
+    e = hipGetLastError();
+  }
+  const int tiles = a.pieces > 1 ? a.key_slots : a.far_slots, most = 1 << 19;  // of at most 16 workgroups each
   for (int first = 0; first < tiles && e == hipSuccess; first += most) {
     const int n = std::min(tiles - first, most);
     hipLaunchKernelGGL((attn_grad_join_kernel<T, D>), dim3(n * (attn_keys(D) / 8)), block, 0, s, a, first);
