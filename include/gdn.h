@@ -712,9 +712,10 @@ typedef struct {
  *               below 2^31
  *   q, q_out    [T, HQ, D], q_out may be q with the same stride
  *   k, v        [T, HK, D]
- * Two tokens with one place in the cache leave either's row there. Rows of q_out
- * that no sequence holds are left as they were; a token without a place in the
- * cache still has its q turned. Fastest with rows of 16-byte aligned pieces.
+ * Two tokens with one place in the cache leave no defined row there: each element
+ * is one of the tokens' own, not all of them the same one's, in k and in v. Rows of
+ * q_out that no sequence holds are left as they were; a token without a place in
+ * the cache still has its q turned. Fastest with rows of 16-byte aligned pieces.
  * Errors: GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_UNSUPPORTED, GDN_ERR_SEQLENS,
  * GDN_ERR_ALIGN (a pointer not aligned to its elements), GDN_ERR_HIP. */
 typedef struct {

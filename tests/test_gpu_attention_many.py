@@ -1,4 +1,4 @@
-"""The softmax attention at the most sequences that a problem may have. Tolerances: relative 2-norms, as in test_long of the attention."""
+"""The softmax attention and its cache at the most sequences that a problem may have, and many tokens with one place. Tolerances: relative 2-norms, as in test_long of the attention."""
 import sys
 
 import pytest
@@ -32,3 +32,20 @@ def test_millions_of_empty_sequences():
         for name, x in dict(g, o=o).items():
             far = float((x[at].double() - ref[name]).norm() / ref[name].norm())
             assert far <= (3 if name in ("dq", "dk") else 2) * 2.0 ** -8, (n, name, far)
+
+
+@pytest.mark.parametrize("D, R", [(128, 0), (80, 74), (64, 64)])
+def test_tokens_with_one_place(D, R):
+    """Each element of the row is one of the tokens' (with R those that do not turn), and no other row changes."""
+    N, size = 300, 16
+    x = torch.arange(1, N + 1, device="cuda").bfloat16()[:, None, None].expand(N, 2, D).contiguous()
+    kc, vc = (torch.zeros(4, size, 2, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, past = (torch.full(s, n, dtype=torch.int32, device="cuda") for s, n in (((N, 2), 2), ((N,), 21)))
+    f = gdn.rotary_inv_freq(R, device="cuda")[0] if R else None
+    gdn.kv_append(x, -x, kc, vc, table, past, inv_freq=f)
+    row = (kc[2, 5, :, R:], -vc[2, 5])
+    assert all(bool(torch.isin(r, x[:, 0, 0]).all()) for r in row)
+    if R:
+        assert bool(kc[2, 5, :, :R].isfinite().all())
+    kc[2, 5], vc[2, 5] = 0, 0
+    assert not kc.any() and not vc.any()
