@@ -1140,12 +1140,17 @@ def _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev):
                       f"{k_cache.stride()} and {v_cache.stride()}")
 
 
+def _unlike(a, b, shape):
+    """Whether strides differ where there is more than one element."""
+    return a != b and any(x != y for x, y, n in zip(a, b, shape) if n > 1)
+
+
 def _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev):
     """The gdn_kv_cache of tensors [pages, page_size, HK, D] in any order of memory."""
     shape, strides, table = k_cache.shape, k_cache.stride(), page_table.stride()
     if (k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.device != dev
             or v_cache.device != dev or v_cache.shape != shape or len(shape) != 4 or shape[2] != HK
-            or shape[3] != D or v_cache.stride() != strides or (strides[3] != 1 and D > 1)
+            or shape[3] != D or _unlike(v_cache.stride(), strides, shape) or (strides[3] != 1 and D > 1)
             or page_table.dtype is not torch.int32 or page_table.device != dev or len(table) != 2):
         raise _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev)
     rows, columns = page_table.shape
@@ -1155,8 +1160,8 @@ def _cache(k_cache, v_cache, page_table, offsets, N, HK, D, dtype, dev):
     page, token, head = strides[:3]
     # an extent of 1 has no stride of its own
     return GdnKvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, columns,
-                      table[0] if N > 1 else 0, page if pages > 1 else max(page, D),
-                      token if size > 1 else max(token, D), head if HK > 1 else max(head, D),
+                      table[0] if N > 1 else 0, page if pages > 1 else D, token if size > 1 else D,
+                      head if HK > 1 else D,
                       page_table.data_ptr(), _dev(offsets, (N,), torch.int32, "offsets", dev))
 
 
