@@ -1140,6 +1140,12 @@ def _bad_cache(k_cache, v_cache, page_table, N, HK, D, dtype, dev):
                       f"{k_cache.stride()} and {v_cache.stride()}")
 
 
+def _cache_heads(k_cache):
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache must be [pages, page_size, HK, D], got {tuple(k_cache.shape)}")
+    return k_cache.shape[2]
+
+
 def _unlike(a, b, shape):
     """Whether strides differ where there is more than one element."""
     return a != b and any(x != y for x, y, n in zip(a, b, shape) if n > 1)
@@ -1295,7 +1301,7 @@ def attn_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens, offsets, window=
     T, HQ, D = q.shape
     qp, qs = _rows(q, q.dtype, "q", dev)
     N, cu, host = _bounds(cu_seqlens, cu_seqlens_host, dev)
-    HK = k_cache.shape[2]
+    HK = _cache_heads(k_cache)
     p = GdnAttnProblem(N, T, HQ, HK, D, _half(q, "q"), window, sinks, scale, cu, host, qs, 0, 0)
     cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, q.dtype, dev)
     return _on_stream(dev, stream, _attn_call("gdn_attn_fwd_paged", p, cache, q, want_lse, (qp,)), q,
@@ -1310,7 +1316,7 @@ def attn_step(q, k_cache, v_cache, page_table, offsets, window=0, sinks=0, scale
     dev = _on_device(q, "q")
     N, HQ, D = q.shape
     qp, qs = _rows(q, q.dtype, "q", dev)
-    HK = k_cache.shape[2]
+    HK = _cache_heads(k_cache)
     p = GdnAttnProblem(N, N, HQ, HK, D, _half(q, "q"), window, sinks, scale, None, None, qs, 0, 0)
     cache = _cache(k_cache, v_cache, page_table, offsets, N, HK, D, q.dtype, dev)
     return _on_stream(dev, stream, _attn_call("gdn_attn_step", p, cache, q, want_lse, (qp,)), q, k_cache,

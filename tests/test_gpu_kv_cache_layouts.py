@@ -35,3 +35,54 @@ def test_an_extent_of_one_has_no_stride(pages, size, HK):
     u, w = kc.clone(), vc.clone()
     gdn.kv_append(k[:1], k[:1], u, odd(w), table[:1], past[:1])
     assert torch.equal(u, x) and torch.equal(w, y) and not torch.equal(x, kc)
+
+
+def test_what_is_no_cache_or_token():
+    """A cache or tokens of another number of extents: the binding's own errors."""
+    q, k, kc, t, off = bf(1, 4, 64), bf(1, 2, 64), bf(5, 16, 2, 64), ints(1, 2)[None], ints(0)
+    for bad in (kc[0, 0], kc[0, 0, 0], kc[None], kc.flatten()):
+        for f in (lambda: gdn.attn_step(q, bad, bad, t, off), lambda: gdn.attn_fwd_paged(q, bad, bad, t, ints(0, 1), off),
+                  lambda: gdn.kv_append(k, k, bad, bad, t, off)):
+            with pytest.raises(ValueError, match="k_cache must be"):
+                f()
+
+
+def behind(T, cu, D, paged, window=0, sinks=0):
+    """outputs of a call whose last sequence ends before T, and of one without the rows behind"""
+    import ctypes
+    HQ, HK, size = 4, 2, 16
+    q, k, v = bf(T, HQ, D), bf(T, HK, D, seed=1), bf(T, HK, D, seed=2)
+    N, dcu = len(cu) - 1, ints(*cu)
+    o, lse = torch.full_like(q, 7.0), torch.full((T, HQ), 7.0, device="cuda")
+    p = gdn.GdnAttnProblem(N, T, HQ, HK, D, 0, window, sinks, 0.0, dcu.data_ptr(), None, 0, 0, 0)
+    args = [ctypes.byref(p)]
+    if paged:
+        cols = 300
+        table = (torch.arange(N * cols, dtype=torch.int32).view(N, cols) + 1).cuda()
+        kc, vc = bf(N * cols + 1, size, HK, D, seed=1), bf(N * cols + 1, size, HK, D, seed=2)
+        past = ints(*[700 + n for n in range(N)])
+        c = gdn._cache(kc, vc, table, past, N, HK, D, q.dtype, q.device)
+        args.append(ctypes.byref(c))
+        name, ptrs = "gdn_attn_fwd_paged", [q]
+        want = gdn.attn_fwd_paged(q[:cu[-1]], kc, vc, table, dcu, past, window=window, sinks=sinks, want_lse=True)
+    else:
+        name, ptrs = "gdn_attn_fwd", [q, k, v]
+        want = gdn.attn_fwd(q[:cu[-1]], k[:cu[-1]], v[:cu[-1]], dcu, window=window, sinks=sinks, want_lse=True)
+    n = getattr(gdn._lib, name + "_workspace_size")(*args)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda").fill_(255)
+    gdn._check(getattr(gdn._lib, name)(*args, *[x.data_ptr() for x in ptrs], o.data_ptr(), lse.data_ptr(), ws.data_ptr(), n,
+                                       torch.cuda.current_stream().cuda_stream), name)
+    return o, lse, want, n
+
+
+@pytest.mark.parametrize("D, window, sinks", [(64, 0, 0), (128, 900, 3), (256, 0, 0)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_rows_behind_the_last_sequence_stay_where_keys_are_split(D, paged, window, sinks):
+    """Against the call without those rows, whose parts of the keys may be others: a rounding of o and 2^-12 of lse."""
+    T, cu = 2500, [0, 900, 900, 2111]
+    o, lse, want, n = behind(T, cu, D, paged, window, sinks)
+    assert n > 0  # split
+    assert bool((o[cu[-1]:] == 7).all()) and bool((lse[cu[-1]:] == 7).all())
+    a, b = o[:cu[-1]].double(), want[0].double()
+    assert float((a - b).norm()) <= 2.0 ** -8 * 2 * float(b.norm())
+    assert float((lse[:cu[-1]] - want[1]).abs().max()) < 2.0 ** -12
