@@ -1,5 +1,5 @@
 // Gradients of the causal softmax attention over packed sequences. With the
-// forward's lse, P = e^(scale s - lse), delta = dO . o for each row, and
+// forward's lse, P = e^(scale s - lse), delta = dO . o = sum P (dO V^T) for each row, and
 //   dS = scale P (dO V^T - delta):   dq = dS K,   dk = dS^T q,   dv = P^T dO,
 // the rows of all query heads of a key head summed in dk and dv.
 //
@@ -29,6 +29,11 @@ namespace {
 
 constexpr int kGradKeys = 64;  // keys a step of dq's kernel
 constexpr int grad_threads(int D) { return D == 128 ? 512 : 256; }
+// Fewest keys of a row whose delta is formed from the rounded o. dO V^T - delta cancels most where few keys are seen, and o's
+// rounding then weighs more than dS's own: sequences of 1 and 2 tokens, 8 + 2 heads of 256, bf16, dq 0.0042 of its norm off, with delta
+// from the weights 0.0023; from n keys on the share is o's rounding over sqrt(n). It costs the tiles at a sequence's
+// start, and all those of such a window, one more pass over their keys.
+constexpr int kFewKeys = 64;
 constexpr int kGradRows = 64;  // rows a step of dk's and dv's kernel, one to a lane, in parts of 32
 
 template <typename T>
@@ -236,9 +241,35 @@ __global__ __launch_bounds__(2 * attn_rows(D), D == 256 ? 1 : 2) void attn_grad_
       vr.request(v, n, vrows, tid);
     });
   };
-  fill(0, k0, v0);
+  // delta from o as it was rounded, or where a row may see few keys from the weights, in a pass of its own
+  if (t0 < kFewKeys || (pk.window && (int64_t)pk.window + pk.sinks < kFewKeys)) {
+#pragma unroll 1
+    for (int i = 0; i < kt.count; ++i) {
+      fill(i, k0, v0);
+      __syncthreads();
+      const int j0 = kt.at(i) * kT;
+      for_each<2>([&](auto half) {
+        f32x16 s, dp;
 #pragma unroll
-  for (int s = 0; s < N; ++s) delta += dot8<T>(y[s], g[s]);
+        for (int d = 0; d < N; ++d) {
+          const int at = (fresh(ka) ^ (16 * d)) + 32 * half * D;
+          s = mfma32_of<T>(*reinterpret_cast<const uint4*>(k0 + at), q[d], d == 0 ? f32x16{} : s);
+          dp = mfma32_of<T>(*reinterpret_cast<const uint4*>(v0 + at), g[d], d == 0 ? f32x16{} : dp);
+        }
+        const int first = j0 + 4 * hi, most = t - first, least = from - first, sunk = pk.sinks - first;
+        for_each<16>([&](auto element) {
+          constexpr int e = element, j = 32 * half + 8 * (e / 4) + e % 4;
+          const float x = j <= most && (j > least || j < sunk) ? s[e] : kMinusInf;
+          delta = fmaf(exp2_fast(fmaf(x, c, -lse)), dp[e], delta);
+        });
+      });
+      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < N; ++s) delta += dot8<T>(y[s], g[s]);
+  }
+  fill(0, k0, v0);
   delta = sum_halves(delta);
   scaled = scale * delta;
   if (live && hi == 0) {
