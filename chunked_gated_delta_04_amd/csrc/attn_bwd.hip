@@ -10,15 +10,15 @@
 // each operand that follows from scores is used where it stands in the accumulator.
 //
 // Bound by the matrix unit and the waits around it. 2 x 8192 tokens, 16 + 2 heads
-// of 256 columns: dq 1.48 ms (1.11 PFLOP/s of its three products), dk and dv 2.6 ms
-// (0.85, of four); window 1024, 16 + 4 heads of 128: 245 us, 415 us, joining 13 us.
+// of 256 columns: dq 1.52 ms (1.09 PFLOP/s of its three products), dk and dv 2.6 to 2.7 ms
+// (0.83, of four); window 1024, 16 + 4 heads of 128: 250 us, 420 us, joining 13 us.
 //
 // P and dS are rounded once to the inputs' type, where they are multiplied; all
 // sums are fp32. fp16's range is short for dS, which falls with the number of keys
 // and with the cotangent's size: it is multiplied in units of a power of two that
 // follows its largest value (see refit), dq and dk are taken back at the end. 8192 keys of 128
 // columns, a cotangent of size 0.001: dq is 0.0005 of its norm off, of which 0.0004 is its own rounding;
-// in one unit for all it was 0.024. So are the weights, in one unit. The units cost the backward of ten ragged sequences of 64 columns 4 of 62 us.
+// in one unit for all it was 0.024. Weights are in one unit, 2^-14. It costs the backward in fp16 3 to 6 %.
 #include <algorithm>
 
 #include "attn_tile.h"

@@ -21,8 +21,8 @@
 //
 // Bound by the matrix unit and by what the vector unit adds to it: the slots of
 // a step interleave the scores of the next tile, the weights of this one and the
-// product of the one before. 2 x 8192 tokens, 16 + 2 heads of 256 columns: 1085 us,
-// 1.01 PFLOP/s (a library's product of 8192^3: 1.32). With tiles through registers, masks
+// product of the one before. 2 x 8192 tokens, 16 + 2 heads of 256 columns: 1072 to 1086 us,
+// 1.02 PFLOP/s (a library's product of 8192^3: 1.32). With tiles through registers, masks
 // by positions and the compiler's own order it was 2365 us.
 #include <algorithm>
 
@@ -35,7 +35,7 @@ namespace {
 constexpr int kFwdKeys = 64;  // keys a tile
 
 // where the keys are: token rows, pages whose rows come in groups of 8 (see request_group; 8 x 512 tokens, four after 1000 to
-// 2000, 152.7 us, by rows 165.4), other pages, and a window's, whose edge may leave part of a group unread
+// 2000: by rows 8 % more), other pages, and a window's, whose edge may leave part of a group unread
 enum { kTokens, kGroups, kPages };
 
 }  // namespace
@@ -402,7 +402,7 @@ template <typename T, int D>
 hipError_t join_of(const AttnArgs& a, hipStream_t s) {
   const int64_t units = (int64_t)a.pack.T * a.pack.HQ * (D / 64);
   const dim3 block(256);
-  // a lane's eight requests hold every part where the rows alone fill no chip (one row of 16 heads over 131072 tokens, 256
+  // a lane's eight requests hold every part where the rows alone fill no chip (one token of 16 + 2 heads over 131072, 128
   // parts: 61.9 us, with one share 76.4)
   if (a.splits > 16 && units < 4096)
     hipLaunchKernelGGL((attn_join_kernel<T, D, 16>), dim3((uint32_t)units), block, 0, s, a);

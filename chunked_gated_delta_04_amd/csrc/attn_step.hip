@@ -1,7 +1,7 @@
 // Softmax attention of one new token a sequence over its paged cache.
 //
-// HBM bound: every visible key and value is read once, for all query heads of
-// its key head (up to 16 rows of one matrix product). The keys of a sequence
+// HBM bound: every visible key and value is read once for 16 query heads of its
+// key head (the rows of one matrix product), and again for each further 16. The keys of a sequence
 // are split over workgroups, as many as fill the chip, and over the four waves
 // of each; a wave goes over its tiles of 32 keys by itself, with its own
 // maximum and sum and its own LDS, no barrier and its next tile's rows on
