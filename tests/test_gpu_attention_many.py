@@ -1,4 +1,5 @@
-"""The softmax attention and its cache at the most sequences that a problem may have, and many tokens with one place. Tolerances: relative 2-norms, as in test_long of the attention."""
+"""The softmax attention and its cache with very many sequences, many tokens with one place, and fp16 gradients replayed
+with other data. Tolerances: relative 2-norms, as in test_long of the attention."""
 import sys
 
 import pytest
@@ -49,3 +50,50 @@ def test_tokens_with_one_place(D, R):
         assert bool(kc[2, 5, :, :R].isfinite().all())
     kc[2, 5], vc[2, 5] = 0, 0
     assert not kc.any() and not vc.any()
+
+
+def test_appends_of_thousands_of_sequences():
+    """Places of tokens among many boundaries, empty sequences and idle ones between: each row by its own indices."""
+    gen = torch.Generator().manual_seed(3)
+    N, size, HK, D = 9001, 8, 1, 64
+    lens = torch.randint(0, 4, (N,), generator=gen) * (torch.rand(N, generator=gen) < 0.6)
+    lens[-1] = 0
+    past = torch.randint(-2, 20, (N,), generator=gen)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    T = int(cu[-1])
+    table = torch.randperm(3 * N, generator=gen).view(N, 3) + 1
+    k, v = (torch.randn(T, HK, D, generator=gen).bfloat16() for _ in range(2))
+    kc, vc = (torch.zeros(3 * N + 1, size, HK, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    gdn.kv_append(k.cuda(), v.cuda(), kc, vc, table.int().cuda(), past.int().cuda(), cu_seqlens=cu.int().cuda())
+    seq = torch.repeat_interleave(torch.arange(N), lens)
+    pos = past[seq] + torch.arange(T) - cu[seq]
+    put = (pos >= 0) & (pos < 3 * size)
+    at = table[seq[put], pos[put] // size], pos[put] % size
+    for got, x in ((kc, k), (vc, v)):
+        want = torch.zeros(got.shape, dtype=torch.bfloat16)
+        want[at] = x[put]
+        assert torch.equal(got.cpu(), want)
+
+
+@pytest.mark.parametrize("window, sinks", [(0, 0), (100, 3)])
+def test_fp16_gradients_captured_and_replayed(window, sinks):
+    """The units that score gradients are in follow the data of the replay, not of the capture."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    T, mask = 700, dict(window=window, sinks=sinks)
+    q, k, v, dO = (torch.randn(T, h, 64, generator=gen, device="cuda").half() for h in (4, 2, 2, 4))
+    cu = torch.tensor([0, 300, T], dtype=torch.int32, device="cuda")
+    o, lse = gdn.attn_fwd(q, k, v, cu, want_lse=True, **mask)
+    run = lambda: gdn.attn_bwd(q, k, v, cu, o, lse, dO, **mask)  # noqa: E731
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = run()
+    whole = dO.clone()
+    for size in (1, 2.0 ** -12, 2.0 ** 10, 1):
+        dO.copy_(whole * size)
+        g.replay()
+        _ = torch.randn(300, 300, device="cuda") @ torch.randn(300, 300, device="cuda")
+        torch.cuda.synchronize()
+        want = run()
+        assert all(torch.equal(got[n], want[n]) and bool(want[n].isfinite().all()) and bool(want[n].any()) for n in want), size

@@ -1,4 +1,4 @@
-"""Caches in the orders of memory that the binding takes, and what it refuses, and rows of outputs that no sequence holds."""
+"""Caches in the orders of memory that the binding takes, shared pages, what it refuses, and rows of outputs that no sequence holds."""
 import pytest
 import torch
 
@@ -86,3 +86,19 @@ def test_rows_behind_the_last_sequence_stay_where_keys_are_split(D, paged, windo
     a, b = o[:cu[-1]].double(), want[0].double()
     assert float((a - b).norm()) <= 2.0 ** -8 * 2 * float(b.norm())
     assert float((lse[:cu[-1]] - want[1]).abs().max()) < 2.0 ** -12
+
+
+def test_sequences_share_pages():
+    """A page in several rows of the table, and twice in one: what copies of it give."""
+    D, size, HK = 64, 16, 2
+    kc, vc, q = bf(12, size, HK, D), bf(12, size, HK, D, seed=1), bf(60, 6, D, seed=2)
+    shared = ints(5, 2, 9, 1, 5, 2, 7, 9, 5, 5, 5, 5).view(3, 4)
+    own = torch.arange(1, 13, device="cuda").int().view(3, 4)
+    k2, v2 = (torch.cat([c[:1], c[shared.flatten().long()]]) for c in (kc, vc))
+    for mask in (dict(), dict(window=20, sinks=3)):
+        past = ints(63, 40, 17)
+        a, b = (gdn.attn_step(q[:3], *c, past, want_lse=True, **mask) for c in ((kc, vc, shared), (k2, v2, own)))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        cu, past = ints(0, 20, 40, 60), ints(44, 20, 0)
+        a, b = (gdn.attn_fwd_paged(q, *c, cu, past, want_lse=True, **mask) for c in ((kc, vc, shared), (k2, v2, own)))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
